@@ -371,6 +371,214 @@ MSSM_API mssm_status mssm_selective_state_update(float *state, const void *x,
                                         mssm_step_dims dims, mssm_dtypes dtypes,
                                         void *stream);
 
+/* Sizes of a layer norm: `rows` independent rows of `dim` values. */
+typedef struct {
+    int64_t rows;    /* >= 0 */
+    int64_t dim;     /* >= 0 */
+} mssm_norm_dims;
+
+/*
+ * Layer norm in front of a layer.  For every row:
+ *
+ *   mean     = sum_d x[d] / dim
+ *   rstd     = 1 / sqrt(sum_d (x[d] - mean)^2 / dim + eps)
+ *   y[d]     = (x[d] - mean) * rstd * weight[d] + bias[d]
+ *
+ * The variance is summed from the differences to the mean, in float32.
+ *
+ * Arguments (device pointers unless stated):
+ *   x        (rows, dim), dtype `io`       required
+ *   weight   (dim) float32                 nullable -> 1
+ *   bias     (dim) float32                 nullable -> 0
+ *   eps      (host) >= 0 and finite
+ *   y        (rows, dim), dtype `io`       required (output)
+ *   mean, rstd  (rows) float32             nullable (outputs, read by the
+ *                                          backward)
+ * Errors: MSSM_ERR_INVALID_ARG for a null required pointer, a negative size,
+ * an unknown dtype, eps < 0 or not finite, or an output overlapping an input
+ * or another output; MSSM_ERR_UNSUPPORTED for param dtype != F32 or
+ * rows >= 2^31 or dim >= 2^31.  rows == 0 or dim == 0: nothing to do, MSSM_OK.
+ */
+MSSM_API mssm_status mssm_layer_norm_fwd(const void *x, const float *weight,
+                                const float *bias, float eps, void *y,
+                                float *mean, float *rstd, mssm_norm_dims dims,
+                                mssm_dtypes dtypes, void *stream);
+
+/*
+ * Backward of the layer norm.  With xhat = (x - mean) * rstd and
+ * e[d] = dy[d] * weight[d], per row:
+ *
+ *   dx[d]      = rstd * (e[d] - mean_d(e) - xhat[d] * mean_d(e * xhat))
+ *   dweight[d] = sum_rows dy[d] * xhat[d],   dbias[d] = sum_rows dy[d]
+ *
+ *   dy, x       (rows, dim), dtype `io`    required
+ *   mean, rstd  (rows) float32             required (of the forward)
+ *   weight      (dim) float32              nullable -> 1
+ *   dx          (rows, dim), dtype `io`    required (output)
+ *   dweight, dbias  (dim) float32          nullable (outputs)
+ * dweight and dbias are summed in an order that depends on the sizes alone
+ * (repeatable bit for bit), through stream-ordered scratch of at most
+ * 8 * 1024 * dim bytes.  rows == 0 zero-fills dweight and dbias.  Errors as
+ * for the forward.
+ */
+MSSM_API mssm_status mssm_layer_norm_bwd(const void *dy, const void *x,
+                                const float *mean, const float *rstd,
+                                const float *weight, void *dx, float *dweight,
+                                float *dbias, mssm_norm_dims dims,
+                                mssm_dtypes dtypes, void *stream);
+
+/* Sizes of a gated linear recurrence. */
+typedef struct {
+    int64_t batch;   /* >= 0 */
+    int64_t seqlen;  /* L >= 0 (ignored by the single-step update) */
+    int64_t dim;     /* channels >= 0 */
+} mssm_recurrence_dims;
+
+/*
+ * Gated linear recurrence: one decay per step and channel, both gates formed
+ * from inputs.  For every batch b and channel d, from h = h0:
+ *
+ *   log a_t   = -scale * softplus(lam[d]) * sigmoid(r[b,t,d])
+ *   h         = a_t * h + sqrt(1 - a_t^2) * sigmoid(i[b,t,d]) * x[b,t,d]
+ *   y[b,t,d]  = h;   h_last[b,d] = h after t = L-1
+ *
+ * 1 - a_t^2 is formed from a_t - 1 = expm1(log a_t), so that decays next to 1
+ * lose nothing.
+ *
+ * Arguments (device pointers unless stated):
+ *   x, r, i  (batch, L, dim), dtype `io`   required (r, i before the sigmoid)
+ *   lam      (dim) float32                 required
+ *   scale    (host) >= 0 and finite
+ *   h0       (batch, dim) float32          nullable -> 0; may be the very
+ *                                          buffer passed as h_last
+ *   y        (batch, L, dim), dtype `io`   required (output)
+ *   h_last   (batch, dim) float32          nullable (output)
+ * Long sequences are cut into segments whose carries pass between workgroups
+ * in a fixed association: results are repeatable bit for bit.  Scratch for
+ * the carries is stream-ordered.
+ * Errors as for mssm_selective_scan_fwd; also MSSM_ERR_INVALID_ARG for a scale
+ * that is negative or not finite, MSSM_ERR_UNSUPPORTED when one of the sizes
+ * reaches 2^31.  batch == 0 or dim == 0: nothing to do, MSSM_OK.  L == 0:
+ * h_last receives h0 (or zeros), y is empty.
+ */
+MSSM_API mssm_status mssm_gated_recurrence_fwd(const void *x, const void *r,
+                                const void *i, const float *lam, float scale,
+                                const float *h0, void *y, float *h_last,
+                                mssm_recurrence_dims dims, mssm_dtypes dtypes,
+                                void *stream);
+
+/*
+ * Backward of the gated linear recurrence, given its inputs, its output y
+ * (the states, in dtype `io`) and the gradients dy and dh_last.  With
+ * m = sqrt(1 - a^2) and g_t = dy_t + a_{t+1} g_{t+1} (dh_last added at the
+ * last step):
+ *
+ *   w    = g h_{t-1} a log(a) - g sigmoid(i) x a^2 (log(a) / m)
+ *   dx   = g m sigmoid(i)          di = g m sigmoid(i) x (1 - sigmoid(i))
+ *   dr   = w (1 - sigmoid(r))      dlam = sum w * sigmoid(lam) / softplus(lam)
+ *   dh0  = a_0 g_0
+ *
+ * log(a) / m tends to 0 with log(a) and is taken as 0 where m is 0.
+ *
+ *   y, dy       (batch, L, dim), dtype `io`   required
+ *   dh_last     (batch, dim) float32          nullable -> 0
+ *   dx, dr, di  (batch, L, dim), dtype `io`   required (outputs)
+ *   dlam        (dim) float32                 nullable (output)
+ *   dh0         (batch, dim) float32          nullable (output)
+ * dlam is summed in a fixed order (repeatable bit for bit).  Scratch (the
+ * carries and dlam's partial sums) is stream-ordered.  L == 0: dlam is zero,
+ * dh0 = dh_last.  Errors as for the forward; no output may overlap an input
+ * or another output.
+ */
+MSSM_API mssm_status mssm_gated_recurrence_bwd(const void *x, const void *r,
+                                const void *i, const float *lam, float scale,
+                                const float *h0, const void *y, const void *dy,
+                                const float *dh_last, void *dx, void *dr,
+                                void *di, float *dlam, float *dh0,
+                                mssm_recurrence_dims dims, mssm_dtypes dtypes,
+                                void *stream);
+
+/*
+ * One decode step of the gated linear recurrence on a cached state, in
+ * place: the forward at L = 1 with h0 = h_last = state.
+ *
+ *   state    (batch, dim) float32          required, read and overwritten
+ *   x, r, i  (batch, dim), dtype `io`      required
+ *   y        (batch, dim), dtype `io`      required (output)
+ * Errors as for the forward; state and y must not overlap any input or each
+ * other.
+ */
+MSSM_API mssm_status mssm_gated_recurrence_update(float *state, const void *x,
+                                const void *r, const void *i, const float *lam,
+                                float scale, void *y,
+                                mssm_recurrence_dims dims, mssm_dtypes dtypes,
+                                void *stream);
+
+/* Sizes of a cross entropy over a vocabulary projection. */
+typedef struct {
+    int64_t tokens;  /* T >= 0 */
+    int64_t dim;     /* width of the hidden states, >= 1 */
+    int64_t vocab;   /* V >= 1 */
+} mssm_loss_dims;
+
+/*
+ * Softmax cross entropy of a projection onto a vocabulary, the logits formed
+ * in pieces on chip and never stored.  For every token t:
+ *
+ *   l[v]    = sum_d hidden[t,d] * weight[v,d]
+ *   lse[t]  = log sum_v exp(l[v])
+ *   loss[t] = lse[t] - l[targets[t]]      0 where targets[t] == ignore_index
+ *
+ * A target outside [0, vocab) that is not ignore_index reads nothing out of
+ * range: its loss is NaN.
+ *
+ * Arguments (device pointers unless stated):
+ *   hidden   (tokens, dim), dtype `io`     required
+ *   weight   (vocab, dim), dtype `io`      required
+ *   targets  (tokens) int64                required
+ *   loss     (tokens) float32              required (output)
+ *   lse      (tokens) float32              nullable (output, read by the
+ *                                          backward)
+ * Logits are float32 sums of exact products (bf16) or float32 products.
+ * Errors: as for mssm_layer_norm_fwd; also MSSM_ERR_INVALID_ARG for dim < 1 or
+ * vocab < 1, MSSM_ERR_UNSUPPORTED for tokens or vocab >= 2^30 or dim >= 2^24.
+ * tokens == 0: nothing to do, MSSM_OK.  Scratch is stream-ordered: the pieces'
+ * maxima and sums and, where dim or an address is not 16-byte aligned,
+ * aligned copies of hidden and weight.
+ */
+MSSM_API mssm_status mssm_linear_cross_entropy_fwd(const void *hidden,
+                                const void *weight, const int64_t *targets,
+                                int64_t ignore_index, float *loss, float *lse,
+                                mssm_loss_dims dims, mssm_dtypes dtypes,
+                                void *stream);
+
+/*
+ * Backward of the projected cross entropy.  With
+ * p[t,v] = (exp(l[t,v] - lse[t]) - [v == targets[t]]) * dloss[t]
+ * (0 for ignored tokens, whatever their hidden state and dloss hold):
+ *
+ *   dhidden[t,:] = sum_v p[t,v] * weight[v,:]
+ *   dweight[v,:] = sum_t p[t,v] * hidden[t,:]
+ *
+ *   lse      (tokens) float32              required (of the forward)
+ *   dloss    (tokens) float32              required
+ *   dhidden  (tokens, dim), dtype `io`     required (output)
+ *   dweight  (vocab, dim), dtype `io`      required (output)
+ * The logits are formed again, a piece of the vocabulary at a time; p is held
+ * in dtype `io` for that piece only.  Sums are float32 in a fixed order
+ * (repeatable bit for bit).  A target outside [0, vocab) that is not
+ * ignore_index makes that token's dhidden and its terms of dweight NaN.
+ * Scratch is stream-ordered; its size does not grow with the vocabulary
+ * except for one copy of weight.  tokens == 0 zero-fills dweight.  Errors as
+ * for the forward.
+ */
+MSSM_API mssm_status mssm_linear_cross_entropy_bwd(const void *hidden,
+                                const void *weight, const int64_t *targets,
+                                int64_t ignore_index, const float *lse,
+                                const float *dloss, void *dhidden,
+                                void *dweight, mssm_loss_dims dims,
+                                mssm_dtypes dtypes, void *stream);
+
 /* Force a kernel variant for subsequent calls made by THIS thread
  * (MSSM_VARIANT_AUTO restores the shape-based choice).  A variant that does
  * not apply to the entry point or shape makes that call return

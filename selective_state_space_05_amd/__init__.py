@@ -10,6 +10,13 @@ call raises -- there is no CPU fallback.
 """
 from .api import (  # noqa: F401
     MssmError,
+    gated_recurrence_bwd,
+    gated_recurrence_fwd,
+    gated_recurrence_update,
+    layer_norm_bwd,
+    layer_norm_fwd,
+    linear_cross_entropy_bwd,
+    linear_cross_entropy_fwd,
     selective_scan_bwd,
     selective_scan_conv_fwd,
     selective_scan_fwd,
@@ -19,6 +26,8 @@ from .api import (  # noqa: F401
     version,
 )
 
-__all__ = ["MssmError", "selective_scan_bwd", "selective_scan_conv_fwd", "selective_scan_fwd",
-           "selective_scan_fwd_noalloc", "selective_state_update",
+__all__ = ["MssmError", "gated_recurrence_bwd", "gated_recurrence_fwd", "gated_recurrence_update",
+           "layer_norm_bwd", "layer_norm_fwd", "linear_cross_entropy_bwd",
+           "linear_cross_entropy_fwd", "selective_scan_bwd", "selective_scan_conv_fwd",
+           "selective_scan_fwd", "selective_scan_fwd_noalloc", "selective_state_update",
            "ssd_scalar_fwd", "version"]

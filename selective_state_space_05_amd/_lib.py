@@ -56,6 +56,13 @@ EXPORTED = (
     "mssm_source_hash",
     "mssm_device_status",
     "mssm_selective_scan_fwd_h0_noalloc",
+    "mssm_layer_norm_fwd",
+    "mssm_layer_norm_bwd",
+    "mssm_gated_recurrence_fwd",
+    "mssm_gated_recurrence_bwd",
+    "mssm_gated_recurrence_update",
+    "mssm_linear_cross_entropy_fwd",
+    "mssm_linear_cross_entropy_bwd",
 )
 # Every symbol include/mssm_probes.h declares (measurement probes).
 EXPORTED_PROBES = (
@@ -82,6 +89,20 @@ class SSDDims(ctypes.Structure):
 class StepDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("dstate", ctypes.c_int64)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64)]
+
+
+class RecurrenceDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("dim", ctypes.c_int64)]
+
+
+class LossDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("vocab", ctypes.c_int64)]
 
 
 class DTypes(ctypes.Structure):
@@ -123,6 +144,25 @@ def _declare(L):
     L.mssm_selective_state_update.argtypes = [fp, vp, vp, fp, fp, vp, vp, fp, vp, vp,
                                               StepDims, DTypes, vp]
     L.mssm_selective_state_update.restype = ctypes.c_int
+    f32, i64 = ctypes.c_float, ctypes.c_int64
+    L.mssm_layer_norm_fwd.argtypes = [vp, fp, fp, f32, vp, fp, fp, NormDims, DTypes, vp]
+    L.mssm_layer_norm_fwd.restype = ctypes.c_int
+    L.mssm_layer_norm_bwd.argtypes = [vp, vp, fp, fp, fp, vp, fp, fp, NormDims, DTypes, vp]
+    L.mssm_layer_norm_bwd.restype = ctypes.c_int
+    L.mssm_gated_recurrence_fwd.argtypes = [vp, vp, vp, fp, f32, fp, vp, fp, RecurrenceDims,
+                                            DTypes, vp]
+    L.mssm_gated_recurrence_fwd.restype = ctypes.c_int
+    L.mssm_gated_recurrence_bwd.argtypes = [vp, vp, vp, fp, f32, fp, vp, vp, fp, vp, vp, vp, fp,
+                                            fp, RecurrenceDims, DTypes, vp]
+    L.mssm_gated_recurrence_bwd.restype = ctypes.c_int
+    L.mssm_gated_recurrence_update.argtypes = [fp, vp, vp, vp, fp, f32, vp, RecurrenceDims,
+                                               DTypes, vp]
+    L.mssm_gated_recurrence_update.restype = ctypes.c_int
+    L.mssm_linear_cross_entropy_fwd.argtypes = [vp, vp, vp, i64, fp, fp, LossDims, DTypes, vp]
+    L.mssm_linear_cross_entropy_fwd.restype = ctypes.c_int
+    L.mssm_linear_cross_entropy_bwd.argtypes = [vp, vp, vp, i64, fp, fp, vp, vp, LossDims,
+                                                DTypes, vp]
+    L.mssm_linear_cross_entropy_bwd.restype = ctypes.c_int
     L.mssm_force_variant.argtypes = [ctypes.c_int]
     L.mssm_force_variant.restype = ctypes.c_int
     L.mssm_last_variant.argtypes = []

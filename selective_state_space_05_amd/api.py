@@ -414,6 +414,242 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
     return y
 
 
+def _on_gpu(t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor, got %s" % type(t).__name__)
+    if t.device.type != "cuda":
+        raise ValueError("tensors must live on a GPU device")
+    return t.device
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
+    """Layer norm over the last dimension on the GPU.
+
+    x: (..., dim) float32 or bfloat16; weight, bias: (dim,) float32 (None: 1
+    and 0).  Returns ``(y, mean, rstd)``: y like x, mean and rstd (...)
+    float32, which the backward takes.
+    """
+    L = _lib.lib()
+    dev = _on_gpu(x)
+    _need(x, "x")
+    io = _io_dtype(x)
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    for name, t in (("weight", weight), ("bias", bias)):
+        _need(t, name, torch.float32, dev)
+        if t is not None and tuple(t.shape) != (dim,):
+            raise ValueError("%s must be (dim,)" % name)
+    _need_shape(out, "out", x.shape)
+    y = out if out is not None else torch.empty_like(x)
+    _need(y, "out", x.dtype, dev)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        st = L.mssm_layer_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), float(eps), _ptr(y),
+                                   _ptr(mean), _ptr(rstd), _lib.NormDims(rows, dim),
+                                   _lib.DTypes(io, _lib.MSSM_F32), _stream_handle(dev))
+    _check(st)
+    return y, mean, rstd
+
+
+def layer_norm_bwd(dy, x, mean, rstd, weight=None):
+    """Gradients of the layer norm for the output gradient ``dy`` (like x);
+    mean and rstd are the forward's.  Returns a dict: dx like x, dweight and
+    dbias (dim,) float32."""
+    L = _lib.lib()
+    dev = _on_gpu(x)
+    io = _io_dtype(x)
+    _need(x, "x")
+    _need(dy, "dy", x.dtype, dev)
+    if dy is None or dy.shape != x.shape or x.dim() < 1:
+        raise ValueError("x and dy must share one (..., dim) shape")
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        _need(t, name, torch.float32, dev)
+        _need_shape(t, name, x.shape[:-1])
+    _need(weight, "weight", torch.float32, dev)
+    _need_shape(weight, "weight", (dim,))
+    g = {"dx": torch.empty_like(x),
+         "dweight": torch.empty((dim,), dtype=torch.float32, device=dev),
+         "dbias": torch.empty((dim,), dtype=torch.float32, device=dev)}
+    with torch.cuda.device(dev):
+        st = L.mssm_layer_norm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
+                                   _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]),
+                                   _lib.NormDims(rows, dim), _lib.DTypes(io, _lib.MSSM_F32),
+                                   _stream_handle(dev))
+    _check(st)
+    return g
+
+
+def _recurrence_args(x, r, i, lam, ndim):
+    """Shared checks of the gated recurrence; returns (device, dim)."""
+    dev = _on_gpu(x)
+    _io_dtype(x)
+    _need(x, "x")
+    if x.dim() != ndim:
+        raise ValueError("x must be (batch, L, dim)" if ndim == 3 else "x must be (batch, dim)")
+    for name, t in (("r", r), ("i", i)):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        _need(t, name, x.dtype, dev)
+        _need_shape(t, name, x.shape)
+    if lam is None:
+        raise ValueError("lam is required")
+    _need(lam, "lam", torch.float32, dev)
+    _need_shape(lam, "lam", (x.shape[-1],))
+    return dev, x.shape[-1]
+
+
+def gated_recurrence_fwd(x, r, i, lam, scale=8.0, h0=None, return_last_state=True, out=None,
+                         h_out=None):
+    """Gated linear recurrence on the GPU:
+    log a_t = -scale softplus(lam) sigmoid(r_t),
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t, y_t = h_t.
+
+    x, r, i: (batch, L, dim) float32 or bfloat16 (one dtype); lam: (dim,)
+    float32; h0: (batch, dim) float32 initial state (None: zero; it may be
+    passed as ``h_out`` too, to advance a state in place).  Returns
+    ``(y, h_last)``: y like x, h_last (batch, dim) float32 (None if
+    ``return_last_state`` is False).
+    """
+    L = _lib.lib()
+    dev, dim = _recurrence_args(x, r, i, lam, 3)
+    batch, seqlen = x.shape[:2]
+    for name, t in (("h0", h0), ("h_out", h_out)):
+        _need(t, name, torch.float32, dev)
+        _need_shape(t, name, (batch, dim))
+    _need_shape(out, "out", x.shape)
+    y = out if out is not None else torch.empty_like(x)
+    _need(y, "out", x.dtype, dev)
+    h_last = None
+    if return_last_state:
+        h_last = h_out if h_out is not None else torch.empty(
+            (batch, dim), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        st = L.mssm_gated_recurrence_fwd(
+            _ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(scale), _ptr(h0), _ptr(y), _ptr(h_last),
+            _lib.RecurrenceDims(batch, seqlen, dim), _lib.DTypes(_io_dtype(x), _lib.MSSM_F32),
+            _stream_handle(dev))
+    _check(st)
+    return y, h_last
+
+
+def gated_recurrence_bwd(x, r, i, lam, y, dy, scale=8.0, h0=None, dh_last=None):
+    """Gradients of the gated linear recurrence for output gradients ``dy``
+    (like x) and ``dh_last`` ((batch, dim) float32, None: zero); y is the
+    forward's output.  Returns a dict: dx, dr, di like x; dlam (dim,) and dh0
+    (batch, dim) float32."""
+    L = _lib.lib()
+    dev, dim = _recurrence_args(x, r, i, lam, 3)
+    batch, seqlen = x.shape[:2]
+    for name, t in (("y", y), ("dy", dy)):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        _need(t, name, x.dtype, dev)
+        _need_shape(t, name, x.shape)
+    for name, t in (("h0", h0), ("dh_last", dh_last)):
+        _need(t, name, torch.float32, dev)
+        _need_shape(t, name, (batch, dim))
+    g = {"dx": torch.empty_like(x), "dr": torch.empty_like(x), "di": torch.empty_like(x),
+         "dlam": torch.empty((dim,), dtype=torch.float32, device=dev),
+         "dh0": torch.empty((batch, dim), dtype=torch.float32, device=dev)}
+    with torch.cuda.device(dev):
+        st = L.mssm_gated_recurrence_bwd(
+            _ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(scale), _ptr(h0), _ptr(y), _ptr(dy),
+            _ptr(dh_last), _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["di"]), _ptr(g["dlam"]),
+            _ptr(g["dh0"]), _lib.RecurrenceDims(batch, seqlen, dim),
+            _lib.DTypes(_io_dtype(x), _lib.MSSM_F32), _stream_handle(dev))
+    _check(st)
+    return g
+
+
+def gated_recurrence_update(state, x, r, i, lam, scale=8.0, out=None):
+    """One decode step of the gated linear recurrence, advancing ``state``
+    ((batch, dim) float32) in place; x, r, i: (batch, dim).  Returns y like
+    x."""
+    L = _lib.lib()
+    dev, dim = _recurrence_args(x, r, i, lam, 2)
+    if state is None:
+        raise ValueError("state is required")
+    _need(state, "state", torch.float32, dev)
+    _need_shape(state, "state", x.shape)
+    _need_shape(out, "out", x.shape)
+    y = out if out is not None else torch.empty_like(x)
+    _need(y, "out", x.dtype, dev)
+    with torch.cuda.device(dev):
+        st = L.mssm_gated_recurrence_update(
+            _ptr(state), _ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(scale), _ptr(y),
+            _lib.RecurrenceDims(x.shape[0], 1, dim), _lib.DTypes(_io_dtype(x), _lib.MSSM_F32),
+            _stream_handle(dev))
+    _check(st)
+    return y
+
+
+def _loss_args(hidden, weight, targets):
+    """Shared checks of the projected cross entropy; returns (device, dims, dtypes)."""
+    dev = _on_gpu(hidden)
+    io = _io_dtype(hidden)
+    _need(hidden, "hidden")
+    for name, t in (("weight", weight), ("targets", targets)):
+        if t is None:
+            raise ValueError("%s is required" % name)
+    _need(weight, "weight", hidden.dtype, dev)
+    _need(targets, "targets", torch.int64, dev)
+    if hidden.dim() != 2 or weight.dim() != 2 or hidden.shape[1] != weight.shape[1]:
+        raise ValueError("hidden must be (tokens, dim) and weight (vocab, dim)")
+    _need_shape(targets, "targets", (hidden.shape[0],))
+    return (dev, _lib.LossDims(hidden.shape[0], hidden.shape[1], weight.shape[0]),
+            _lib.DTypes(io, _lib.MSSM_F32))
+
+
+def linear_cross_entropy_fwd(hidden, weight, targets, ignore_index=-100):
+    """Softmax cross entropy of the logits ``hidden @ weight.T`` on the GPU,
+    without storing them.
+
+    hidden: (tokens, dim), weight: (vocab, dim), float32 or bfloat16 (one
+    dtype); targets: (tokens,) int64.  Returns ``(loss, lse)``, both (tokens,)
+    float32: the loss is 0 where the target is ``ignore_index`` and NaN where
+    it is out of range; lse is the logits' log sum exp, which the backward
+    takes.
+    """
+    L = _lib.lib()
+    dev, dims, dt = _loss_args(hidden, weight, targets)
+    loss = torch.empty((hidden.shape[0],), dtype=torch.float32, device=dev)
+    lse = torch.empty((hidden.shape[0],), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        st = L.mssm_linear_cross_entropy_fwd(_ptr(hidden), _ptr(weight), _ptr(targets),
+                                             int(ignore_index), _ptr(loss), _ptr(lse), dims, dt,
+                                             _stream_handle(dev))
+    _check(st)
+    return loss, lse
+
+
+def linear_cross_entropy_bwd(hidden, weight, targets, lse, dloss, ignore_index=-100):
+    """Gradients of the projected cross entropy for the gradients ``dloss``
+    ((tokens,) float32) of the tokens' losses; lse is the forward's.  Returns
+    a dict: dhidden like hidden, dweight like weight."""
+    L = _lib.lib()
+    dev, dims, dt = _loss_args(hidden, weight, targets)
+    for name, t in (("lse", lse), ("dloss", dloss)):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        _need(t, name, torch.float32, dev)
+        _need_shape(t, name, (hidden.shape[0],))
+    g = {"dhidden": torch.empty_like(hidden), "dweight": torch.empty_like(weight)}
+    with torch.cuda.device(dev):
+        st = L.mssm_linear_cross_entropy_bwd(_ptr(hidden), _ptr(weight), _ptr(targets),
+                                             int(ignore_index), _ptr(lse), _ptr(dloss),
+                                             _ptr(g["dhidden"]), _ptr(g["dweight"]), dims, dt,
+                                             _stream_handle(dev))
+    _check(st)
+    return g
+
+
 def probe_copy(src, dst):
     """Launch the streaming copy probe (mssm_probe_copy) from ``src`` to
     ``dst`` (contiguous device tensors of the same byte size) on the current

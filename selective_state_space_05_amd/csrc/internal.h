@@ -164,6 +164,70 @@ hipError_t launch_probe_valu(int op, int iters, float *out, hipStream_t stream);
 hipError_t launch_state_update(const StepArgs &a, hipStream_t stream);
 bool state_update_supported(const StepArgs &a);
 
+// One layer norm, already validated: x, y, dy, dx (rows, dim); weight, bias,
+// dweight, dbias (dim); mean, rstd (rows).  The forward leaves dy, dx and the
+// weight gradients null.
+struct NormArgs {
+    const void *x;
+    const float *weight;      // may be null -> 1
+    const float *bias;        // may be null -> 0
+    float eps;
+    void *y;
+    float *mean;              // forward: output, may be null
+    float *rstd;
+    const void *dy;
+    void *dx;
+    float *dweight;           // may be null
+    float *dbias;             // may be null
+    int64_t rows, dim;
+    IoType io;
+};
+hipError_t launch_layer_norm_fwd(const NormArgs &a, hipStream_t stream);
+hipError_t launch_layer_norm_bwd(const NormArgs &a, hipStream_t stream);
+
+// One gated linear recurrence, already validated: activations (batch, L, dim),
+// states (batch, dim), lam (dim).  h0 may be the same buffer as h_last.
+struct RecurrenceArgs {
+    const void *x;
+    const void *r;
+    const void *i;
+    const float *lam;
+    float scale;
+    const float *h0;          // may be null -> 0
+    void *y;                  // forward: output; backward: input
+    float *h_last;            // may be null
+    const void *dy;           // backward only, from here on
+    const float *dh_last;     // may be null -> 0
+    void *dx;
+    void *dr;
+    void *di;
+    float *dlam;              // may be null
+    float *dh0;               // may be null
+    int64_t batch, L, dim;
+    IoType io;
+};
+bool gated_recurrence_supported(const RecurrenceArgs &a);
+hipError_t launch_gated_recurrence_fwd(const RecurrenceArgs &a, hipStream_t stream);
+hipError_t launch_gated_recurrence_bwd(const RecurrenceArgs &a, hipStream_t stream);
+
+// One cross entropy over a vocabulary projection, already validated: hidden,
+// dhidden (tokens, dim); weight, dweight (vocab, dim); the rest (tokens).
+struct LossArgs {
+    const void *hidden;
+    const void *weight;
+    const int64_t *targets;
+    int64_t ignore_index;
+    float *loss;              // forward
+    float *lse;               // forward: output, may be null; backward: input
+    const float *dloss;       // backward only, from here on
+    void *dhidden;
+    void *dweight;
+    int64_t tokens, dim, vocab;
+    IoType io;
+};
+hipError_t launch_linear_cross_entropy_fwd(const LossArgs &a, hipStream_t stream);
+hipError_t launch_linear_cross_entropy_bwd(const LossArgs &a, hipStream_t stream);
+
 hipError_t launch_ssd_recurrent(const SSDArgs &a, hipStream_t stream);
 bool ssd_recurrent_supported(const SSDArgs &a);
 

@@ -1,0 +1,440 @@
+// linear_cross_entropy.hip -- softmax cross entropy of the logits
+// l = hidden weight^T over a large vocabulary, forward and backward, the
+// logits formed a tile at a time on the matrix cores and never stored.
+//
+// Forward: every tile of logits gives, per token, its maximum m and
+// s = sum exp(l - m); the tiles' pairs join as
+//   (m1, s1) + (m2, s2) = (max, s1 e^(m1 - max) + s2 e^(m2 - max)),
+// lse = m + log s and loss = lse - l_target.
+//
+// Backward, for a piece of the vocabulary at a time:
+//   p = (exp(l - lse) - [v == target]) dloss   (0 for ignored tokens)
+//   dhidden += p weight,   dweight = p^T hidden
+// with the logits formed again and p held in the I/O dtype for that piece
+// only.  In bfloat16 the rounding of p (half a step, 2^-9 relative, of
+// either sign) averages over the sums it enters.
+//
+// All three products run on one kernel: C[m, n] = sum_k A[m, k] B[n, k] with
+// both operands stored along k, for which weight, hidden and p are also laid
+// out transposed.
+#include "device_math.h"
+#include "internal.h"
+
+namespace mssm {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kRowBytes = 128;   // of k staged per step and operand row
+constexpr int kChunks = kRowBytes / 16;
+constexpr int kBM = 128, kBN = 128;
+constexpr int kThreads = 256;    // four waves, 2 x 2, 64 x 64 of C each
+constexpr int kWM = 64, kWN = 64;
+
+// One product step over the 16 bytes of k that each lane holds of its A row
+// (lane % 32) and its B row: bfloat16 holds k 8 (lane / 32) .. + 7 of one
+// 32x32x16 product; float32 four products of 32x32x2, the order of k inside
+// them being the same for A and B.
+__device__ __forceinline__ void mma(f32x16 &c, u32x4 a, u32x4 b, uint16_t) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x16 &c, u32x4 a, u32x4 b, float) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[j], y[j], c, 0, 0, 0);
+}
+
+// Rows of one operand: `rows` of them, `ld` bytes apart, 16-byte aligned.
+struct Rows {
+    const unsigned char *p;
+    int64_t ld;
+    int rows;
+};
+
+// Row of C inside a 32 x 32 block that element e of a lane's accumulator is
+// (its column is lane % 32).
+__device__ __forceinline__ int acc_row(int e, int lane) { return 8 * (e / 4) + 4 * (lane / 32) + e % 4; }
+
+template <typename T, typename Epilogue>
+__global__ __launch_bounds__(kThreads) void product_kernel(Rows A, Rows B, int64_t kbytes, int mtiles,
+                                                           Epilogue ep) {
+    __shared__ __align__(16) unsigned char lds[(kBM + kBN) * kRowBytes];
+    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    const int m0 = static_cast<int>(blockIdx.x % mtiles) * kBM, n0 = static_cast<int>(blockIdx.x / mtiles) * kBN;
+    const int wm = (wave / 2) * kWM, wn = (wave % 2) * kWN;
+    f32x16 acc[kWM / 32][kWN / 32];
+#pragma unroll
+    for (int i = 0; i < kWM / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < kWN / 32; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    const int col = tid % kChunks;
+    for (int64_t k0 = 0; k0 < kbytes; k0 += kRowBytes) {
+        const int64_t kk = k0 + 16 * col;
+        __syncthreads();
+        // rows past the end and k past the end are zeros
+#pragma unroll
+        for (int s = 0; s < (kBM + kBN) * kChunks / kThreads; ++s) {
+            const int row = s * (kThreads / kChunks) + tid / kChunks;
+            u32x4 v = {0, 0, 0, 0};
+            if (kk < kbytes) {
+                if (row < kBM) {
+                    if (m0 + row < A.rows)
+                        v = *reinterpret_cast<const u32x4 *>(A.p + (m0 + row) * A.ld + kk);
+                } else if (n0 + row - kBM < B.rows) {
+                    v = *reinterpret_cast<const u32x4 *>(B.p + (n0 + row - kBM) * B.ld + kk);
+                }
+            }
+            // chunks of a row are rotated by the row so that lanes reading one
+            // chunk of consecutive rows hit different banks
+            *reinterpret_cast<u32x4 *>(lds + row * kRowBytes + ((col ^ (row % kChunks)) * 16)) = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kChunks; c += 2) {
+            u32x4 a[kWM / 32], b[kWN / 32];
+            const int ch = c + lane / 32;
+#pragma unroll
+            for (int i = 0; i < kWM / 32; ++i) {
+                const int row = wm + 32 * i + lane % 32;
+                a[i] = *reinterpret_cast<const u32x4 *>(lds + row * kRowBytes + ((ch ^ (row % kChunks)) * 16));
+            }
+#pragma unroll
+            for (int j = 0; j < kWN / 32; ++j) {
+                const int row = kBM + wn + 32 * j + lane % 32;
+                b[j] = *reinterpret_cast<const u32x4 *>(lds + row * kRowBytes + ((ch ^ (row % kChunks)) * 16));
+            }
+#pragma unroll
+            for (int i = 0; i < kWM / 32; ++i)
+#pragma unroll
+                for (int j = 0; j < kWN / 32; ++j) mma(acc[i][j], a[i], b[j], T{});
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kWN / 32; ++j) ep.column(m0 + wm, n0 + wn + 32 * j + lane % 32, lane, &acc[0][j]);
+}
+
+// ---- forward: maximum and sum of exponentials of a token over a tile's words
+struct LossTile {
+    float2 *part;              // [vocabulary tile of kWM words][token]
+    float *target_logit;       // [token]
+    const int64_t *targets;
+    int tokens, words, word0;  // words of this piece; word0: the piece's first
+    int part0;                 // first part of this piece
+    __device__ void column(int m, int t, int lane, const f32x16 *acc) const {
+        if (t >= tokens) t = -1;
+        const int64_t target = t >= 0 ? targets[t] - word0 : -1;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kWM / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int v = m + 32 * i + acc_row(e, lane);
+                const float l = acc[i * (kWN / 32)][e];
+                if (v < words) top = fmaxf(top, l);
+                if (v == target && v < words) target_logit[t] = l;
+            }
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWM / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int v = m + 32 * i + acc_row(e, lane);
+                if (v < words) sum += fast_exp2((acc[i * (kWN / 32)][e] - ref) * kLog2e);
+            }
+        sum += __shfl_xor(sum, 32);
+        if (t >= 0 && lane < 32) part[static_cast<int64_t>(part0 + m / kWM) * tokens + t] = make_float2(top, sum);
+    }
+};
+
+__global__ __launch_bounds__(256) void loss_join_kernel(const float2 *__restrict__ part, int parts, int tokens,
+                                                        const int64_t *__restrict__ targets, int64_t ignore,
+                                                        int64_t vocab, float *__restrict__ loss,
+                                                        float *__restrict__ lse) {
+    const int t = blockIdx.x * 256 + threadIdx.x;
+    if (t >= tokens) return;
+    float m = -INFINITY, s = 0.0f;
+    for (int k = 0; k < parts; ++k) {
+        const float2 p = part[static_cast<int64_t>(k) * tokens + t];
+        const float top = fmaxf(m, p.x), ref = top == -INFINITY ? 0.0f : top;
+        s = s * fast_exp2((m - ref) * kLog2e) + p.y * fast_exp2((p.x - ref) * kLog2e);
+        m = top;
+    }
+    const float l = m + fast_log2(s) * kLn2;
+    if (lse) lse[t] = l;
+    const int64_t target = targets[t];
+    loss[t] = target == ignore ? 0.0f : (target < 0 || target >= vocab) ? NAN : l - loss[t];
+}
+
+// ---- backward: p of a piece, in both layouts
+template <typename T>
+struct ProbTile {
+    T *p, *pt;                 // p[token][word] and pt[word][token]
+    int64_t ldp, ldpt;         // elements
+    const int64_t *targets;
+    const float *lse, *dloss;
+    int64_t ignore, vocab;
+    int tokens, words, word0;
+    __device__ void column(int m, int t, int lane, const f32x16 *acc) const {
+        if (t >= ldpt) return;
+        const int64_t target = t < tokens ? targets[t] : ignore;
+        const bool live = target != ignore;
+        const float ref = live ? lse[t] : 0.0f;
+        float g = live ? dloss[t] : 0.0f;
+        if (live && (target < 0 || target >= vocab)) g = NAN;
+#pragma unroll
+        for (int i = 0; i < kWM / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int v = m + 32 * i + acc_row(e, lane);
+                if (v >= ldp) continue;
+                float x = 0.0f;
+                if (live && v < words) {
+                    x = fast_exp2((acc[i * (kWN / 32)][e] - ref) * kLog2e);
+                    x = (x - (v + word0 == target ? 1.0f : 0.0f)) * g;
+                }
+                if (t < tokens) Io<T>::store(p, t * ldp + v, x);
+                if (v < words) Io<T>::store(pt, v * ldpt + t, x);
+            }
+    }
+};
+
+// ---- backward: rows of a gradient, [n][m]; accumulated over pieces in float32
+template <typename T>
+struct GradTile {
+    float *sum;                // float32 accumulator, or null
+    T *out;                    // output, or null
+    int64_t ld;
+    int rows, cols;            // of the output
+    bool add;                  // sum holds earlier pieces
+    __device__ void column(int m, int n, int lane, const f32x16 *acc) const {
+        if (n >= rows) return;
+#pragma unroll
+        for (int i = 0; i < kWM / 32; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int d = m + 32 * i + acc_row(e, lane);
+                if (d >= cols) continue;
+                float v = acc[i * (kWN / 32)][e];
+                const int64_t at = n * ld + d;
+                if (add) v += sum[at];
+                if (out) Io<T>::store(out, at, v);
+                else sum[at] = v;
+            }
+    }
+};
+
+// Copy of rows [0, rows) x [0, cols) with rows `ldo` elements apart, zero past
+// the columns.
+template <typename T>
+__global__ __launch_bounds__(256) void align_rows_kernel(const T *__restrict__ in, T *__restrict__ out,
+                                                         int64_t rows, int64_t cols, int64_t ldo) {
+    const int64_t n = rows * ldo;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k < n;
+         k += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = k / ldo, c = k - r * ldo;
+        out[k] = c < cols ? in[r * cols + c] : T{};
+    }
+}
+
+// out[c][r] = in[r][c], zero for rows past the end and for rows whose target
+// is `ignore` (targets may be null: then every row counts).
+template <typename T>
+__global__ __launch_bounds__(256) void transpose_kernel(const T *__restrict__ in, T *__restrict__ out, int rows,
+                                                        int cols, int64_t ldo,
+                                                        const int64_t *__restrict__ targets, int64_t ignore) {
+    __shared__ T tile[32][33];
+    const int c0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+    for (int k = ty; k < 32; k += 8) {
+        const int r = r0 + k, c = c0 + tx;
+        T v{};
+        if (r < rows && c < cols && !(targets && targets[r] == ignore)) v = in[static_cast<int64_t>(r) * cols + c];
+        tile[k][tx] = v;
+    }
+    __syncthreads();
+    for (int k = ty; k < 32; k += 8) {
+        const int c = c0 + k, r = r0 + tx;
+        if (c < cols && r < ldo) out[static_cast<int64_t>(c) * ldo + r] = tile[tx][k];
+    }
+}
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t ceil_div(int64_t n, int64_t by) { return (n + by - 1) / by; }
+
+template <typename T>
+bool aligned(const void *p, int64_t dim) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && dim * sizeof(T) % 16 == 0;
+}
+
+template <typename T, typename Epilogue>
+hipError_t product(Rows A, Rows B, int64_t kbytes, const Epilogue &ep, hipStream_t stream) {
+    const int64_t mt = ceil_div(A.rows, kBM), nt = ceil_div(B.rows, kBN);
+    hipLaunchKernelGGL((product_kernel<T, Epilogue>), dim3(static_cast<uint32_t>(mt * nt)), dim3(kThreads), 0,
+                       stream, A, B, kbytes, static_cast<int>(mt), ep);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t align_rows(const T *in, T *out, int64_t rows, int64_t cols, int64_t ldo, hipStream_t stream) {
+    const int64_t blocks = ceil_div(rows * ldo, 256 * 4);
+    hipLaunchKernelGGL(align_rows_kernel<T>, dim3(static_cast<uint32_t>(blocks < 65536 ? blocks : 65536)),
+                       dim3(256), 0, stream, in, out, rows, cols, ldo);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t transpose(const T *in, T *out, int64_t rows, int64_t cols, int64_t ldo, const int64_t *targets,
+                     int64_t ignore, hipStream_t stream) {
+    hipLaunchKernelGGL(transpose_kernel<T>,
+                       dim3(static_cast<uint32_t>(ceil_div(cols, 32)), static_cast<uint32_t>(ceil_div(ldo, 32))),
+                       dim3(256), 0, stream, in, out, static_cast<int>(rows), static_cast<int>(cols), ldo, targets,
+                       ignore);
+    return hipGetLastError();
+}
+
+// Words of the vocabulary in one piece: p of the piece has at most 2^27
+// elements, and a piece at least 1024 words.
+int64_t piece_words(int64_t tokens, int64_t vocab) {
+    int64_t n = (int64_t(1) << 27) / (tokens < 1 ? 1 : tokens) / 1024 * 1024;
+    if (n < 1024) n = 1024;
+    return n < vocab ? n : vocab;
+}
+
+// Scratch of one call, cut from one allocation.
+struct Scratch {
+    size_t size = 0;
+    unsigned char *base = nullptr;
+    size_t add(size_t bytes) {
+        const size_t at = size;
+        size += (bytes + 255) / 256 * 256;
+        return at;
+    }
+};
+
+template <typename T>
+hipError_t fwd(const LossArgs &a, hipStream_t stream) {
+    const int64_t dimp = round_up(a.dim, 16 / sizeof(T));
+    const bool copy_h = !aligned<T>(a.hidden, a.dim), copy_w = !aligned<T>(a.weight, a.dim);
+    const int64_t piece = copy_w ? piece_words(dimp, a.vocab) : a.vocab;
+    const int64_t parts = ceil_div(a.vocab, piece) * ceil_div(piece, kWM);
+    Scratch s;
+    const size_t at_part = s.add(static_cast<size_t>(parts) * a.tokens * sizeof(float2));
+    const size_t at_h = s.add(copy_h ? static_cast<size_t>(a.tokens) * dimp * sizeof(T) : 0);
+    const size_t at_w = s.add(copy_w ? static_cast<size_t>(piece) * dimp * sizeof(T) : 0);
+    void *mem = nullptr;
+    hipError_t e = scratch_alloc(&mem, s.size, stream);
+    if (e != hipSuccess) return e;
+    unsigned char *base = static_cast<unsigned char *>(mem);
+    float2 *part = reinterpret_cast<float2 *>(base + at_part);
+    const T *h = static_cast<const T *>(a.hidden);
+    if (copy_h) {
+        e = align_rows(h, reinterpret_cast<T *>(base + at_h), a.tokens, a.dim, dimp, stream);
+        h = reinterpret_cast<const T *>(base + at_h);
+    }
+    const Rows B{reinterpret_cast<const unsigned char *>(h), dimp * static_cast<int64_t>(sizeof(T)),
+                 static_cast<int>(a.tokens)};
+    int part0 = 0;
+    for (int64_t w0 = 0; w0 < a.vocab && e == hipSuccess; w0 += piece) {
+        const int64_t words = a.vocab - w0 < piece ? a.vocab - w0 : piece;
+        const T *w = static_cast<const T *>(a.weight) + w0 * a.dim;
+        if (copy_w) {
+            e = align_rows(w, reinterpret_cast<T *>(base + at_w), words, a.dim, dimp, stream);
+            w = reinterpret_cast<const T *>(base + at_w);
+            if (e != hipSuccess) break;
+        }
+        const Rows A{reinterpret_cast<const unsigned char *>(w), dimp * static_cast<int64_t>(sizeof(T)),
+                     static_cast<int>(words)};
+        const LossTile ep{part, a.loss, a.targets, static_cast<int>(a.tokens), static_cast<int>(words),
+                          static_cast<int>(w0), part0};
+        e = product<T>(A, B, dimp * sizeof(T), ep, stream);
+        part0 += static_cast<int>(ceil_div(words, kWM));
+    }
+    if (e == hipSuccess) {
+        hipLaunchKernelGGL(loss_join_kernel, dim3(static_cast<uint32_t>(ceil_div(a.tokens, 256))), dim3(256), 0,
+                           stream, part, part0, static_cast<int>(a.tokens), a.targets, a.ignore_index, a.vocab,
+                           a.loss, a.lse);
+        e = hipGetLastError();
+    }
+    const hipError_t f = scratch_free(mem, stream);
+    return e != hipSuccess ? e : f;
+}
+
+template <typename T>
+hipError_t bwd(const LossArgs &a, hipStream_t stream) {
+    constexpr int64_t kUnit = 16 / sizeof(T);
+    const int64_t dimp = round_up(a.dim, kUnit), tokp = round_up(a.tokens, kUnit);
+    const int64_t piece = piece_words(a.tokens, a.vocab), piecep = round_up(piece, kUnit);
+    const bool copy_h = !aligned<T>(a.hidden, a.dim), copy_w = !aligned<T>(a.weight, a.dim);
+    const bool pieces = piece < a.vocab;
+    Scratch s;
+    const size_t at_h = s.add(copy_h ? static_cast<size_t>(a.tokens) * dimp * sizeof(T) : 0);
+    const size_t at_w = s.add(copy_w ? static_cast<size_t>(piece) * dimp * sizeof(T) : 0);
+    const size_t at_ht = s.add(static_cast<size_t>(a.dim) * tokp * sizeof(T));
+    const size_t at_wt = s.add(static_cast<size_t>(a.dim) * piecep * sizeof(T));
+    const size_t at_p = s.add(static_cast<size_t>(a.tokens) * piecep * sizeof(T));
+    const size_t at_pt = s.add(static_cast<size_t>(piece) * tokp * sizeof(T));
+    const size_t at_sum = s.add(pieces ? static_cast<size_t>(a.tokens) * a.dim * sizeof(float) : 0);
+    void *mem = nullptr;
+    hipError_t e = scratch_alloc(&mem, s.size, stream);
+    if (e != hipSuccess) return e;
+    unsigned char *base = static_cast<unsigned char *>(mem);
+    T *p = reinterpret_cast<T *>(base + at_p), *pt = reinterpret_cast<T *>(base + at_pt);
+    T *ht = reinterpret_cast<T *>(base + at_ht), *wt = reinterpret_cast<T *>(base + at_wt);
+    const T *h = static_cast<const T *>(a.hidden);
+    const int tokens = static_cast<int>(a.tokens), dim = static_cast<int>(a.dim);
+    auto rows = [](const T *q, int64_t ld, int64_t n) {
+        return Rows{reinterpret_cast<const unsigned char *>(q), ld * static_cast<int64_t>(sizeof(T)),
+                    static_cast<int>(n)};
+    };
+    e = transpose(h, ht, a.tokens, a.dim, tokp, a.targets, a.ignore_index, stream);
+    if (e == hipSuccess && copy_h) {
+        e = align_rows(h, reinterpret_cast<T *>(base + at_h), a.tokens, a.dim, dimp, stream);
+        h = reinterpret_cast<const T *>(base + at_h);
+    }
+    for (int64_t w0 = 0; w0 < a.vocab && e == hipSuccess; w0 += piece) {
+        const int64_t words = a.vocab - w0 < piece ? a.vocab - w0 : piece, wordsp = round_up(words, kUnit);
+        const T *w = static_cast<const T *>(a.weight) + w0 * a.dim;
+        e = transpose<T>(w, wt, words, a.dim, wordsp, nullptr, 0, stream);
+        if (e != hipSuccess) break;
+        if (copy_w) {
+            e = align_rows(w, reinterpret_cast<T *>(base + at_w), words, a.dim, dimp, stream);
+            w = reinterpret_cast<const T *>(base + at_w);
+            if (e != hipSuccess) break;
+        }
+        const ProbTile<T> prob{p, pt, wordsp, tokp, a.targets, a.lse, a.dloss, a.ignore_index, a.vocab,
+                               tokens, static_cast<int>(words), static_cast<int>(w0)};
+        e = product<T>(rows(w, dimp, words), rows(h, dimp, a.tokens), dimp * sizeof(T), prob, stream);
+        if (e != hipSuccess) break;
+        float *sum = pieces ? reinterpret_cast<float *>(base + at_sum) : nullptr;
+        const GradTile<T> dh{sum, w0 + words >= a.vocab ? static_cast<T *>(a.dhidden) : nullptr, a.dim, tokens,
+                             dim, w0 > 0};
+        e = product<T>(rows(wt, wordsp, a.dim), rows(p, wordsp, a.tokens), wordsp * sizeof(T), dh, stream);
+        if (e != hipSuccess) break;
+        const GradTile<T> dw{nullptr, static_cast<T *>(a.dweight) + w0 * a.dim, a.dim, static_cast<int>(words),
+                             dim, false};
+        e = product<T>(rows(ht, tokp, a.dim), rows(pt, tokp, words), tokp * sizeof(T), dw, stream);
+    }
+    const hipError_t f = scratch_free(mem, stream);
+    return e != hipSuccess ? e : f;
+}
+
+}  // namespace
+
+hipError_t launch_linear_cross_entropy_fwd(const LossArgs &a, hipStream_t stream) {
+    return a.io == IO_F32 ? fwd<float>(a, stream) : fwd<uint16_t>(a, stream);
+}
+
+hipError_t launch_linear_cross_entropy_bwd(const LossArgs &a, hipStream_t stream) {
+    return a.io == IO_F32 ? bwd<float>(a, stream) : bwd<uint16_t>(a, stream);
+}
+
+}  // namespace mssm

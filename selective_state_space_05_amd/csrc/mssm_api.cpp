@@ -4,6 +4,7 @@
 // exercised without a GPU.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdint>
@@ -70,6 +71,28 @@ hipError_t zero_fill(float *p, int64_t n, hipStream_t s) {
     int64_t blocks = (n + 255) / 256;
     if (blocks > 4096) blocks = 4096;
     hipLaunchKernelGGL(zero_fill_kernel, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, s, p, n);
+    return hipGetLastError();
+}
+
+// The same for a range of bytes that may start and end inside a word.
+__global__ void zero_fill_bytes_kernel(unsigned char *p, int64_t n) {
+    int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    const int64_t head = min(n, static_cast<int64_t>((4 - (reinterpret_cast<uintptr_t>(p) & 3)) & 3));
+    const int64_t words = (n - head) / 4, tail = head + 4 * words;
+    uint32_t *w = reinterpret_cast<uint32_t *>(p + head);
+    if (i < head) p[i] = 0;
+    if (i < n - tail) p[tail + i] = 0;
+    for (; i < words; i += stride) w[i] = 0;
+}
+
+hipError_t zero_fill_bytes(void *p, int64_t n, hipStream_t s) {
+    if (n <= 0) return hipSuccess;
+    int64_t blocks = (n / 4 + 255) / 256;
+    if (blocks < 1) blocks = 1;
+    if (blocks > 4096) blocks = 4096;
+    hipLaunchKernelGGL(zero_fill_bytes_kernel, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, s,
+                       static_cast<unsigned char *>(p), n);
     return hipGetLastError();
 }
 
@@ -318,6 +341,92 @@ mssm_status ssd_fwd(const void *x, const void *dt, const float *dt_bias, const f
     }
     if (e != hipSuccess) return hip_fail(e, "SSD launch");
     g_last_variant = v;
+    return MSSM_OK;
+}
+
+// Sizes in bytes of a layer norm's operands, after the checks both passes share.
+struct NormSizes {
+    int64_t act_bytes, dim_bytes, row_bytes;
+};
+
+mssm_status check_norm(mssm_norm_dims d, mssm_dtypes dtypes, NormSizes *z) {
+    if (mssm_status s = check_dtypes(dtypes)) return s;
+    if (d.rows < 0 || d.dim < 0)
+        return fail(MSSM_ERR_INVALID_ARG, "negative size (rows %lld, dim %lld)", (long long)d.rows,
+                    (long long)d.dim);
+    const int64_t lim = int64_t(1) << 31;
+    if (d.rows >= lim || d.dim >= lim)
+        return fail(MSSM_ERR_UNSUPPORTED, "rows %lld or dim %lld reaches 2^31", (long long)d.rows,
+                    (long long)d.dim);
+    if (!mul_ok(d.rows, d.dim, &z->act_bytes) ||
+        !mul_ok(z->act_bytes, dtypes.io == MSSM_F32 ? 4 : 2, &z->act_bytes))
+        return fail(MSSM_ERR_INVALID_ARG, "sizes overflow int64");
+    z->dim_bytes = d.dim * 4;
+    z->row_bytes = d.rows * 4;
+    return MSSM_OK;
+}
+
+struct RecurrenceSizes {
+    int64_t rows, act_bytes;   // rows = batch * dim
+};
+
+mssm_status check_recurrence(mssm_recurrence_dims d, float scale, mssm_dtypes dtypes,
+                             RecurrenceSizes *z) {
+    if (mssm_status s = check_dtypes(dtypes)) return s;
+    if (d.batch < 0 || d.seqlen < 0 || d.dim < 0)
+        return fail(MSSM_ERR_INVALID_ARG, "negative size (batch %lld, L %lld, dim %lld)",
+                    (long long)d.batch, (long long)d.seqlen, (long long)d.dim);
+    if (!(scale >= 0.0f) || !std::isfinite(scale))
+        return fail(MSSM_ERR_INVALID_ARG, "scale must be finite and >= 0, got %g", (double)scale);
+    const int64_t lim = int64_t(1) << 31;
+    if (d.batch >= lim || d.seqlen >= lim || d.dim >= lim)
+        return fail(MSSM_ERR_UNSUPPORTED, "a size reaches 2^31 (batch %lld, L %lld, dim %lld)",
+                    (long long)d.batch, (long long)d.seqlen, (long long)d.dim);
+    int64_t state_bytes;
+    if (!mul_ok(d.batch, d.dim, &z->rows) || !mul_ok(z->rows, 4, &state_bytes) ||
+        !mul_ok(z->rows, d.seqlen, &z->act_bytes) ||
+        !mul_ok(z->act_bytes, dtypes.io == MSSM_F32 ? 4 : 2, &z->act_bytes))
+        return fail(MSSM_ERR_INVALID_ARG, "sizes overflow int64");
+    return MSSM_OK;
+}
+
+// An empty sequence: the state `out` (n floats, may be null) receives `in`,
+// or zeros.
+mssm_status copy_or_zero_state(const char *out_name, float *out, const char *in_name,
+                               const float *in, int64_t n, hipStream_t st) {
+    g_last_variant = MSSM_VARIANT_AUTO;
+    if (!out || out == in || n == 0) return MSSM_OK;
+    hipError_t e;
+    if (in) {
+        if (overlaps(range(out_name, out, n * 4), range(in_name, in, n * 4)))
+            return fail(MSSM_ERR_INVALID_ARG, "output %s overlaps input %s", out_name, in_name);
+        e = hipMemcpyAsync(out, in, n * 4, hipMemcpyDeviceToDevice, st);
+    } else {
+        e = zero_fill(out, n, st);
+    }
+    if (e != hipSuccess) return hip_fail(e, "copy of the state of an empty sequence");
+    return MSSM_OK;
+}
+
+struct LossSizes {
+    int64_t hidden_bytes, weight_bytes;
+};
+
+mssm_status check_loss(mssm_loss_dims d, mssm_dtypes dtypes, LossSizes *z) {
+    if (mssm_status s = check_dtypes(dtypes)) return s;
+    if (d.tokens < 0)
+        return fail(MSSM_ERR_INVALID_ARG, "negative size (tokens %lld)", (long long)d.tokens);
+    if (d.dim < 1 || d.vocab < 1)
+        return fail(MSSM_ERR_INVALID_ARG, "dim and vocab must be >= 1, got %lld and %lld",
+                    (long long)d.dim, (long long)d.vocab);
+    const int64_t lim = int64_t(1) << 30;
+    if (d.tokens >= lim || d.vocab >= lim || d.dim >= (int64_t(1) << 24))
+        return fail(MSSM_ERR_UNSUPPORTED,
+                    "tokens %lld or vocab %lld reaches 2^30, or dim %lld reaches 2^24",
+                    (long long)d.tokens, (long long)d.vocab, (long long)d.dim);
+    const int64_t esz = dtypes.io == MSSM_F32 ? 4 : 2;   // at most 2^56 bytes
+    z->hidden_bytes = d.tokens * d.dim * esz;
+    z->weight_bytes = d.vocab * d.dim * esz;
     return MSSM_OK;
 }
 
@@ -582,6 +691,233 @@ mssm_status mssm_selective_state_update(float *state, const void *x, const void 
         return fail(MSSM_ERR_UNSUPPORTED, "state update does not support this shape");
     const hipError_t e = mssm::launch_state_update(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(e, "state-update launch");
+    g_last_variant = MSSM_VARIANT_AUTO;
+    return MSSM_OK;
+}
+
+mssm_status mssm_layer_norm_fwd(const void *x, const float *weight, const float *bias, float eps,
+                                void *y, float *mean, float *rstd, mssm_norm_dims dims,
+                                mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    NormSizes z;
+    if (mssm_status s = check_norm(dims, dtypes, &z)) return s;
+    if (!(eps >= 0.0f) || !std::isfinite(eps))
+        return fail(MSSM_ERR_INVALID_ARG, "eps must be finite and >= 0, got %g", (double)eps);
+    if (dims.rows == 0 || dims.dim == 0) {
+        g_last_variant = MSSM_VARIANT_AUTO;
+        return MSSM_OK;
+    }
+    if (!x) return fail(MSSM_ERR_INVALID_ARG, "x is null");
+    if (!y) return fail(MSSM_ERR_INVALID_ARG, "y is null");
+    const Range ins[] = {range("x", x, z.act_bytes), range("weight", weight, z.dim_bytes),
+                         range("bias", bias, z.dim_bytes)};
+    const Range outs[] = {range("y", y, z.act_bytes), range("mean", mean, z.row_bytes),
+                          range("rstd", rstd, z.row_bytes)};
+    if (mssm_status c = check_overlaps(ins, 3, outs, 3, nullptr, nullptr)) return c;
+    mssm::NormArgs a{x, weight, bias, eps, y, mean, rstd, nullptr, nullptr, nullptr, nullptr,
+                     dims.rows, dims.dim, dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16};
+    const hipError_t e = mssm::launch_layer_norm_fwd(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "layer-norm launch");
+    g_last_variant = MSSM_VARIANT_AUTO;
+    return MSSM_OK;
+}
+
+mssm_status mssm_layer_norm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
+                                const float *weight, void *dx, float *dweight, float *dbias,
+                                mssm_norm_dims dims, mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    NormSizes z;
+    if (mssm_status s = check_norm(dims, dtypes, &z)) return s;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const Range outs[] = {range("dx", dx, z.act_bytes), range("dweight", dweight, z.dim_bytes),
+                          range("dbias", dbias, z.dim_bytes)};
+    if (dims.rows == 0 || dims.dim == 0) {
+        if (overlaps(outs[1], outs[2])) return fail(MSSM_ERR_INVALID_ARG, "dweight overlaps dbias");
+        hipError_t e = hipSuccess;
+        if (dweight) e = zero_fill(dweight, dims.dim, st);
+        if (e == hipSuccess && dbias) e = zero_fill(dbias, dims.dim, st);
+        if (e != hipSuccess) return hip_fail(e, "zero-fill of the gradients");
+        g_last_variant = MSSM_VARIANT_AUTO;
+        return MSSM_OK;
+    }
+    if (!dy) return fail(MSSM_ERR_INVALID_ARG, "dy is null");
+    if (!x) return fail(MSSM_ERR_INVALID_ARG, "x is null");
+    if (!mean) return fail(MSSM_ERR_INVALID_ARG, "mean is null");
+    if (!rstd) return fail(MSSM_ERR_INVALID_ARG, "rstd is null");
+    if (!dx) return fail(MSSM_ERR_INVALID_ARG, "dx is null");
+    const Range ins[] = {range("dy", dy, z.act_bytes), range("x", x, z.act_bytes),
+                         range("mean", mean, z.row_bytes), range("rstd", rstd, z.row_bytes),
+                         range("weight", weight, z.dim_bytes)};
+    if (mssm_status c = check_overlaps(ins, 5, outs, 3, nullptr, nullptr)) return c;
+    mssm::NormArgs a{x, weight, nullptr, 0.0f, nullptr, const_cast<float *>(mean),
+                     const_cast<float *>(rstd), dy, dx, dweight, dbias, dims.rows, dims.dim,
+                     dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16};
+    const hipError_t e = mssm::launch_layer_norm_bwd(a, st);
+    if (e != hipSuccess) return hip_fail(e, "layer-norm backward launch");
+    g_last_variant = MSSM_VARIANT_AUTO;
+    return MSSM_OK;
+}
+
+mssm_status mssm_gated_recurrence_fwd(const void *x, const void *r, const void *i, const float *lam,
+                                      float scale, const float *h0, void *y, float *h_last,
+                                      mssm_recurrence_dims dims, mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    RecurrenceSizes z;
+    if (mssm_status s = check_recurrence(dims, scale, dtypes, &z)) return s;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (z.rows == 0) {
+        g_last_variant = MSSM_VARIANT_AUTO;
+        return MSSM_OK;
+    }
+    if (dims.seqlen == 0) return copy_or_zero_state("h_last", h_last, "h0", h0, z.rows, st);
+    if (!x) return fail(MSSM_ERR_INVALID_ARG, "x is null");
+    if (!r) return fail(MSSM_ERR_INVALID_ARG, "r is null");
+    if (!i) return fail(MSSM_ERR_INVALID_ARG, "i is null");
+    if (!lam) return fail(MSSM_ERR_INVALID_ARG, "lam is null");
+    if (!y) return fail(MSSM_ERR_INVALID_ARG, "y is null");
+    const Range ins[] = {range("x", x, z.act_bytes), range("r", r, z.act_bytes),
+                         range("i", i, z.act_bytes), range("lam", lam, dims.dim * 4),
+                         range("h0", h0, z.rows * 4)};
+    const Range outs[] = {range("y", y, z.act_bytes), range("h_last", h_last, z.rows * 4)};
+    if (mssm_status c = check_overlaps(ins, 5, outs, 2, h0, h_last)) return c;
+    mssm::RecurrenceArgs a{};
+    a.x = x; a.r = r; a.i = i; a.lam = lam; a.scale = scale; a.h0 = h0; a.y = y; a.h_last = h_last;
+    a.batch = dims.batch; a.L = dims.seqlen; a.dim = dims.dim;
+    a.io = dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16;
+    if (!mssm::gated_recurrence_supported(a))
+        return fail(MSSM_ERR_UNSUPPORTED, "gated recurrence does not support this shape");
+    const hipError_t e = mssm::launch_gated_recurrence_fwd(a, st);
+    if (e != hipSuccess) return hip_fail(e, "gated-recurrence launch");
+    g_last_variant = MSSM_VARIANT_AUTO;
+    return MSSM_OK;
+}
+
+mssm_status mssm_gated_recurrence_bwd(const void *x, const void *r, const void *i, const float *lam,
+                                      float scale, const float *h0, const void *y, const void *dy,
+                                      const float *dh_last, void *dx, void *dr, void *di,
+                                      float *dlam, float *dh0, mssm_recurrence_dims dims,
+                                      mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    RecurrenceSizes z;
+    if (mssm_status s = check_recurrence(dims, scale, dtypes, &z)) return s;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const Range outs[] = {range("dx", dx, z.act_bytes), range("dr", dr, z.act_bytes),
+                          range("di", di, z.act_bytes), range("dlam", dlam, dims.dim * 4),
+                          range("dh0", dh0, z.rows * 4)};
+    if (z.rows == 0 || dims.seqlen == 0) {
+        if (overlaps(outs[3], outs[4])) return fail(MSSM_ERR_INVALID_ARG, "dlam overlaps dh0");
+        if (overlaps(outs[3], range("dh_last", dh_last, z.rows * 4)))
+            return fail(MSSM_ERR_INVALID_ARG, "output dlam overlaps input dh_last");
+        if (dh0 && dh0 == dh_last) return fail(MSSM_ERR_INVALID_ARG, "output dh0 overlaps input dh_last");
+        if (mssm_status s = copy_or_zero_state("dh0", dh0, "dh_last", dh_last, z.rows, st)) return s;
+        if (dlam) {
+            const hipError_t e = zero_fill(dlam, dims.dim, st);
+            if (e != hipSuccess) return hip_fail(e, "zero-fill of dlam");
+        }
+        return MSSM_OK;
+    }
+    if (!x) return fail(MSSM_ERR_INVALID_ARG, "x is null");
+    if (!r) return fail(MSSM_ERR_INVALID_ARG, "r is null");
+    if (!i) return fail(MSSM_ERR_INVALID_ARG, "i is null");
+    if (!lam) return fail(MSSM_ERR_INVALID_ARG, "lam is null");
+    if (!y) return fail(MSSM_ERR_INVALID_ARG, "y is null");
+    if (!dy) return fail(MSSM_ERR_INVALID_ARG, "dy is null");
+    if (!dx) return fail(MSSM_ERR_INVALID_ARG, "dx is null");
+    if (!dr) return fail(MSSM_ERR_INVALID_ARG, "dr is null");
+    if (!di) return fail(MSSM_ERR_INVALID_ARG, "di is null");
+    const Range ins[] = {range("x", x, z.act_bytes), range("r", r, z.act_bytes),
+                         range("i", i, z.act_bytes), range("lam", lam, dims.dim * 4),
+                         range("h0", h0, z.rows * 4), range("y", y, z.act_bytes),
+                         range("dy", dy, z.act_bytes), range("dh_last", dh_last, z.rows * 4)};
+    if (mssm_status c = check_overlaps(ins, 8, outs, 5, nullptr, nullptr)) return c;
+    mssm::RecurrenceArgs a{};
+    a.x = x; a.r = r; a.i = i; a.lam = lam; a.scale = scale; a.h0 = h0;
+    a.y = const_cast<void *>(y); a.dy = dy; a.dh_last = dh_last;
+    a.dx = dx; a.dr = dr; a.di = di; a.dlam = dlam; a.dh0 = dh0;
+    a.batch = dims.batch; a.L = dims.seqlen; a.dim = dims.dim;
+    a.io = dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16;
+    if (!mssm::gated_recurrence_supported(a))
+        return fail(MSSM_ERR_UNSUPPORTED, "gated recurrence does not support this shape");
+    const hipError_t e = mssm::launch_gated_recurrence_bwd(a, st);
+    if (e != hipSuccess) return hip_fail(e, "gated-recurrence backward launch");
+    g_last_variant = MSSM_VARIANT_AUTO;
+    return MSSM_OK;
+}
+
+mssm_status mssm_gated_recurrence_update(float *state, const void *x, const void *r, const void *i,
+                                         const float *lam, float scale, void *y,
+                                         mssm_recurrence_dims dims, mssm_dtypes dtypes, void *stream) {
+    if (dims.batch > 0 && dims.dim > 0 && !state) {
+        g_last_error.clear();
+        return fail(MSSM_ERR_INVALID_ARG, "state is null");
+    }
+    dims.seqlen = 1;
+    return mssm_gated_recurrence_fwd(x, r, i, lam, scale, state, y, state, dims, dtypes, stream);
+}
+
+mssm_status mssm_linear_cross_entropy_fwd(const void *hidden, const void *weight,
+                                          const int64_t *targets, int64_t ignore_index, float *loss,
+                                          float *lse, mssm_loss_dims dims, mssm_dtypes dtypes,
+                                          void *stream) {
+    g_last_error.clear();
+    LossSizes z;
+    if (mssm_status s = check_loss(dims, dtypes, &z)) return s;
+    if (dims.tokens == 0) {
+        g_last_variant = MSSM_VARIANT_AUTO;
+        return MSSM_OK;
+    }
+    if (!hidden) return fail(MSSM_ERR_INVALID_ARG, "hidden is null");
+    if (!weight) return fail(MSSM_ERR_INVALID_ARG, "weight is null");
+    if (!targets) return fail(MSSM_ERR_INVALID_ARG, "targets is null");
+    if (!loss) return fail(MSSM_ERR_INVALID_ARG, "loss is null");
+    const Range ins[] = {range("hidden", hidden, z.hidden_bytes), range("weight", weight, z.weight_bytes),
+                         range("targets", targets, dims.tokens * 8)};
+    const Range outs[] = {range("loss", loss, dims.tokens * 4), range("lse", lse, dims.tokens * 4)};
+    if (mssm_status c = check_overlaps(ins, 3, outs, 2, nullptr, nullptr)) return c;
+    mssm::LossArgs a{hidden, weight, targets, ignore_index, loss, lse, nullptr, nullptr, nullptr,
+                     dims.tokens, dims.dim, dims.vocab,
+                     dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16};
+    const hipError_t e = mssm::launch_linear_cross_entropy_fwd(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "cross-entropy launch");
+    g_last_variant = MSSM_VARIANT_AUTO;
+    return MSSM_OK;
+}
+
+mssm_status mssm_linear_cross_entropy_bwd(const void *hidden, const void *weight,
+                                          const int64_t *targets, int64_t ignore_index,
+                                          const float *lse, const float *dloss, void *dhidden,
+                                          void *dweight, mssm_loss_dims dims, mssm_dtypes dtypes,
+                                          void *stream) {
+    g_last_error.clear();
+    LossSizes z;
+    if (mssm_status s = check_loss(dims, dtypes, &z)) return s;
+    if (!dweight) return fail(MSSM_ERR_INVALID_ARG, "dweight is null");
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (dims.tokens == 0) {
+        // zero bits are zeros in either dtype; a bf16 buffer may start and
+        // end inside a 4-byte word
+        const hipError_t e = zero_fill_bytes(dweight, z.weight_bytes, st);
+        if (e != hipSuccess) return hip_fail(e, "zero-fill of dweight");
+        g_last_variant = MSSM_VARIANT_AUTO;
+        return MSSM_OK;
+    }
+    if (!hidden) return fail(MSSM_ERR_INVALID_ARG, "hidden is null");
+    if (!weight) return fail(MSSM_ERR_INVALID_ARG, "weight is null");
+    if (!targets) return fail(MSSM_ERR_INVALID_ARG, "targets is null");
+    if (!lse) return fail(MSSM_ERR_INVALID_ARG, "lse is null");
+    if (!dloss) return fail(MSSM_ERR_INVALID_ARG, "dloss is null");
+    if (!dhidden) return fail(MSSM_ERR_INVALID_ARG, "dhidden is null");
+    const Range ins[] = {range("hidden", hidden, z.hidden_bytes), range("weight", weight, z.weight_bytes),
+                         range("targets", targets, dims.tokens * 8), range("lse", lse, dims.tokens * 4),
+                         range("dloss", dloss, dims.tokens * 4)};
+    const Range outs[] = {range("dhidden", dhidden, z.hidden_bytes),
+                          range("dweight", dweight, z.weight_bytes)};
+    if (mssm_status c = check_overlaps(ins, 5, outs, 2, nullptr, nullptr)) return c;
+    mssm::LossArgs a{hidden, weight, targets, ignore_index, nullptr, const_cast<float *>(lse), dloss,
+                     dhidden, dweight, dims.tokens, dims.dim, dims.vocab,
+                     dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16};
+    const hipError_t e = mssm::launch_linear_cross_entropy_bwd(a, st);
+    if (e != hipSuccess) return hip_fail(e, "cross-entropy backward launch");
     g_last_variant = MSSM_VARIANT_AUTO;
     return MSSM_OK;
 }
