@@ -371,6 +371,18 @@ MSSM_API mssm_status mssm_selective_state_update(float *state, const void *x,
                                         mssm_step_dims dims, mssm_dtypes dtypes,
                                         void *stream);
 
+/*
+ * Workspaces.  The calls below that need scratch take it from the caller:
+ * `workspace` is a device buffer of at least `workspace_bytes` bytes, as the
+ * matching _workspace query says, 256-byte aligned, that overlaps no operand
+ * and may be reused once the call's work on the stream has finished.  A call
+ * then allocates nothing, so it may be captured into a HIP graph.  With
+ * workspace NULL the call takes its scratch stream-ordered from the library's
+ * pool.  Queries return the bytes (0: none needed), or -1 for sizes or dtypes
+ * that the call would refuse (mssm_last_error() says why); they need no GPU.
+ * A workspace that is too small or misaligned is MSSM_ERR_INVALID_ARG.
+ */
+
 /* Sizes of a layer norm: `rows` independent rows of `dim` values. */
 typedef struct {
     int64_t rows;    /* >= 0 */
@@ -417,15 +429,16 @@ MSSM_API mssm_status mssm_layer_norm_fwd(const void *x, const float *weight,
  *   dx          (rows, dim), dtype `io`    required (output)
  *   dweight, dbias  (dim) float32          nullable (outputs)
  * dweight and dbias are summed in an order that depends on the sizes alone
- * (repeatable bit for bit), through stream-ordered scratch of at most
- * 8 * 1024 * dim bytes.  rows == 0 zero-fills dweight and dbias.  Errors as
- * for the forward.
+ * (repeatable bit for bit), through partial sums in the workspace.
+ * rows == 0 zero-fills dweight and dbias.  Errors as for the forward.
  */
 MSSM_API mssm_status mssm_layer_norm_bwd(const void *dy, const void *x,
                                 const float *mean, const float *rstd,
                                 const float *weight, void *dx, float *dweight,
-                                float *dbias, mssm_norm_dims dims,
+                                float *dbias, void *workspace,
+                                int64_t workspace_bytes, mssm_norm_dims dims,
                                 mssm_dtypes dtypes, void *stream);
+MSSM_API int64_t mssm_layer_norm_bwd_workspace(mssm_norm_dims dims, mssm_dtypes dtypes);
 
 /* Sizes of a gated linear recurrence. */
 typedef struct {
@@ -454,18 +467,23 @@ typedef struct {
  *   y        (batch, L, dim), dtype `io`   required (output)
  *   h_last   (batch, dim) float32          nullable (output)
  * Long sequences are cut into segments whose carries pass between workgroups
- * in a fixed association: results are repeatable bit for bit.  Scratch for
- * the carries is stream-ordered.
+ * in a fixed association (through the workspace): results are repeatable bit
+ * for bit.
  * Errors as for mssm_selective_scan_fwd; also MSSM_ERR_INVALID_ARG for a scale
- * that is negative or not finite, MSSM_ERR_UNSUPPORTED when one of the sizes
- * reaches 2^31.  batch == 0 or dim == 0: nothing to do, MSSM_OK.  L == 0:
+ * that is negative or not finite, MSSM_ERR_UNSUPPORTED for dim >= 2^21, for
+ * another size or batch * dim >= 2^31, or where the sequences' segments of
+ * 128 steps by 32 channels reach 2^30.  batch == 0 or dim == 0: nothing to do, MSSM_OK.  L == 0:
  * h_last receives h0 (or zeros), y is empty.
  */
 MSSM_API mssm_status mssm_gated_recurrence_fwd(const void *x, const void *r,
                                 const void *i, const float *lam, float scale,
                                 const float *h0, void *y, float *h_last,
+                                void *workspace, int64_t workspace_bytes,
                                 mssm_recurrence_dims dims, mssm_dtypes dtypes,
                                 void *stream);
+/* For the forward (backward == 0) or the backward. */
+MSSM_API int64_t mssm_gated_recurrence_workspace(mssm_recurrence_dims dims,
+                                mssm_dtypes dtypes, int backward);
 
 /*
  * Backward of the gated linear recurrence, given its inputs, its output y
@@ -485,9 +503,8 @@ MSSM_API mssm_status mssm_gated_recurrence_fwd(const void *x, const void *r,
  *   dx, dr, di  (batch, L, dim), dtype `io`   required (outputs)
  *   dlam        (dim) float32                 nullable (output)
  *   dh0         (batch, dim) float32          nullable (output)
- * dlam is summed in a fixed order (repeatable bit for bit).  Scratch (the
- * carries and dlam's partial sums) is stream-ordered.  L == 0: dlam is zero,
- * dh0 = dh_last.  Errors as for the forward; no output may overlap an input
+ * dlam is summed in a fixed order (repeatable bit for bit), through partial
+ * sums in the workspace.  L == 0: dlam is zero, dh0 = dh_last.  Errors as for the forward; no output may overlap an input
  * or another output.
  */
 MSSM_API mssm_status mssm_gated_recurrence_bwd(const void *x, const void *r,
@@ -495,6 +512,7 @@ MSSM_API mssm_status mssm_gated_recurrence_bwd(const void *x, const void *r,
                                 const float *h0, const void *y, const void *dy,
                                 const float *dh_last, void *dx, void *dr,
                                 void *di, float *dlam, float *dh0,
+                                void *workspace, int64_t workspace_bytes,
                                 mssm_recurrence_dims dims, mssm_dtypes dtypes,
                                 void *stream);
 
@@ -541,16 +559,22 @@ typedef struct {
  *                                          backward)
  * Logits are float32 sums of exact products (bf16) or float32 products.
  * Errors: as for mssm_layer_norm_fwd; also MSSM_ERR_INVALID_ARG for dim < 1 or
- * vocab < 1, MSSM_ERR_UNSUPPORTED for tokens or vocab >= 2^30 or dim >= 2^24.
- * tokens == 0: nothing to do, MSSM_OK.  Scratch is stream-ordered: the pieces'
- * maxima and sums and, where dim or an address is not 16-byte aligned,
- * aligned copies of hidden and weight.
+ * vocab < 1, MSSM_ERR_UNSUPPORTED for tokens >= 2^20, vocab >= 2^30 or
+ * dim >= 2^20.  tokens == 0: nothing to do, MSSM_OK.  The workspace holds the
+ * pieces' maxima and sums and, where a row of dim values is not a multiple of
+ * 16 bytes or an address is not 16-byte aligned, an aligned copy of hidden and
+ * of a piece of weight.
  */
 MSSM_API mssm_status mssm_linear_cross_entropy_fwd(const void *hidden,
                                 const void *weight, const int64_t *targets,
                                 int64_t ignore_index, float *loss, float *lse,
+                                void *workspace, int64_t workspace_bytes,
                                 mssm_loss_dims dims, mssm_dtypes dtypes,
                                 void *stream);
+/* For the forward (backward == 0) or the backward; `aligned`: nonzero when
+ * hidden and weight start on 16-byte boundaries. */
+MSSM_API int64_t mssm_linear_cross_entropy_workspace(mssm_loss_dims dims,
+                                mssm_dtypes dtypes, int backward, int aligned);
 
 /*
  * Backward of the projected cross entropy.  With
@@ -568,15 +592,16 @@ MSSM_API mssm_status mssm_linear_cross_entropy_fwd(const void *hidden,
  * in dtype `io` for that piece only.  Sums are float32 in a fixed order
  * (repeatable bit for bit).  A target outside [0, vocab) that is not
  * ignore_index makes that token's dhidden and its terms of dweight NaN.
- * Scratch is stream-ordered; its size does not grow with the vocabulary
- * except for one copy of weight.  tokens == 0 zero-fills dweight.  Errors as
+ * The workspace does not grow with the vocabulary past one piece of it.
+ * tokens == 0 zero-fills dweight.  Errors as
  * for the forward.
  */
 MSSM_API mssm_status mssm_linear_cross_entropy_bwd(const void *hidden,
                                 const void *weight, const int64_t *targets,
                                 int64_t ignore_index, const float *lse,
                                 const float *dloss, void *dhidden,
-                                void *dweight, mssm_loss_dims dims,
+                                void *dweight, void *workspace,
+                                int64_t workspace_bytes, mssm_loss_dims dims,
                                 mssm_dtypes dtypes, void *stream);
 
 /* Force a kernel variant for subsequent calls made by THIS thread
@@ -606,6 +631,7 @@ MSSM_API const char *mssm_source_hash(void);
 
 /* Status bits that kernels set on a device while they run. */
 #define MSSM_DEVICE_LOOKBACK_TIMEOUT 0x1u /* a look-back wait gave up */
+#define MSSM_DEVICE_RECURRENCE_TIMEOUT 0x2u /* the same in the gated recurrence */
 
 /*
  * Device status of the CURRENT device.  Waits for all work queued on the
@@ -620,6 +646,8 @@ MSSM_API const char *mssm_source_hash(void);
  * before they wait, so this marks a defect, not a slow device; that call's
  * outputs from the affected segment on (y and h_last) are NaN rather than
  * wrong numbers, and the call itself returned MSSM_OK when it was queued.
+ * MSSM_DEVICE_RECURRENCE_TIMEOUT: the same for a segment of the gated linear
+ * recurrence or its backward.
  *
  * Errors: MSSM_ERR_INVALID_ARG if bits is NULL; MSSM_ERR_HIP if the
  * synchronisation or a copy fails (including a fault of earlier work).

@@ -32,7 +32,8 @@ VARIANT_PAIRSCAN = 6
 VARIANT_PAIRSCAN2 = 7
 
 MAX_DSTATE = 64
-DEVICE_LOOKBACK_TIMEOUT = 0x1   # mssm_device_status bit
+DEVICE_LOOKBACK_TIMEOUT = 0x1   # mssm_device_status bits
+DEVICE_RECURRENCE_TIMEOUT = 0x2
 NOALLOC_SCRATCH_BYTES = 8 << 20  # scratch array of the no-alloc entry point
 CONV_WIDTH = 4
 SSD_MAX_DSTATE = 256
@@ -61,6 +62,9 @@ EXPORTED = (
     "mssm_gated_recurrence_fwd",
     "mssm_gated_recurrence_bwd",
     "mssm_gated_recurrence_update",
+    "mssm_gated_recurrence_workspace",
+    "mssm_layer_norm_bwd_workspace",
+    "mssm_linear_cross_entropy_workspace",
     "mssm_linear_cross_entropy_fwd",
     "mssm_linear_cross_entropy_bwd",
 )
@@ -147,22 +151,30 @@ def _declare(L):
     f32, i64 = ctypes.c_float, ctypes.c_int64
     L.mssm_layer_norm_fwd.argtypes = [vp, fp, fp, f32, vp, fp, fp, NormDims, DTypes, vp]
     L.mssm_layer_norm_fwd.restype = ctypes.c_int
-    L.mssm_layer_norm_bwd.argtypes = [vp, vp, fp, fp, fp, vp, fp, fp, NormDims, DTypes, vp]
+    L.mssm_layer_norm_bwd.argtypes = [vp, vp, fp, fp, fp, vp, fp, fp, vp, i64, NormDims,
+                                      DTypes, vp]
     L.mssm_layer_norm_bwd.restype = ctypes.c_int
-    L.mssm_gated_recurrence_fwd.argtypes = [vp, vp, vp, fp, f32, fp, vp, fp, RecurrenceDims,
-                                            DTypes, vp]
+    L.mssm_gated_recurrence_fwd.argtypes = [vp, vp, vp, fp, f32, fp, vp, fp, vp, i64,
+                                            RecurrenceDims, DTypes, vp]
     L.mssm_gated_recurrence_fwd.restype = ctypes.c_int
     L.mssm_gated_recurrence_bwd.argtypes = [vp, vp, vp, fp, f32, fp, vp, vp, fp, vp, vp, vp, fp,
-                                            fp, RecurrenceDims, DTypes, vp]
+                                            fp, vp, i64, RecurrenceDims, DTypes, vp]
     L.mssm_gated_recurrence_bwd.restype = ctypes.c_int
     L.mssm_gated_recurrence_update.argtypes = [fp, vp, vp, vp, fp, f32, vp, RecurrenceDims,
                                                DTypes, vp]
     L.mssm_gated_recurrence_update.restype = ctypes.c_int
-    L.mssm_linear_cross_entropy_fwd.argtypes = [vp, vp, vp, i64, fp, fp, LossDims, DTypes, vp]
-    L.mssm_linear_cross_entropy_fwd.restype = ctypes.c_int
-    L.mssm_linear_cross_entropy_bwd.argtypes = [vp, vp, vp, i64, fp, fp, vp, vp, LossDims,
+    L.mssm_linear_cross_entropy_fwd.argtypes = [vp, vp, vp, i64, fp, fp, vp, i64, LossDims,
                                                 DTypes, vp]
+    L.mssm_linear_cross_entropy_fwd.restype = ctypes.c_int
+    L.mssm_linear_cross_entropy_bwd.argtypes = [vp, vp, vp, i64, fp, fp, vp, vp, vp, i64,
+                                                LossDims, DTypes, vp]
     L.mssm_linear_cross_entropy_bwd.restype = ctypes.c_int
+    L.mssm_layer_norm_bwd_workspace.argtypes = [NormDims, DTypes]
+    L.mssm_layer_norm_bwd_workspace.restype = i64
+    L.mssm_gated_recurrence_workspace.argtypes = [RecurrenceDims, DTypes, ctypes.c_int]
+    L.mssm_gated_recurrence_workspace.restype = i64
+    L.mssm_linear_cross_entropy_workspace.argtypes = [LossDims, DTypes, ctypes.c_int, ctypes.c_int]
+    L.mssm_linear_cross_entropy_workspace.restype = i64
     L.mssm_force_variant.argtypes = [ctypes.c_int]
     L.mssm_force_variant.restype = ctypes.c_int
     L.mssm_last_variant.argtypes = []

@@ -422,6 +422,18 @@ def _on_gpu(t):
     return t.device
 
 
+def _workspace(nbytes, dev):
+    """Scratch of a call from torch's allocator, whose blocks are 512-byte
+    aligned and stay with the stream (and the graph capture) they are
+    allocated on.  Returns (tensor or None, address or None, bytes)."""
+    if nbytes < 0:      # sizes the call itself refuses, with the reason
+        return None, None, 0
+    if nbytes == 0:
+        return None, None, 0
+    t = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+    return t, t.data_ptr(), nbytes
+
+
 def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
     """Layer norm over the last dimension on the GPU.
 
@@ -477,11 +489,12 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None):
     g = {"dx": torch.empty_like(x),
          "dweight": torch.empty((dim,), dtype=torch.float32, device=dev),
          "dbias": torch.empty((dim,), dtype=torch.float32, device=dev)}
+    dims, dt = _lib.NormDims(rows, dim), _lib.DTypes(io, _lib.MSSM_F32)
     with torch.cuda.device(dev):
+        ws, at, nbytes = _workspace(L.mssm_layer_norm_bwd_workspace(dims, dt), dev)
         st = L.mssm_layer_norm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
-                                   _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]),
-                                   _lib.NormDims(rows, dim), _lib.DTypes(io, _lib.MSSM_F32),
-                                   _stream_handle(dev))
+                                   _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]), at, nbytes,
+                                   dims, dt, _stream_handle(dev))
     _check(st)
     return g
 
@@ -530,11 +543,12 @@ def gated_recurrence_fwd(x, r, i, lam, scale=8.0, h0=None, return_last_state=Tru
     if return_last_state:
         h_last = h_out if h_out is not None else torch.empty(
             (batch, dim), dtype=torch.float32, device=dev)
+    dims, dt = _lib.RecurrenceDims(batch, seqlen, dim), _lib.DTypes(_io_dtype(x), _lib.MSSM_F32)
     with torch.cuda.device(dev):
+        ws, at, nbytes = _workspace(L.mssm_gated_recurrence_workspace(dims, dt, 0), dev)
         st = L.mssm_gated_recurrence_fwd(
             _ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(scale), _ptr(h0), _ptr(y), _ptr(h_last),
-            _lib.RecurrenceDims(batch, seqlen, dim), _lib.DTypes(_io_dtype(x), _lib.MSSM_F32),
-            _stream_handle(dev))
+            at, nbytes, dims, dt, _stream_handle(dev))
     _check(st)
     return y, h_last
 
@@ -558,12 +572,13 @@ def gated_recurrence_bwd(x, r, i, lam, y, dy, scale=8.0, h0=None, dh_last=None):
     g = {"dx": torch.empty_like(x), "dr": torch.empty_like(x), "di": torch.empty_like(x),
          "dlam": torch.empty((dim,), dtype=torch.float32, device=dev),
          "dh0": torch.empty((batch, dim), dtype=torch.float32, device=dev)}
+    dims, dt = _lib.RecurrenceDims(batch, seqlen, dim), _lib.DTypes(_io_dtype(x), _lib.MSSM_F32)
     with torch.cuda.device(dev):
+        ws, at, nbytes = _workspace(L.mssm_gated_recurrence_workspace(dims, dt, 1), dev)
         st = L.mssm_gated_recurrence_bwd(
             _ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(scale), _ptr(h0), _ptr(y), _ptr(dy),
             _ptr(dh_last), _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["di"]), _ptr(g["dlam"]),
-            _ptr(g["dh0"]), _lib.RecurrenceDims(batch, seqlen, dim),
-            _lib.DTypes(_io_dtype(x), _lib.MSSM_F32), _stream_handle(dev))
+            _ptr(g["dh0"]), at, nbytes, dims, dt, _stream_handle(dev))
     _check(st)
     return g
 
@@ -591,7 +606,8 @@ def gated_recurrence_update(state, x, r, i, lam, scale=8.0, out=None):
 
 
 def _loss_args(hidden, weight, targets):
-    """Shared checks of the projected cross entropy; returns (device, dims, dtypes)."""
+    """Shared checks of the projected cross entropy; returns (device, dims,
+    dtypes, whether both matrices start on 16-byte boundaries)."""
     dev = _on_gpu(hidden)
     io = _io_dtype(hidden)
     _need(hidden, "hidden")
@@ -604,7 +620,8 @@ def _loss_args(hidden, weight, targets):
         raise ValueError("hidden must be (tokens, dim) and weight (vocab, dim)")
     _need_shape(targets, "targets", (hidden.shape[0],))
     return (dev, _lib.LossDims(hidden.shape[0], hidden.shape[1], weight.shape[0]),
-            _lib.DTypes(io, _lib.MSSM_F32))
+            _lib.DTypes(io, _lib.MSSM_F32),
+            int((hidden.data_ptr() | weight.data_ptr()) % 16 == 0))
 
 
 def linear_cross_entropy_fwd(hidden, weight, targets, ignore_index=-100):
@@ -618,13 +635,14 @@ def linear_cross_entropy_fwd(hidden, weight, targets, ignore_index=-100):
     takes.
     """
     L = _lib.lib()
-    dev, dims, dt = _loss_args(hidden, weight, targets)
+    dev, dims, dt, on16 = _loss_args(hidden, weight, targets)
     loss = torch.empty((hidden.shape[0],), dtype=torch.float32, device=dev)
     lse = torch.empty((hidden.shape[0],), dtype=torch.float32, device=dev)
     with torch.cuda.device(dev):
+        ws, at, nbytes = _workspace(L.mssm_linear_cross_entropy_workspace(dims, dt, 0, on16), dev)
         st = L.mssm_linear_cross_entropy_fwd(_ptr(hidden), _ptr(weight), _ptr(targets),
-                                             int(ignore_index), _ptr(loss), _ptr(lse), dims, dt,
-                                             _stream_handle(dev))
+                                             int(ignore_index), _ptr(loss), _ptr(lse), at, nbytes,
+                                             dims, dt, _stream_handle(dev))
     _check(st)
     return loss, lse
 
@@ -634,7 +652,7 @@ def linear_cross_entropy_bwd(hidden, weight, targets, lse, dloss, ignore_index=-
     ((tokens,) float32) of the tokens' losses; lse is the forward's.  Returns
     a dict: dhidden like hidden, dweight like weight."""
     L = _lib.lib()
-    dev, dims, dt = _loss_args(hidden, weight, targets)
+    dev, dims, dt, on16 = _loss_args(hidden, weight, targets)
     for name, t in (("lse", lse), ("dloss", dloss)):
         if t is None:
             raise ValueError("%s is required" % name)
@@ -642,10 +660,11 @@ def linear_cross_entropy_bwd(hidden, weight, targets, lse, dloss, ignore_index=-
         _need_shape(t, name, (hidden.shape[0],))
     g = {"dhidden": torch.empty_like(hidden), "dweight": torch.empty_like(weight)}
     with torch.cuda.device(dev):
+        ws, at, nbytes = _workspace(L.mssm_linear_cross_entropy_workspace(dims, dt, 1, on16), dev)
         st = L.mssm_linear_cross_entropy_bwd(_ptr(hidden), _ptr(weight), _ptr(targets),
                                              int(ignore_index), _ptr(lse), _ptr(dloss),
-                                             _ptr(g["dhidden"]), _ptr(g["dweight"]), dims, dt,
-                                             _stream_handle(dev))
+                                             _ptr(g["dhidden"]), _ptr(g["dweight"]), at, nbytes,
+                                             dims, dt, _stream_handle(dev))
     _check(st)
     return g
 

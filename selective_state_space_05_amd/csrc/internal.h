@@ -183,7 +183,9 @@ struct NormArgs {
     IoType io;
 };
 hipError_t launch_layer_norm_fwd(const NormArgs &a, hipStream_t stream);
-hipError_t launch_layer_norm_bwd(const NormArgs &a, hipStream_t stream);
+// workspace: null to allocate from the pool; else at least the bytes said.
+hipError_t launch_layer_norm_bwd(const NormArgs &a, void *workspace, hipStream_t stream);
+size_t layer_norm_bwd_workspace(const NormArgs &a);
 
 // One gated linear recurrence, already validated: activations (batch, L, dim),
 // states (batch, dim), lam (dim).  h0 may be the same buffer as h_last.
@@ -207,8 +209,11 @@ struct RecurrenceArgs {
     IoType io;
 };
 bool gated_recurrence_supported(const RecurrenceArgs &a);
-hipError_t launch_gated_recurrence_fwd(const RecurrenceArgs &a, hipStream_t stream);
-hipError_t launch_gated_recurrence_bwd(const RecurrenceArgs &a, hipStream_t stream);
+size_t gated_recurrence_workspace(const RecurrenceArgs &a, bool bwd);
+hipError_t launch_gated_recurrence_fwd(const RecurrenceArgs &a, void *workspace, hipStream_t stream);
+hipError_t launch_gated_recurrence_bwd(const RecurrenceArgs &a, void *workspace, hipStream_t stream);
+// Its kernels' status bits, as device_status.
+hipError_t recurrence_status(uint32_t *bits, bool clear);
 
 // One cross entropy over a vocabulary projection, already validated: hidden,
 // dhidden (tokens, dim); weight, dweight (vocab, dim); the rest (tokens).
@@ -225,8 +230,10 @@ struct LossArgs {
     int64_t tokens, dim, vocab;
     IoType io;
 };
-hipError_t launch_linear_cross_entropy_fwd(const LossArgs &a, hipStream_t stream);
-hipError_t launch_linear_cross_entropy_bwd(const LossArgs &a, hipStream_t stream);
+// aligned: hidden and weight start on 16-byte boundaries.
+size_t linear_cross_entropy_workspace(const LossArgs &a, bool bwd, bool aligned);
+hipError_t launch_linear_cross_entropy_fwd(const LossArgs &a, void *workspace, hipStream_t stream);
+hipError_t launch_linear_cross_entropy_bwd(const LossArgs &a, void *workspace, hipStream_t stream);
 
 hipError_t launch_ssd_recurrent(const SSDArgs &a, hipStream_t stream);
 bool ssd_recurrent_supported(const SSDArgs &a);

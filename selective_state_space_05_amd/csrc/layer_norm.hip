@@ -122,17 +122,19 @@ hipError_t fwd(const NormArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+int64_t slices_of(const NormArgs &a) { return a.rows < 64 ? a.rows : 64; }
+
 template <typename T>
-hipError_t bwd(const NormArgs &a, hipStream_t stream) {
+hipError_t bwd(const NormArgs &a, void *workspace, hipStream_t stream) {
     const int dim = static_cast<int>(a.dim);
     hipLaunchKernelGGL(norm_bwd_dx_kernel<T>, dim3(static_cast<uint32_t>(a.rows)), dim3(kThreads), 0, stream,
                        static_cast<const T *>(a.dy), static_cast<const T *>(a.x), a.mean, a.rstd, a.weight,
                        static_cast<T *>(a.dx), dim);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!a.dweight && !a.dbias)) return e;
-    const int slices = static_cast<int>(a.rows < 64 ? a.rows : 64);
-    void *part = nullptr;
-    e = scratch_alloc(&part, static_cast<size_t>(slices) * 2 * dim * sizeof(float), stream);
+    const int slices = static_cast<int>(slices_of(a));
+    void *part = workspace;
+    if (!part) e = scratch_alloc(&part, layer_norm_bwd_workspace(a), stream);
     if (e != hipSuccess) return e;
     const uint32_t cols = static_cast<uint32_t>((a.dim + kThreads - 1) / kThreads);
     hipLaunchKernelGGL(norm_bwd_part_kernel<T>, dim3(cols, slices), dim3(kThreads), 0, stream,
@@ -141,18 +143,23 @@ hipError_t bwd(const NormArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL(norm_bwd_sum_kernel, dim3(cols), dim3(kThreads), 0, stream,
                        static_cast<const float *>(part), slices, a.dweight, a.dbias, dim);
     e = hipGetLastError();
-    const hipError_t f = scratch_free(part, stream);
-    return e != hipSuccess ? e : f;
+    if (!workspace) {
+        const hipError_t f = scratch_free(part, stream);
+        if (e == hipSuccess) e = f;
+    }
+    return e;
 }
 
 }  // namespace
+
+size_t layer_norm_bwd_workspace(const NormArgs &a) { return static_cast<size_t>(slices_of(a)) * 2 * a.dim * sizeof(float); }
 
 hipError_t launch_layer_norm_fwd(const NormArgs &a, hipStream_t stream) {
     return a.io == IO_F32 ? fwd<float>(a, stream) : fwd<uint16_t>(a, stream);
 }
 
-hipError_t launch_layer_norm_bwd(const NormArgs &a, hipStream_t stream) {
-    return a.io == IO_F32 ? bwd<float>(a, stream) : bwd<uint16_t>(a, stream);
+hipError_t launch_layer_norm_bwd(const NormArgs &a, void *workspace, hipStream_t stream) {
+    return a.io == IO_F32 ? bwd<float>(a, workspace, stream) : bwd<uint16_t>(a, workspace, stream);
 }
 
 }  // namespace mssm

@@ -174,13 +174,38 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const float2 *__restrict
     loss[t] = target == ignore ? 0.0f : (target < 0 || target >= vocab) ? NAN : l - loss[t];
 }
 
-// ---- backward: p of a piece, in both layouts
+// ---- backward ----------------------------------------------------------------------
+
+// The largest finite |dloss| of the tokens that have a loss (1 if there is
+// none): p is held relative to it.  The gradient of a mean is the same for
+// every token and rarely a bfloat16; divided by this it is 1, so that holding
+// p - 1 of a target's word costs p, not a rounding of dloss.
+__global__ __launch_bounds__(1024) void grad_scale_kernel(const float *__restrict__ dloss,
+                                                          const int64_t *__restrict__ targets, int64_t ignore,
+                                                          int tokens, float *__restrict__ scale) {
+    __shared__ float sh[16];
+    float m = 0.0f;
+    for (int t = threadIdx.x; t < tokens; t += 1024) {
+        const float g = fabsf(dloss[t]);
+        if (targets[t] != ignore && g < INFINITY) m = fmaxf(m, g);
+    }
+#pragma unroll
+    for (int k = 32; k >= 1; k /= 2) m = fmaxf(m, __shfl_xor(m, k));
+    if (threadIdx.x % 64 == 0) sh[threadIdx.x / 64] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < 16; ++k) m = fmaxf(m, sh[k]);
+        *scale = m > 0.0f ? m : 1.0f;
+    }
+}
+
+// p of a piece, in both layouts
 template <typename T>
 struct ProbTile {
     T *p, *pt;                 // p[token][word] and pt[word][token]
     int64_t ldp, ldpt;         // elements
     const int64_t *targets;
-    const float *lse, *dloss;
+    const float *lse, *dloss, *scale;
     int64_t ignore, vocab;
     int tokens, words, word0;
     __device__ void column(int m, int t, int lane, const f32x16 *acc) const {
@@ -188,7 +213,7 @@ struct ProbTile {
         const int64_t target = t < tokens ? targets[t] : ignore;
         const bool live = target != ignore;
         const float ref = live ? lse[t] : 0.0f;
-        float g = live ? dloss[t] : 0.0f;
+        float g = live ? dloss[t] / *scale : 0.0f;
         if (live && (target < 0 || target >= vocab)) g = NAN;
 #pragma unroll
         for (int i = 0; i < kWM / 32; ++i)
@@ -212,6 +237,7 @@ template <typename T>
 struct GradTile {
     float *sum;                // float32 accumulator, or null
     T *out;                    // output, or null
+    const float *scale;        // the output is the sum times this
     int64_t ld;
     int rows, cols;            // of the output
     bool add;                  // sum holds earlier pieces
@@ -226,7 +252,7 @@ struct GradTile {
                 float v = acc[i * (kWN / 32)][e];
                 const int64_t at = n * ld + d;
                 if (add) v += sum[at];
-                if (out) Io<T>::store(out, at, v);
+                if (out) Io<T>::store(out, at, v * *scale);
                 else sum[at] = v;
             }
     }
@@ -270,9 +296,8 @@ __global__ __launch_bounds__(256) void transpose_kernel(const T *__restrict__ in
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t ceil_div(int64_t n, int64_t by) { return (n + by - 1) / by; }
 
-template <typename T>
-bool aligned(const void *p, int64_t dim) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && dim * sizeof(T) % 16 == 0;
+bool on_16(const LossArgs &a) {
+    return ((reinterpret_cast<uintptr_t>(a.hidden) | reinterpret_cast<uintptr_t>(a.weight)) & 15u) == 0;
 }
 
 template <typename T, typename Epilogue>
@@ -303,138 +328,155 @@ hipError_t transpose(const T *in, T *out, int64_t rows, int64_t cols, int64_t ld
 
 // Words of the vocabulary in one piece: p of the piece has at most 2^27
 // elements, and a piece at least 1024 words.
-int64_t piece_words(int64_t tokens, int64_t vocab) {
-    int64_t n = (int64_t(1) << 27) / (tokens < 1 ? 1 : tokens) / 1024 * 1024;
+int64_t piece_words(int64_t rows, int64_t vocab) {
+    int64_t n = (int64_t(1) << 27) / (rows < 1 ? 1 : rows) / 1024 * 1024;
     if (n < 1024) n = 1024;
     return n < vocab ? n : vocab;
 }
 
-// Scratch of one call, cut from one allocation.
-struct Scratch {
-    size_t size = 0;
-    unsigned char *base = nullptr;
-    size_t add(size_t bytes) {
-        const size_t at = size;
-        size += (bytes + 255) / 256 * 256;
-        return at;
-    }
+// Sizes of a call and its workspace, cut into 256-byte aligned arrays.
+struct Plan {
+    bool copy;                 // rows of hidden and weight are copied to aligned ones
+    int64_t dimp, tokp;        // padded row lengths (elements)
+    int64_t piece, piecep;     // words of a piece
+    int64_t parts;
+    size_t at_part, at_h, at_w, at_ht, at_wt, at_p, at_pt, at_sum, at_scale, bytes;
 };
 
-template <typename T>
-hipError_t fwd(const LossArgs &a, hipStream_t stream) {
-    const int64_t dimp = round_up(a.dim, 16 / sizeof(T));
-    const bool copy_h = !aligned<T>(a.hidden, a.dim), copy_w = !aligned<T>(a.weight, a.dim);
-    const int64_t piece = copy_w ? piece_words(dimp, a.vocab) : a.vocab;
-    const int64_t parts = ceil_div(a.vocab, piece) * ceil_div(piece, kWM);
-    Scratch s;
-    const size_t at_part = s.add(static_cast<size_t>(parts) * a.tokens * sizeof(float2));
-    const size_t at_h = s.add(copy_h ? static_cast<size_t>(a.tokens) * dimp * sizeof(T) : 0);
-    const size_t at_w = s.add(copy_w ? static_cast<size_t>(piece) * dimp * sizeof(T) : 0);
-    void *mem = nullptr;
-    hipError_t e = scratch_alloc(&mem, s.size, stream);
-    if (e != hipSuccess) return e;
-    unsigned char *base = static_cast<unsigned char *>(mem);
-    float2 *part = reinterpret_cast<float2 *>(base + at_part);
-    const T *h = static_cast<const T *>(a.hidden);
-    if (copy_h) {
-        e = align_rows(h, reinterpret_cast<T *>(base + at_h), a.tokens, a.dim, dimp, stream);
-        h = reinterpret_cast<const T *>(base + at_h);
+Plan make_plan(const LossArgs &a, bool bwd, bool aligned) {
+    Plan p{};
+    const int64_t esz = a.io == IO_F32 ? 4 : 2, unit = 16 / esz;
+    p.copy = !aligned || a.dim % unit != 0;
+    p.dimp = round_up(a.dim, unit);
+    p.tokp = round_up(a.tokens, unit);
+    const auto add = [&](int64_t bytes) {
+        const size_t at = p.bytes;
+        p.bytes += static_cast<size_t>(round_up(bytes, 256));
+        return at;
+    };
+    p.piece = piece_words(bwd || a.tokens > p.dimp ? a.tokens : p.dimp, a.vocab);
+    p.piecep = round_up(p.piece, unit);
+    if (p.copy) {
+        p.at_h = add(a.tokens * p.dimp * esz);
+        p.at_w = add(p.piece * p.dimp * esz);
     }
-    const Rows B{reinterpret_cast<const unsigned char *>(h), dimp * static_cast<int64_t>(sizeof(T)),
-                 static_cast<int>(a.tokens)};
-    int part0 = 0;
-    for (int64_t w0 = 0; w0 < a.vocab && e == hipSuccess; w0 += piece) {
-        const int64_t words = a.vocab - w0 < piece ? a.vocab - w0 : piece;
-        const T *w = static_cast<const T *>(a.weight) + w0 * a.dim;
-        if (copy_w) {
-            e = align_rows(w, reinterpret_cast<T *>(base + at_w), words, a.dim, dimp, stream);
-            w = reinterpret_cast<const T *>(base + at_w);
-            if (e != hipSuccess) break;
-        }
-        const Rows A{reinterpret_cast<const unsigned char *>(w), dimp * static_cast<int64_t>(sizeof(T)),
-                     static_cast<int>(words)};
-        const LossTile ep{part, a.loss, a.targets, static_cast<int>(a.tokens), static_cast<int>(words),
-                          static_cast<int>(w0), part0};
-        e = product<T>(A, B, dimp * sizeof(T), ep, stream);
-        part0 += static_cast<int>(ceil_div(words, kWM));
+    if (!bwd) {
+        p.parts = a.vocab / p.piece * ceil_div(p.piece, kWM) + ceil_div(a.vocab % p.piece, kWM);
+        p.at_part = add(p.parts * a.tokens * 8);
+        return p;
     }
-    if (e == hipSuccess) {
-        hipLaunchKernelGGL(loss_join_kernel, dim3(static_cast<uint32_t>(ceil_div(a.tokens, 256))), dim3(256), 0,
-                           stream, part, part0, static_cast<int>(a.tokens), a.targets, a.ignore_index, a.vocab,
-                           a.loss, a.lse);
-        e = hipGetLastError();
-    }
-    const hipError_t f = scratch_free(mem, stream);
-    return e != hipSuccess ? e : f;
+    p.at_ht = add(a.dim * p.tokp * esz);
+    p.at_wt = add(a.dim * p.piecep * esz);
+    p.at_p = add(a.tokens * p.piecep * esz);
+    p.at_pt = add(p.piece * p.tokp * esz);
+    p.at_scale = add(4);
+    if (p.piece < a.vocab) p.at_sum = add(a.tokens * a.dim * 4);
+    return p;
 }
 
 template <typename T>
-hipError_t bwd(const LossArgs &a, hipStream_t stream) {
-    constexpr int64_t kUnit = 16 / sizeof(T);
-    const int64_t dimp = round_up(a.dim, kUnit), tokp = round_up(a.tokens, kUnit);
-    const int64_t piece = piece_words(a.tokens, a.vocab), piecep = round_up(piece, kUnit);
-    const bool copy_h = !aligned<T>(a.hidden, a.dim), copy_w = !aligned<T>(a.weight, a.dim);
-    const bool pieces = piece < a.vocab;
-    Scratch s;
-    const size_t at_h = s.add(copy_h ? static_cast<size_t>(a.tokens) * dimp * sizeof(T) : 0);
-    const size_t at_w = s.add(copy_w ? static_cast<size_t>(piece) * dimp * sizeof(T) : 0);
-    const size_t at_ht = s.add(static_cast<size_t>(a.dim) * tokp * sizeof(T));
-    const size_t at_wt = s.add(static_cast<size_t>(a.dim) * piecep * sizeof(T));
-    const size_t at_p = s.add(static_cast<size_t>(a.tokens) * piecep * sizeof(T));
-    const size_t at_pt = s.add(static_cast<size_t>(piece) * tokp * sizeof(T));
-    const size_t at_sum = s.add(pieces ? static_cast<size_t>(a.tokens) * a.dim * sizeof(float) : 0);
-    void *mem = nullptr;
-    hipError_t e = scratch_alloc(&mem, s.size, stream);
-    if (e != hipSuccess) return e;
-    unsigned char *base = static_cast<unsigned char *>(mem);
-    T *p = reinterpret_cast<T *>(base + at_p), *pt = reinterpret_cast<T *>(base + at_pt);
-    T *ht = reinterpret_cast<T *>(base + at_ht), *wt = reinterpret_cast<T *>(base + at_wt);
+Rows rows_of(const T *q, int64_t ld, int64_t n) {
+    return Rows{reinterpret_cast<const unsigned char *>(q), ld * static_cast<int64_t>(sizeof(T)), static_cast<int>(n)};
+}
+
+template <typename T>
+hipError_t fwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_t stream) {
+    float2 *part = reinterpret_cast<float2 *>(base + p.at_part);
     const T *h = static_cast<const T *>(a.hidden);
-    const int tokens = static_cast<int>(a.tokens), dim = static_cast<int>(a.dim);
-    auto rows = [](const T *q, int64_t ld, int64_t n) {
-        return Rows{reinterpret_cast<const unsigned char *>(q), ld * static_cast<int64_t>(sizeof(T)),
-                    static_cast<int>(n)};
-    };
-    e = transpose(h, ht, a.tokens, a.dim, tokp, a.targets, a.ignore_index, stream);
-    if (e == hipSuccess && copy_h) {
-        e = align_rows(h, reinterpret_cast<T *>(base + at_h), a.tokens, a.dim, dimp, stream);
-        h = reinterpret_cast<const T *>(base + at_h);
+    hipError_t e = hipSuccess;
+    if (p.copy) {
+        e = align_rows(h, reinterpret_cast<T *>(base + p.at_h), a.tokens, a.dim, p.dimp, stream);
+        h = reinterpret_cast<const T *>(base + p.at_h);
     }
-    for (int64_t w0 = 0; w0 < a.vocab && e == hipSuccess; w0 += piece) {
-        const int64_t words = a.vocab - w0 < piece ? a.vocab - w0 : piece, wordsp = round_up(words, kUnit);
+    int part0 = 0;
+    for (int64_t w0 = 0; w0 < a.vocab && e == hipSuccess; w0 += p.piece) {
+        const int64_t words = a.vocab - w0 < p.piece ? a.vocab - w0 : p.piece;
         const T *w = static_cast<const T *>(a.weight) + w0 * a.dim;
-        e = transpose<T>(w, wt, words, a.dim, wordsp, nullptr, 0, stream);
-        if (e != hipSuccess) break;
-        if (copy_w) {
-            e = align_rows(w, reinterpret_cast<T *>(base + at_w), words, a.dim, dimp, stream);
-            w = reinterpret_cast<const T *>(base + at_w);
+        if (p.copy) {
+            e = align_rows(w, reinterpret_cast<T *>(base + p.at_w), words, a.dim, p.dimp, stream);
+            w = reinterpret_cast<const T *>(base + p.at_w);
             if (e != hipSuccess) break;
         }
-        const ProbTile<T> prob{p, pt, wordsp, tokp, a.targets, a.lse, a.dloss, a.ignore_index, a.vocab,
-                               tokens, static_cast<int>(words), static_cast<int>(w0)};
-        e = product<T>(rows(w, dimp, words), rows(h, dimp, a.tokens), dimp * sizeof(T), prob, stream);
-        if (e != hipSuccess) break;
-        float *sum = pieces ? reinterpret_cast<float *>(base + at_sum) : nullptr;
-        const GradTile<T> dh{sum, w0 + words >= a.vocab ? static_cast<T *>(a.dhidden) : nullptr, a.dim, tokens,
-                             dim, w0 > 0};
-        e = product<T>(rows(wt, wordsp, a.dim), rows(p, wordsp, a.tokens), wordsp * sizeof(T), dh, stream);
-        if (e != hipSuccess) break;
-        const GradTile<T> dw{nullptr, static_cast<T *>(a.dweight) + w0 * a.dim, a.dim, static_cast<int>(words),
-                             dim, false};
-        e = product<T>(rows(ht, tokp, a.dim), rows(pt, tokp, words), tokp * sizeof(T), dw, stream);
+        const LossTile ep{part, a.loss, a.targets, static_cast<int>(a.tokens), static_cast<int>(words),
+                          static_cast<int>(w0), part0};
+        e = product<T>(rows_of(w, p.dimp, words), rows_of(h, p.dimp, a.tokens), p.dimp * sizeof(T), ep, stream);
+        part0 += static_cast<int>(ceil_div(words, kWM));
     }
-    const hipError_t f = scratch_free(mem, stream);
-    return e != hipSuccess ? e : f;
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(loss_join_kernel, dim3(static_cast<uint32_t>(ceil_div(a.tokens, 256))), dim3(256), 0, stream,
+                       part, part0, static_cast<int>(a.tokens), a.targets, a.ignore_index, a.vocab, a.loss, a.lse);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t bwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_t stream) {
+    T *pr = reinterpret_cast<T *>(base + p.at_p), *pt = reinterpret_cast<T *>(base + p.at_pt);
+    T *ht = reinterpret_cast<T *>(base + p.at_ht), *wt = reinterpret_cast<T *>(base + p.at_wt);
+    float *scale = reinterpret_cast<float *>(base + p.at_scale);
+    const T *h = static_cast<const T *>(a.hidden);
+    const int tokens = static_cast<int>(a.tokens), dim = static_cast<int>(a.dim);
+    hipLaunchKernelGGL(grad_scale_kernel, dim3(1), dim3(1024), 0, stream, a.dloss, a.targets, a.ignore_index, tokens,
+                       scale);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess) e = transpose(h, ht, a.tokens, a.dim, p.tokp, a.targets, a.ignore_index, stream);
+    if (e == hipSuccess && p.copy) {
+        e = align_rows(h, reinterpret_cast<T *>(base + p.at_h), a.tokens, a.dim, p.dimp, stream);
+        h = reinterpret_cast<const T *>(base + p.at_h);
+    }
+    for (int64_t w0 = 0; w0 < a.vocab && e == hipSuccess; w0 += p.piece) {
+        const int64_t words = a.vocab - w0 < p.piece ? a.vocab - w0 : p.piece;
+        const int64_t wordsp = round_up(words, 16 / sizeof(T));
+        const T *w = static_cast<const T *>(a.weight) + w0 * a.dim;
+        e = transpose<T>(w, wt, words, a.dim, wordsp, nullptr, 0, stream);
+        if (e == hipSuccess && p.copy) {
+            e = align_rows(w, reinterpret_cast<T *>(base + p.at_w), words, a.dim, p.dimp, stream);
+            w = reinterpret_cast<const T *>(base + p.at_w);
+        }
+        if (e != hipSuccess) break;
+        const ProbTile<T> prob{pr, pt, wordsp, p.tokp, a.targets, a.lse, a.dloss, scale, a.ignore_index, a.vocab,
+                               tokens, static_cast<int>(words), static_cast<int>(w0)};
+        e = product<T>(rows_of(w, p.dimp, words), rows_of(h, p.dimp, a.tokens), p.dimp * sizeof(T), prob, stream);
+        if (e != hipSuccess) break;
+        float *sum = p.piece < a.vocab ? reinterpret_cast<float *>(base + p.at_sum) : nullptr;
+        const GradTile<T> dh{sum, w0 + words >= a.vocab ? static_cast<T *>(a.dhidden) : nullptr, scale, a.dim, tokens,
+                             dim, w0 > 0};
+        e = product<T>(rows_of(wt, wordsp, a.dim), rows_of(pr, wordsp, a.tokens), wordsp * sizeof(T), dh, stream);
+        if (e != hipSuccess) break;
+        const GradTile<T> dw{nullptr, static_cast<T *>(a.dweight) + w0 * a.dim, scale, a.dim, static_cast<int>(words),
+                             dim, false};
+        e = product<T>(rows_of(ht, p.tokp, a.dim), rows_of(pt, p.tokp, words), p.tokp * sizeof(T), dw, stream);
+    }
+    return e;
+}
+
+hipError_t launch(const LossArgs &a, bool backward, void *workspace, hipStream_t stream) {
+    const Plan p = make_plan(a, backward, on_16(a));
+    void *mem = workspace;
+    hipError_t e = hipSuccess;
+    if (!mem) e = scratch_alloc(&mem, p.bytes, stream);
+    if (e != hipSuccess) return e;
+    unsigned char *base = static_cast<unsigned char *>(mem);
+    if (a.io == IO_F32) e = backward ? bwd<float>(a, p, base, stream) : fwd<float>(a, p, base, stream);
+    else e = backward ? bwd<uint16_t>(a, p, base, stream) : fwd<uint16_t>(a, p, base, stream);
+    if (!workspace) {
+        const hipError_t f = scratch_free(mem, stream);
+        if (e == hipSuccess) e = f;
+    }
+    return e;
 }
 
 }  // namespace
 
-hipError_t launch_linear_cross_entropy_fwd(const LossArgs &a, hipStream_t stream) {
-    return a.io == IO_F32 ? fwd<float>(a, stream) : fwd<uint16_t>(a, stream);
+size_t linear_cross_entropy_workspace(const LossArgs &a, bool backward, bool aligned) {
+    return make_plan(a, backward, aligned).bytes;
 }
 
-hipError_t launch_linear_cross_entropy_bwd(const LossArgs &a, hipStream_t stream) {
-    return a.io == IO_F32 ? bwd<float>(a, stream) : bwd<uint16_t>(a, stream);
+hipError_t launch_linear_cross_entropy_fwd(const LossArgs &a, void *workspace, hipStream_t stream) {
+    return launch(a, false, workspace, stream);
+}
+
+hipError_t launch_linear_cross_entropy_bwd(const LossArgs &a, void *workspace, hipStream_t stream) {
+    return launch(a, true, workspace, stream);
 }
 
 }  // namespace mssm

@@ -344,6 +344,21 @@ mssm_status ssd_fwd(const void *x, const void *dt, const float *dt_bias, const f
     return MSSM_OK;
 }
 
+// A caller's workspace of `need` bytes (null: none given), as the range that
+// the overlap check takes.
+mssm_status check_workspace(const void *p, int64_t bytes, size_t need, Range *out) {
+    *out = range("workspace", p, static_cast<int64_t>(need));
+    if (!p) return MSSM_OK;
+    if (bytes < 0 || static_cast<size_t>(bytes) < need)
+        return fail(MSSM_ERR_INVALID_ARG, "workspace of %lld bytes is smaller than the %zu needed",
+                    (long long)bytes, need);
+    if (reinterpret_cast<uintptr_t>(p) % 256 != 0)
+        return fail(MSSM_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+    return MSSM_OK;
+}
+
+mssm::IoType io_type(mssm_dtypes dt) { return dt.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16; }
+
 // Sizes in bytes of a layer norm's operands, after the checks both passes share.
 struct NormSizes {
     int64_t act_bytes, dim_bytes, row_bytes;
@@ -408,6 +423,10 @@ mssm_status copy_or_zero_state(const char *out_name, float *out, const char *in_
     return MSSM_OK;
 }
 
+bool on_16(const void *p, const void *q) {
+    return ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
+}
+
 struct LossSizes {
     int64_t hidden_bytes, weight_bytes;
 };
@@ -419,12 +438,12 @@ mssm_status check_loss(mssm_loss_dims d, mssm_dtypes dtypes, LossSizes *z) {
     if (d.dim < 1 || d.vocab < 1)
         return fail(MSSM_ERR_INVALID_ARG, "dim and vocab must be >= 1, got %lld and %lld",
                     (long long)d.dim, (long long)d.vocab);
-    const int64_t lim = int64_t(1) << 30;
-    if (d.tokens >= lim || d.vocab >= lim || d.dim >= (int64_t(1) << 24))
+    const int64_t lim = int64_t(1) << 20;
+    if (d.tokens >= lim || d.vocab >= (int64_t(1) << 30) || d.dim >= lim)
         return fail(MSSM_ERR_UNSUPPORTED,
-                    "tokens %lld or vocab %lld reaches 2^30, or dim %lld reaches 2^24",
-                    (long long)d.tokens, (long long)d.vocab, (long long)d.dim);
-    const int64_t esz = dtypes.io == MSSM_F32 ? 4 : 2;   // at most 2^56 bytes
+                    "tokens %lld or dim %lld reaches 2^20, or vocab %lld reaches 2^30",
+                    (long long)d.tokens, (long long)d.dim, (long long)d.vocab);
+    const int64_t esz = dtypes.io == MSSM_F32 ? 4 : 2;   // at most 2^52 bytes
     z->hidden_bytes = d.tokens * d.dim * esz;
     z->weight_bytes = d.vocab * d.dim * esz;
     return MSSM_OK;
@@ -715,7 +734,7 @@ mssm_status mssm_layer_norm_fwd(const void *x, const float *weight, const float 
                           range("rstd", rstd, z.row_bytes)};
     if (mssm_status c = check_overlaps(ins, 3, outs, 3, nullptr, nullptr)) return c;
     mssm::NormArgs a{x, weight, bias, eps, y, mean, rstd, nullptr, nullptr, nullptr, nullptr,
-                     dims.rows, dims.dim, dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16};
+                     dims.rows, dims.dim, io_type(dtypes)};
     const hipError_t e = mssm::launch_layer_norm_fwd(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(e, "layer-norm launch");
     g_last_variant = MSSM_VARIANT_AUTO;
@@ -724,13 +743,18 @@ mssm_status mssm_layer_norm_fwd(const void *x, const float *weight, const float 
 
 mssm_status mssm_layer_norm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
                                 const float *weight, void *dx, float *dweight, float *dbias,
-                                mssm_norm_dims dims, mssm_dtypes dtypes, void *stream) {
+                                void *workspace, int64_t workspace_bytes, mssm_norm_dims dims,
+                                mssm_dtypes dtypes, void *stream) {
     g_last_error.clear();
     NormSizes z;
     if (mssm_status s = check_norm(dims, dtypes, &z)) return s;
     hipStream_t st = static_cast<hipStream_t>(stream);
+    mssm::NormArgs a{x, weight, nullptr, 0.0f, nullptr, const_cast<float *>(mean),
+                     const_cast<float *>(rstd), dy, dx, dweight, dbias, dims.rows, dims.dim, io_type(dtypes)};
+    Range ws;
+    if (mssm_status s = check_workspace(workspace, workspace_bytes, mssm::layer_norm_bwd_workspace(a), &ws)) return s;
     const Range outs[] = {range("dx", dx, z.act_bytes), range("dweight", dweight, z.dim_bytes),
-                          range("dbias", dbias, z.dim_bytes)};
+                          range("dbias", dbias, z.dim_bytes), ws};
     if (dims.rows == 0 || dims.dim == 0) {
         if (overlaps(outs[1], outs[2])) return fail(MSSM_ERR_INVALID_ARG, "dweight overlaps dbias");
         hipError_t e = hipSuccess;
@@ -748,11 +772,8 @@ mssm_status mssm_layer_norm_bwd(const void *dy, const void *x, const float *mean
     const Range ins[] = {range("dy", dy, z.act_bytes), range("x", x, z.act_bytes),
                          range("mean", mean, z.row_bytes), range("rstd", rstd, z.row_bytes),
                          range("weight", weight, z.dim_bytes)};
-    if (mssm_status c = check_overlaps(ins, 5, outs, 3, nullptr, nullptr)) return c;
-    mssm::NormArgs a{x, weight, nullptr, 0.0f, nullptr, const_cast<float *>(mean),
-                     const_cast<float *>(rstd), dy, dx, dweight, dbias, dims.rows, dims.dim,
-                     dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16};
-    const hipError_t e = mssm::launch_layer_norm_bwd(a, st);
+    if (mssm_status c = check_overlaps(ins, 5, outs, 4, nullptr, nullptr)) return c;
+    const hipError_t e = mssm::launch_layer_norm_bwd(a, workspace, st);
     if (e != hipSuccess) return hip_fail(e, "layer-norm backward launch");
     g_last_variant = MSSM_VARIANT_AUTO;
     return MSSM_OK;
@@ -760,6 +781,7 @@ mssm_status mssm_layer_norm_bwd(const void *dy, const void *x, const float *mean
 
 mssm_status mssm_gated_recurrence_fwd(const void *x, const void *r, const void *i, const float *lam,
                                       float scale, const float *h0, void *y, float *h_last,
+                                      void *workspace, int64_t workspace_bytes,
                                       mssm_recurrence_dims dims, mssm_dtypes dtypes, void *stream) {
     g_last_error.clear();
     RecurrenceSizes z;
@@ -778,15 +800,18 @@ mssm_status mssm_gated_recurrence_fwd(const void *x, const void *r, const void *
     const Range ins[] = {range("x", x, z.act_bytes), range("r", r, z.act_bytes),
                          range("i", i, z.act_bytes), range("lam", lam, dims.dim * 4),
                          range("h0", h0, z.rows * 4)};
-    const Range outs[] = {range("y", y, z.act_bytes), range("h_last", h_last, z.rows * 4)};
-    if (mssm_status c = check_overlaps(ins, 5, outs, 2, h0, h_last)) return c;
     mssm::RecurrenceArgs a{};
     a.x = x; a.r = r; a.i = i; a.lam = lam; a.scale = scale; a.h0 = h0; a.y = y; a.h_last = h_last;
     a.batch = dims.batch; a.L = dims.seqlen; a.dim = dims.dim;
-    a.io = dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16;
+    a.io = io_type(dtypes);
     if (!mssm::gated_recurrence_supported(a))
         return fail(MSSM_ERR_UNSUPPORTED, "gated recurrence does not support this shape");
-    const hipError_t e = mssm::launch_gated_recurrence_fwd(a, st);
+    Range ws;
+    if (mssm_status s = check_workspace(workspace, workspace_bytes, mssm::gated_recurrence_workspace(a, false), &ws))
+        return s;
+    const Range outs[] = {range("y", y, z.act_bytes), range("h_last", h_last, z.rows * 4), ws};
+    if (mssm_status c = check_overlaps(ins, 5, outs, 3, h0, h_last)) return c;
+    const hipError_t e = mssm::launch_gated_recurrence_fwd(a, workspace, st);
     if (e != hipSuccess) return hip_fail(e, "gated-recurrence launch");
     g_last_variant = MSSM_VARIANT_AUTO;
     return MSSM_OK;
@@ -795,15 +820,16 @@ mssm_status mssm_gated_recurrence_fwd(const void *x, const void *r, const void *
 mssm_status mssm_gated_recurrence_bwd(const void *x, const void *r, const void *i, const float *lam,
                                       float scale, const float *h0, const void *y, const void *dy,
                                       const float *dh_last, void *dx, void *dr, void *di,
-                                      float *dlam, float *dh0, mssm_recurrence_dims dims,
+                                      float *dlam, float *dh0, void *workspace,
+                                      int64_t workspace_bytes, mssm_recurrence_dims dims,
                                       mssm_dtypes dtypes, void *stream) {
     g_last_error.clear();
     RecurrenceSizes z;
     if (mssm_status s = check_recurrence(dims, scale, dtypes, &z)) return s;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const Range outs[] = {range("dx", dx, z.act_bytes), range("dr", dr, z.act_bytes),
+    Range outs[] = {range("dx", dx, z.act_bytes), range("dr", dr, z.act_bytes),
                           range("di", di, z.act_bytes), range("dlam", dlam, dims.dim * 4),
-                          range("dh0", dh0, z.rows * 4)};
+                          range("dh0", dh0, z.rows * 4), Range{}};
     if (z.rows == 0 || dims.seqlen == 0) {
         if (overlaps(outs[3], outs[4])) return fail(MSSM_ERR_INVALID_ARG, "dlam overlaps dh0");
         if (overlaps(outs[3], range("dh_last", dh_last, z.rows * 4)))
@@ -829,16 +855,18 @@ mssm_status mssm_gated_recurrence_bwd(const void *x, const void *r, const void *
                          range("i", i, z.act_bytes), range("lam", lam, dims.dim * 4),
                          range("h0", h0, z.rows * 4), range("y", y, z.act_bytes),
                          range("dy", dy, z.act_bytes), range("dh_last", dh_last, z.rows * 4)};
-    if (mssm_status c = check_overlaps(ins, 8, outs, 5, nullptr, nullptr)) return c;
     mssm::RecurrenceArgs a{};
     a.x = x; a.r = r; a.i = i; a.lam = lam; a.scale = scale; a.h0 = h0;
     a.y = const_cast<void *>(y); a.dy = dy; a.dh_last = dh_last;
     a.dx = dx; a.dr = dr; a.di = di; a.dlam = dlam; a.dh0 = dh0;
     a.batch = dims.batch; a.L = dims.seqlen; a.dim = dims.dim;
-    a.io = dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16;
+    a.io = io_type(dtypes);
     if (!mssm::gated_recurrence_supported(a))
         return fail(MSSM_ERR_UNSUPPORTED, "gated recurrence does not support this shape");
-    const hipError_t e = mssm::launch_gated_recurrence_bwd(a, st);
+    if (mssm_status s = check_workspace(workspace, workspace_bytes, mssm::gated_recurrence_workspace(a, true), &outs[5]))
+        return s;
+    if (mssm_status c = check_overlaps(ins, 8, outs, 6, nullptr, nullptr)) return c;
+    const hipError_t e = mssm::launch_gated_recurrence_bwd(a, workspace, st);
     if (e != hipSuccess) return hip_fail(e, "gated-recurrence backward launch");
     g_last_variant = MSSM_VARIANT_AUTO;
     return MSSM_OK;
@@ -852,13 +880,13 @@ mssm_status mssm_gated_recurrence_update(float *state, const void *x, const void
         return fail(MSSM_ERR_INVALID_ARG, "state is null");
     }
     dims.seqlen = 1;
-    return mssm_gated_recurrence_fwd(x, r, i, lam, scale, state, y, state, dims, dtypes, stream);
+    return mssm_gated_recurrence_fwd(x, r, i, lam, scale, state, y, state, nullptr, 0, dims, dtypes, stream);
 }
 
 mssm_status mssm_linear_cross_entropy_fwd(const void *hidden, const void *weight,
                                           const int64_t *targets, int64_t ignore_index, float *loss,
-                                          float *lse, mssm_loss_dims dims, mssm_dtypes dtypes,
-                                          void *stream) {
+                                          float *lse, void *workspace, int64_t workspace_bytes,
+                                          mssm_loss_dims dims, mssm_dtypes dtypes, void *stream) {
     g_last_error.clear();
     LossSizes z;
     if (mssm_status s = check_loss(dims, dtypes, &z)) return s;
@@ -872,12 +900,15 @@ mssm_status mssm_linear_cross_entropy_fwd(const void *hidden, const void *weight
     if (!loss) return fail(MSSM_ERR_INVALID_ARG, "loss is null");
     const Range ins[] = {range("hidden", hidden, z.hidden_bytes), range("weight", weight, z.weight_bytes),
                          range("targets", targets, dims.tokens * 8)};
-    const Range outs[] = {range("loss", loss, dims.tokens * 4), range("lse", lse, dims.tokens * 4)};
-    if (mssm_status c = check_overlaps(ins, 3, outs, 2, nullptr, nullptr)) return c;
     mssm::LossArgs a{hidden, weight, targets, ignore_index, loss, lse, nullptr, nullptr, nullptr,
-                     dims.tokens, dims.dim, dims.vocab,
-                     dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16};
-    const hipError_t e = mssm::launch_linear_cross_entropy_fwd(a, static_cast<hipStream_t>(stream));
+                     dims.tokens, dims.dim, dims.vocab, io_type(dtypes)};
+    Range ws;
+    if (mssm_status s = check_workspace(workspace, workspace_bytes,
+                                        mssm::linear_cross_entropy_workspace(a, false, on_16(hidden, weight)), &ws))
+        return s;
+    const Range outs[] = {range("loss", loss, dims.tokens * 4), range("lse", lse, dims.tokens * 4), ws};
+    if (mssm_status c = check_overlaps(ins, 3, outs, 3, nullptr, nullptr)) return c;
+    const hipError_t e = mssm::launch_linear_cross_entropy_fwd(a, workspace, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(e, "cross-entropy launch");
     g_last_variant = MSSM_VARIANT_AUTO;
     return MSSM_OK;
@@ -886,8 +917,8 @@ mssm_status mssm_linear_cross_entropy_fwd(const void *hidden, const void *weight
 mssm_status mssm_linear_cross_entropy_bwd(const void *hidden, const void *weight,
                                           const int64_t *targets, int64_t ignore_index,
                                           const float *lse, const float *dloss, void *dhidden,
-                                          void *dweight, mssm_loss_dims dims, mssm_dtypes dtypes,
-                                          void *stream) {
+                                          void *dweight, void *workspace, int64_t workspace_bytes,
+                                          mssm_loss_dims dims, mssm_dtypes dtypes, void *stream) {
     g_last_error.clear();
     LossSizes z;
     if (mssm_status s = check_loss(dims, dtypes, &z)) return s;
@@ -910,16 +941,52 @@ mssm_status mssm_linear_cross_entropy_bwd(const void *hidden, const void *weight
     const Range ins[] = {range("hidden", hidden, z.hidden_bytes), range("weight", weight, z.weight_bytes),
                          range("targets", targets, dims.tokens * 8), range("lse", lse, dims.tokens * 4),
                          range("dloss", dloss, dims.tokens * 4)};
-    const Range outs[] = {range("dhidden", dhidden, z.hidden_bytes),
-                          range("dweight", dweight, z.weight_bytes)};
-    if (mssm_status c = check_overlaps(ins, 5, outs, 2, nullptr, nullptr)) return c;
     mssm::LossArgs a{hidden, weight, targets, ignore_index, nullptr, const_cast<float *>(lse), dloss,
-                     dhidden, dweight, dims.tokens, dims.dim, dims.vocab,
-                     dtypes.io == MSSM_F32 ? mssm::IO_F32 : mssm::IO_BF16};
-    const hipError_t e = mssm::launch_linear_cross_entropy_bwd(a, st);
+                     dhidden, dweight, dims.tokens, dims.dim, dims.vocab, io_type(dtypes)};
+    Range ws;
+    if (mssm_status s = check_workspace(workspace, workspace_bytes,
+                                        mssm::linear_cross_entropy_workspace(a, true, on_16(hidden, weight)), &ws))
+        return s;
+    const Range outs[] = {range("dhidden", dhidden, z.hidden_bytes),
+                          range("dweight", dweight, z.weight_bytes), ws};
+    if (mssm_status c = check_overlaps(ins, 5, outs, 3, nullptr, nullptr)) return c;
+    const hipError_t e = mssm::launch_linear_cross_entropy_bwd(a, workspace, st);
     if (e != hipSuccess) return hip_fail(e, "cross-entropy backward launch");
     g_last_variant = MSSM_VARIANT_AUTO;
     return MSSM_OK;
+}
+
+int64_t mssm_layer_norm_bwd_workspace(mssm_norm_dims dims, mssm_dtypes dtypes) {
+    g_last_error.clear();
+    NormSizes z;
+    if (check_norm(dims, dtypes, &z)) return -1;
+    mssm::NormArgs a{};
+    a.rows = dims.rows; a.dim = dims.dim; a.io = io_type(dtypes);
+    return static_cast<int64_t>(mssm::layer_norm_bwd_workspace(a));
+}
+
+int64_t mssm_gated_recurrence_workspace(mssm_recurrence_dims dims, mssm_dtypes dtypes, int backward) {
+    g_last_error.clear();
+    RecurrenceSizes z;
+    if (check_recurrence(dims, 0.0f, dtypes, &z)) return -1;
+    if (z.rows == 0 || dims.seqlen == 0) return 0;
+    mssm::RecurrenceArgs a{};
+    a.batch = dims.batch; a.L = dims.seqlen; a.dim = dims.dim; a.io = io_type(dtypes);
+    if (!mssm::gated_recurrence_supported(a)) {
+        fail(MSSM_ERR_UNSUPPORTED, "gated recurrence does not support this shape");
+        return -1;
+    }
+    return static_cast<int64_t>(mssm::gated_recurrence_workspace(a, backward != 0));
+}
+
+int64_t mssm_linear_cross_entropy_workspace(mssm_loss_dims dims, mssm_dtypes dtypes, int backward, int aligned) {
+    g_last_error.clear();
+    LossSizes z;
+    if (check_loss(dims, dtypes, &z)) return -1;
+    if (dims.tokens == 0) return 0;
+    mssm::LossArgs a{};
+    a.tokens = dims.tokens; a.dim = dims.dim; a.vocab = dims.vocab; a.io = io_type(dtypes);
+    return static_cast<int64_t>(mssm::linear_cross_entropy_workspace(a, backward != 0, aligned != 0));
 }
 
 mssm_variant mssm_force_variant(mssm_variant v) {
@@ -948,8 +1015,11 @@ int mssm_version(void) { return 100; }
 mssm_status mssm_device_status(uint32_t *bits, int clear) {
     g_last_error.clear();
     if (!bits) return fail(MSSM_ERR_INVALID_ARG, "bits is null");
-    const hipError_t e = mssm::device_status(bits, clear != 0);
+    uint32_t more = 0;
+    hipError_t e = mssm::device_status(bits, clear != 0);
+    if (e == hipSuccess) e = mssm::recurrence_status(&more, clear != 0);
     if (e != hipSuccess) return hip_fail(e, "device status read");
+    *bits |= more;
     return MSSM_OK;
 }
 

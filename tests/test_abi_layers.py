@@ -25,19 +25,21 @@ def norm_fwd(L, rows=4, dim=8, io=0, param=0, **kw):
 
 
 def norm_bwd(L, rows=4, dim=8, io=0, param=0, **kw):
-    return call(L, "layer_norm_bwd", ["dy", "x", "mean", "rstd", "weight", "dx", "dweight", "dbias"], {},
+    return call(L, "layer_norm_bwd", ["dy", "x", "mean", "rstd", "weight", "dx", "dweight", "dbias", "workspace", "bytes"],
+                dict(workspace=kw.pop("workspace", None), bytes=kw.pop("bytes", 0)),
                 _lib.NormDims(rows, dim), io, param, **kw)
 
 
 def rec_fwd(L, batch=2, seqlen=5, dim=8, io=0, param=0, **kw):
-    return call(L, "gated_recurrence_fwd", ["x", "r", "i", "lam", "scale", "h0", "y", "h_last"],
-                dict(scale=kw.pop("scale", 8.0)), _lib.RecurrenceDims(batch, seqlen, dim), io, param, **kw)
+    return call(L, "gated_recurrence_fwd", ["x", "r", "i", "lam", "scale", "h0", "y", "h_last", "workspace", "bytes"],
+                dict(scale=kw.pop("scale", 8.0), workspace=kw.pop("workspace", None), bytes=kw.pop("bytes", 0)), _lib.RecurrenceDims(batch, seqlen, dim), io, param, **kw)
 
 
 def rec_bwd(L, batch=2, seqlen=5, dim=8, io=0, param=0, **kw):
     return call(L, "gated_recurrence_bwd",
-                ["x", "r", "i", "lam", "scale", "h0", "y", "dy", "dh_last", "dx", "dr", "di", "dlam", "dh0"],
-                dict(scale=kw.pop("scale", 8.0)), _lib.RecurrenceDims(batch, seqlen, dim), io, param, **kw)
+                ["x", "r", "i", "lam", "scale", "h0", "y", "dy", "dh_last", "dx", "dr", "di", "dlam", "dh0",
+                 "workspace", "bytes"],
+                dict(scale=kw.pop("scale", 8.0), workspace=kw.pop("workspace", None), bytes=kw.pop("bytes", 0)), _lib.RecurrenceDims(batch, seqlen, dim), io, param, **kw)
 
 
 def rec_step(L, batch=2, seqlen=1, dim=8, io=0, param=0, **kw):
@@ -46,14 +48,14 @@ def rec_step(L, batch=2, seqlen=1, dim=8, io=0, param=0, **kw):
 
 
 def loss_fwd(L, tokens=4, dim=8, vocab=10, io=0, param=0, **kw):
-    return call(L, "linear_cross_entropy_fwd", ["hidden", "weight", "targets", "ignore", "loss", "lse"],
-                dict(ignore=-100), _lib.LossDims(tokens, dim, vocab), io, param, **kw)
+    return call(L, "linear_cross_entropy_fwd", ["hidden", "weight", "targets", "ignore", "loss", "lse", "workspace", "bytes"],
+                dict(ignore=-100, workspace=kw.pop("workspace", None), bytes=kw.pop("bytes", 0)), _lib.LossDims(tokens, dim, vocab), io, param, **kw)
 
 
 def loss_bwd(L, tokens=4, dim=8, vocab=10, io=0, param=0, **kw):
     return call(L, "linear_cross_entropy_bwd",
-                ["hidden", "weight", "targets", "ignore", "lse", "dloss", "dhidden", "dweight"],
-                dict(ignore=-100), _lib.LossDims(tokens, dim, vocab), io, param, **kw)
+                ["hidden", "weight", "targets", "ignore", "lse", "dloss", "dhidden", "dweight", "workspace", "bytes"],
+                dict(ignore=-100, workspace=kw.pop("workspace", None), bytes=kw.pop("bytes", 0)), _lib.LossDims(tokens, dim, vocab), io, param, **kw)
 
 
 CALLS = {"norm_fwd": norm_fwd, "norm_bwd": norm_bwd, "rec_fwd": rec_fwd, "rec_bwd": rec_bwd,
@@ -127,6 +129,39 @@ def test_empty_calls_need_no_gpu(L):
     assert norm_bwd(L, rows=0, dweight=None, dbias=None) == _lib.MSSM_OK
     assert rec_bwd(L, batch=0, dlam=None, dh0=None) == _lib.MSSM_OK
     assert rec_fwd(L, seqlen=0, h_last=None) == _lib.MSSM_OK
+
+
+def queries(L, io=0):
+    """(call, sizes, its workspace, an input to overlap) where one is needed."""
+    dt = _lib.DTypes(io, 0)
+    return [(norm_bwd, dict(rows=300, dim=40), L.mssm_layer_norm_bwd_workspace(_lib.NormDims(300, 40), dt), "dy"),
+            (rec_fwd, dict(seqlen=3000), L.mssm_gated_recurrence_workspace(_lib.RecurrenceDims(2, 3000, 8), dt, 0), "x"),
+            (rec_bwd, dict(seqlen=3000), L.mssm_gated_recurrence_workspace(_lib.RecurrenceDims(2, 3000, 8), dt, 1), "y"),
+            (loss_fwd, dict(tokens=40), L.mssm_linear_cross_entropy_workspace(_lib.LossDims(40, 8, 10), dt, 0, 1), "hidden"),
+            (loss_bwd, dict(tokens=40), L.mssm_linear_cross_entropy_workspace(_lib.LossDims(40, 8, 10), dt, 1, 1), "weight")]
+
+
+@pytest.mark.parametrize("io", [0, 1])
+def test_workspace_refusals(L, io):
+    for f, sizes, need, operand in queries(L, io):
+        assert need > 0 and need % 4 == 0
+        at = fake(800) // 256 * 256
+        assert f(L, io=io, workspace=at, bytes=need - 1, **sizes) == INVALID and b"smaller" in L.mssm_last_error()
+        assert f(L, io=io, workspace=at, bytes=-1, **sizes) == INVALID
+        assert f(L, io=io, workspace=at + 16, bytes=need, **sizes) == INVALID and b"aligned" in L.mssm_last_error()
+        assert f(L, io=io, workspace=at, bytes=need, **{operand: at}, **sizes) == INVALID
+        assert b"overlap" in L.mssm_last_error()
+
+
+def test_workspace_queries_refuse_what_the_calls_refuse(L):
+    dt, bad = _lib.DTypes(0, 0), _lib.DTypes(7, 0)
+    assert L.mssm_layer_norm_bwd_workspace(_lib.NormDims(-1, 4), dt) == -1 and L.mssm_last_error()
+    assert L.mssm_layer_norm_bwd_workspace(_lib.NormDims(1, 4), bad) == -1
+    assert L.mssm_gated_recurrence_workspace(_lib.RecurrenceDims(1, 1 << 40, 4), dt, 0) == -1
+    assert L.mssm_gated_recurrence_workspace(_lib.RecurrenceDims(1, 9, 1 << 21), dt, 1) == -1
+    assert L.mssm_linear_cross_entropy_workspace(_lib.LossDims(1, 0, 4), dt, 0, 1) == -1
+    assert L.mssm_gated_recurrence_workspace(_lib.RecurrenceDims(1, 0, 4), dt, 1) == 0
+    assert L.mssm_linear_cross_entropy_workspace(_lib.LossDims(0, 4, 4), dt, 1, 1) == 0
 
 
 def test_binding_refuses_before_the_library():

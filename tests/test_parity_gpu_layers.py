@@ -642,3 +642,24 @@ def test_layers_on_another_stream(dev, mssm):
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
+
+def test_layers_in_a_graph(dev, mssm):
+    """Captured once, replayed on new values with eager work in between: every
+    replay equals the eager result."""
+    announce("layers in a graph")
+    t = together_inputs(dev, 60)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        everything(mssm, t)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = everything(mssm, t)
+    for k in range(4):
+        for key, v in together_inputs(dev, 70 + k).items():
+            t[key].copy_(v)
+        want = [v.clone() for v in everything(mssm, t)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), k
