@@ -28,11 +28,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kRowBytes = 128;   // of k staged per step and operand row
+constexpr int kRowBytes = 64;    // of k staged per step and operand row
 constexpr int kChunks = kRowBytes / 16;
-constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 256;    // four waves, 2 x 2, 64 x 64 of C each
-constexpr int kWM = 64, kWN = 64;
+constexpr int kStages = 4;       // steps in LDS at a time
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
 // One product step over the 16 bytes of k that each lane holds of its A row
 // (lane % 32) and its B row: bfloat16 holds k 8 (lane / 32) .. + 7 of one
@@ -56,87 +55,182 @@ struct Rows {
 };
 
 // Row of C inside a 32 x 32 block that element e of a lane's accumulator is
-// (its column is lane % 32).
+// (its column is lane % 32): four consecutive rows for every four elements.
 __device__ __forceinline__ int acc_row(int e, int lane) { return 8 * (e / 4) + 4 * (lane / 32) + e % 4; }
 
-template <typename T, typename Epilogue>
-__global__ __launch_bounds__(kThreads) void product_kernel(Rows A, Rows B, int64_t kbytes, int mtiles,
-                                                           Epilogue ep) {
-    __shared__ __align__(16) unsigned char lds[(kBM + kBN) * kRowBytes];
-    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-    const int m0 = static_cast<int>(blockIdx.x % mtiles) * kBM, n0 = static_cast<int>(blockIdx.x / mtiles) * kBN;
-    const int wm = (wave / 2) * kWM, wn = (wave % 2) * kWN;
-    f32x16 acc[kWM / 32][kWN / 32];
+// A workgroup's tile of C and a wave's part of it.
+template <int BM_, int BN_, int WM_, int WN_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr int I = WM / 32, J = WN / 32, waves_m = BM / WM;
+    static_assert((BM / WM) * (BN / WN) == kWaves, "four waves");
+    static constexpr int stage = (BM + BN) * kRowBytes, lds = kStages * stage;
+};
+
+// Position of workgroup `id` of n: workgroups go to the eight XCDs in turn, so
+// each XCD gets a run of consecutive positions, and a run of 8 tiles of m for
+// each n: the 32 workgroups an XCD holds at a time then share 8 + 4 operand
+// tiles through its L2.
+__device__ __forceinline__ void tile_of(int id, int n, int mt, int nt, int *m, int *nn) {
+    const int per = n / 8, rest = n % 8, x = id % 8;
+    const int t = x * per + min(x, rest) + id / 8;
+    constexpr int kGroup = 8;
+    const int g = t / (kGroup * nt), r = t - g * kGroup * nt, width = min(kGroup, mt - g * kGroup);
+    *m = g * kGroup + r % width;
+    *nn = r / width;
+}
+
+// Wait until at most N of this wave's loads into LDS are under way, then for
+// the other waves.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+}
+
+// C[m, n] = sum_k A[m, k] B[n, k] for one tile.  Rows move from memory straight
+// into LDS, kRowBytes of every row a step, three steps ahead; a wave's operand
+// fragments are read half a step ahead of the products that use them, the
+// first ones of a step right after its barrier, under the last products of
+// the step before.
+template <typename T, typename Shape>
+__device__ __forceinline__ void product_tile(const Rows &A, const Rows &B, int64_t kbytes, int m0, int n0,
+                                             unsigned char *lds, f32x16 (&acc)[Shape::I][Shape::J]) {
+    constexpr int I = Shape::I, J = Shape::J;
+    constexpr int kRowsPer = 64 / kChunks;                        // rows of one load instruction
+    constexpr int kLoads = (Shape::BM + Shape::BN) / kRowsPer;    // of a step
+    constexpr int kMine = (kLoads + kWaves - 1) / kWaves;         // of them, this wave's (the last ones may repeat)
+    const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int chunks = static_cast<int>((kbytes + 15) / 16), steps = (chunks + kChunks - 1) / kChunks;
+    // rows past the end lie past the buffer's end and read as zero
+    const auto rows_at = [](const Rows &R, int first, int most) {
+        // (the minimum is formed in a vector register)
+        const int n = __builtin_amdgcn_readfirstlane(min(R.rows - first, most));
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char *>(R.p) + first * R.ld, 0,
+                                                 n * static_cast<int>(R.ld), 0x00020000);
+    };
+    const __amdgpu_buffer_rsrc_t ra = rows_at(A, m0, Shape::BM), rb = rows_at(B, n0, Shape::BN);
+    const uint32_t lda = static_cast<uint32_t>(A.ld), ldb = static_cast<uint32_t>(B.ld);
+    // The chunks of a row are permuted by the row, so that lanes that read one
+    // chunk of consecutive rows hit different banks: LDS is filled in lane
+    // order, so the lanes fetch them permuted.
+    const int row = lane / kChunks, chunk = (lane % kChunks) ^ ((row / 2) % kChunks);
+    const uint32_t va = row * lda + chunk * 16, vb = row * ldb + chunk * 16;
+    typedef __attribute__((address_space(3))) void Lds;
+    const auto load = [&](int step) {
+        const bool in = step * kChunks + chunk < chunks;          // k past the end reads as zero too
+        const uint32_t oa = in ? va : 0xffffffffu, ob = in ? vb : 0xffffffffu;
+        unsigned char *to = lds + (step % kStages) * Shape::stage;
 #pragma unroll
-    for (int i = 0; i < kWM / 32; ++i)
+        for (int s = 0; s < kMine; ++s) {
+            constexpr int kA = Shape::BM / kRowsPer;
+            static_assert(kA % kWaves == 0, "each of a wave's loads is of one operand");
+            const int q = min(wave + s * kWaves, kLoads - 1);
+            if (s < kA / kWaves)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (Lds *)(to + q * 1024), 16, oa,
+                                                         q * kRowsPer * lda + step * kRowBytes, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (Lds *)(to + q * 1024), 16, ob,
+                                                         (q - kA) * kRowsPer * ldb + step * kRowBytes, 0, 0);
+        }
+    };
+    const int wm = (wave % Shape::waves_m) * Shape::WM, wn = (wave / Shape::waves_m) * Shape::WN;
+    u32x4 fa[2][I], fb[2][J];
+    const auto read = [&](int step, int half) {
+        const unsigned char *from = lds + (step % kStages) * Shape::stage + (lane % 32) * kRowBytes +
+                                    (((2 * half + lane / 32) ^ ((lane / 2) % kChunks)) * 16);
 #pragma unroll
-        for (int j = 0; j < kWN / 32; ++j)
+        for (int i = 0; i < I; ++i) fa[half][i] = *reinterpret_cast<const u32x4 *>(from + (wm + 32 * i) * kRowBytes);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            fb[half][j] = *reinterpret_cast<const u32x4 *>(from + (Shape::BM + wn + 32 * j) * kRowBytes);
+    };
+    const auto multiply = [&](int half) {
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j) mma(acc[i][j], fa[half][i], fb[half][j], T{});
+    };
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    const int col = tid % kChunks;
-    for (int64_t k0 = 0; k0 < kbytes; k0 += kRowBytes) {
-        const int64_t kk = k0 + 16 * col;
-        __syncthreads();
-        // rows past the end and k past the end are zeros
-#pragma unroll
-        for (int s = 0; s < (kBM + kBN) * kChunks / kThreads; ++s) {
-            const int row = s * (kThreads / kChunks) + tid / kChunks;
-            u32x4 v = {0, 0, 0, 0};
-            if (kk < kbytes) {
-                if (row < kBM) {
-                    if (m0 + row < A.rows)
-                        v = *reinterpret_cast<const u32x4 *>(A.p + (m0 + row) * A.ld + kk);
-                } else if (n0 + row - kBM < B.rows) {
-                    v = *reinterpret_cast<const u32x4 *>(B.p + (n0 + row - kBM) * B.ld + kk);
-                }
-            }
-            // chunks of a row are rotated by the row so that lanes reading one
-            // chunk of consecutive rows hit different banks
-            *reinterpret_cast<u32x4 *>(lds + row * kRowBytes + ((col ^ (row % kChunks)) * 16)) = v;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < kChunks; c += 2) {
-            u32x4 a[kWM / 32], b[kWN / 32];
-            const int ch = c + lane / 32;
-#pragma unroll
-            for (int i = 0; i < kWM / 32; ++i) {
-                const int row = wm + 32 * i + lane % 32;
-                a[i] = *reinterpret_cast<const u32x4 *>(lds + row * kRowBytes + ((ch ^ (row % kChunks)) * 16));
-            }
-#pragma unroll
-            for (int j = 0; j < kWN / 32; ++j) {
-                const int row = kBM + wn + 32 * j + lane % 32;
-                b[j] = *reinterpret_cast<const u32x4 *>(lds + row * kRowBytes + ((ch ^ (row % kChunks)) * 16));
-            }
-#pragma unroll
-            for (int i = 0; i < kWM / 32; ++i)
-#pragma unroll
-                for (int j = 0; j < kWN / 32; ++j) mma(acc[i][j], a[i], b[j], T{});
-        }
+    for (int s = 0; s < kStages - 1; ++s) load(s);
+    wait_and_meet<(kStages - 2) * kMine>();
+    load(kStages - 1);
+    read(0, 0);
+    read(0, 1);
+    multiply(0);
+    for (int step = 1; step < steps; ++step) {
+        wait_and_meet<(kStages - 2) * kMine>();
+        load(step + kStages - 1);
+        read(step, 0);
+        multiply(1);
+        __builtin_amdgcn_sched_barrier(0);
+        read(step, 1);
+        multiply(0);
     }
+    multiply(1);
+}
+
+// One grid of products of the same kind: problem 0's tiles, then problem 1's.
+struct Problem {
+    Rows A, B;
+    int64_t kbytes;
+    int mt, nt;
+};
+
+template <typename Epilogue>
+struct Pair {
+    Problem p[2];
+    Epilogue e[2];
+};
+
+template <typename T, typename Shape, typename Epilogue>
+__global__ __launch_bounds__(kThreads, Shape::lds > 81920 ? 1 : 2) void product_kernel(Pair<Epilogue> both) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    const int n0 = both.p[0].mt * both.p[0].nt, id = static_cast<int>(blockIdx.x);
+    const int which = id >= n0 ? 1 : 0;
+    const Problem &p = both.p[which];
+    const Epilogue &ep = both.e[which];
+    int mi, ni;
+    tile_of(id - (which ? n0 : 0), p.mt * p.nt, p.mt, p.nt, &mi, &ni);
+    const int m0 = __builtin_amdgcn_readfirstlane(mi * Shape::BM), t0 = __builtin_amdgcn_readfirstlane(ni * Shape::BN);
+    f32x16 acc[Shape::I][Shape::J];
+    product_tile<T, Shape>(p.A, p.B, p.kbytes, m0, t0, lds, acc);
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int wm = (wave % Shape::waves_m) * Shape::WM, wn = (wave / Shape::waves_m) * Shape::WN;
 #pragma unroll
-    for (int j = 0; j < kWN / 32; ++j) ep.column(m0 + wm, n0 + wn + 32 * j + lane % 32, lane, &acc[0][j]);
+    for (int j = 0; j < Shape::J; ++j) {
+        f32x16 column[Shape::I];
+#pragma unroll
+        for (int i = 0; i < Shape::I; ++i) column[i] = acc[i][j];
+        ep.template column<Shape::I>(m0 + wm, t0 + wn + 32 * j + lane % 32, lane, column);
+    }
 }
 
 // ---- forward: maximum and sum of exponentials of a token over a tile's words
 struct LossTile {
-    float2 *part;              // [vocabulary tile of kWM words][token]
+    float2 *part;              // [32 I words][token]
     float *target_logit;       // [token]
     const int64_t *targets;
     int tokens, words, word0;  // words of this piece; word0: the piece's first
     int part0;                 // first part of this piece
-    __device__ void column(int m, int t, int lane, const f32x16 *acc) const {
+    template <int I>
+    __device__ __forceinline__ void column(int m, int t, int lane, const f32x16 (&acc)[I]) const {
         if (t >= tokens) t = -1;
         const int64_t target = t >= 0 ? targets[t] - word0 : -1;
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kWM / 32; ++i)
+        for (int i = 0; i < I; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int v = m + 32 * i + acc_row(e, lane);
-                const float l = acc[i * (kWN / 32)][e];
+                const float l = acc[i][e];
                 if (v < words) top = fmaxf(top, l);
                 if (v == target && v < words) target_logit[t] = l;
             }
@@ -144,14 +238,14 @@ struct LossTile {
         const float ref = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kWM / 32; ++i)
+        for (int i = 0; i < I; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int v = m + 32 * i + acc_row(e, lane);
-                if (v < words) sum += fast_exp2((acc[i * (kWN / 32)][e] - ref) * kLog2e);
+                if (v < words) sum += fast_exp2((acc[i][e] - ref) * kLog2e);
             }
         sum += __shfl_xor(sum, 32);
-        if (t >= 0 && lane < 32) part[static_cast<int64_t>(part0 + m / kWM) * tokens + t] = make_float2(top, sum);
+        if (t >= 0 && lane < 32 && m < words) part[static_cast<int64_t>(part0 + m / (32 * I)) * tokens + t] = make_float2(top, sum);
     }
 };
 
@@ -208,7 +302,8 @@ struct ProbTile {
     const float *lse, *dloss, *scale;
     int64_t ignore, vocab;
     int tokens, words, word0;
-    __device__ void column(int m, int t, int lane, const f32x16 *acc) const {
+    template <int I>
+    __device__ __forceinline__ void column(int m, int t, int lane, const f32x16 (&acc)[I]) const {
         if (t >= ldpt) return;
         const int64_t target = t < tokens ? targets[t] : ignore;
         const bool live = target != ignore;
@@ -216,14 +311,14 @@ struct ProbTile {
         float g = live ? dloss[t] / *scale : 0.0f;
         if (live && (target < 0 || target >= vocab)) g = NAN;
 #pragma unroll
-        for (int i = 0; i < kWM / 32; ++i)
+        for (int i = 0; i < I; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int v = m + 32 * i + acc_row(e, lane);
                 if (v >= ldp) continue;
                 float x = 0.0f;
                 if (live && v < words) {
-                    x = fast_exp2((acc[i * (kWN / 32)][e] - ref) * kLog2e);
+                    x = fast_exp2((acc[i][e] - ref) * kLog2e);
                     x = (x - (v + word0 == target ? 1.0f : 0.0f)) * g;
                 }
                 if (t < tokens) Io<T>::store(p, t * ldp + v, x);
@@ -241,15 +336,16 @@ struct GradTile {
     int64_t ld;
     int rows, cols;            // of the output
     bool add;                  // sum holds earlier pieces
-    __device__ void column(int m, int n, int lane, const f32x16 *acc) const {
+    template <int I>
+    __device__ __forceinline__ void column(int m, int n, int lane, const f32x16 (&acc)[I]) const {
         if (n >= rows) return;
 #pragma unroll
-        for (int i = 0; i < kWM / 32; ++i)
+        for (int i = 0; i < I; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int d = m + 32 * i + acc_row(e, lane);
                 if (d >= cols) continue;
-                float v = acc[i * (kWN / 32)][e];
+                float v = acc[i][e];
                 const int64_t at = n * ld + d;
                 if (add) v += sum[at];
                 if (out) Io<T>::store(out, at, v * *scale);
@@ -300,12 +396,34 @@ bool on_16(const LossArgs &a) {
     return ((reinterpret_cast<uintptr_t>(a.hidden) | reinterpret_cast<uintptr_t>(a.weight)) & 15u) == 0;
 }
 
-template <typename T, typename Epilogue>
-hipError_t product(Rows A, Rows B, int64_t kbytes, const Epilogue &ep, hipStream_t stream) {
-    const int64_t mt = ceil_div(A.rows, kBM), nt = ceil_div(B.rows, kBN);
-    hipLaunchKernelGGL((product_kernel<T, Epilogue>), dim3(static_cast<uint32_t>(mt * nt)), dim3(kThreads), 0,
-                       stream, A, B, kbytes, static_cast<int>(mt), ep);
+typedef Tile<256, 256, 128, 128> Large;
+typedef Tile<128, 128, 64, 64> Medium;
+typedef Tile<256, 32, 64, 32> Narrow;    // few tokens
+
+template <typename T, typename Shape, typename Epilogue>
+hipError_t product_as(Problem p0, Problem p1, const Epilogue &e0, const Epilogue &e1, hipStream_t stream) {
+    const auto tiles = [](Problem &p) {
+        p.mt = static_cast<int>(ceil_div(p.A.rows, Shape::BM));
+        p.nt = static_cast<int>(ceil_div(p.B.rows, Shape::BN));
+        return static_cast<int64_t>(p.mt) * p.nt;
+    };
+    const int64_t n = tiles(p0) + tiles(p1);
+    const auto kernel = product_kernel<T, Shape, Epilogue>;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, Shape::lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(n)), dim3(kThreads), Shape::lds, stream,
+                       (Pair<Epilogue>{{p0, p1}, {e0, e1}}));
     return hipGetLastError();
+}
+
+// Two products of one kind in one grid (the second may be empty).
+template <typename T, typename Epilogue>
+hipError_t products(const Problem &p0, const Problem &p1, const Epilogue &e0, const Epilogue &e1, int shape,
+                    hipStream_t stream) {
+    if (shape == 0) return product_as<T, Large>(p0, p1, e0, e1, stream);
+    if (shape == 1) return product_as<T, Medium>(p0, p1, e0, e1, stream);
+    return product_as<T, Narrow>(p0, p1, e0, e1, stream);
 }
 
 template <typename T>
@@ -339,7 +457,8 @@ struct Plan {
     bool copy;                 // rows of hidden and weight are copied to aligned ones
     int64_t dimp, tokp;        // padded row lengths (elements)
     int64_t piece, piecep;     // words of a piece
-    int64_t parts;
+    int64_t parts, part_words;
+    int shape, grad_shape;     // of the logits' and the gradients' tiles
     size_t at_part, at_h, at_w, at_ht, at_wt, at_p, at_pt, at_sum, at_scale, bytes;
 };
 
@@ -361,10 +480,15 @@ Plan make_plan(const LossArgs &a, bool bwd, bool aligned) {
         p.at_w = add(p.piece * p.dimp * esz);
     }
     if (!bwd) {
-        p.parts = a.vocab / p.piece * ceil_div(p.piece, kWM) + ceil_div(a.vocab % p.piece, kWM);
+        p.shape = a.tokens <= 32 ? 2 : ceil_div(a.vocab, 256) * ceil_div(a.tokens, 256) >= 256 ? 0 : 1;
+        p.part_words = p.shape == 0 ? Large::WM : p.shape == 1 ? Medium::WM : Narrow::WM;
+        p.parts = a.vocab / p.piece * ceil_div(p.piece, p.part_words) + ceil_div(a.vocab % p.piece, p.part_words);
         p.at_part = add(p.parts * a.tokens * 8);
         return p;
     }
+    const auto tiles = [](int64_t m, int64_t n) { return ceil_div(m, 256) * ceil_div(n, 256); };
+    p.shape = tiles(p.piece, a.tokens) >= 256 ? 0 : 1;
+    p.grad_shape = tiles(a.dim, a.tokens) + tiles(a.dim, p.piece) >= 256 ? 0 : 1;
     p.at_ht = add(a.dim * p.tokp * esz);
     p.at_wt = add(a.dim * p.piecep * esz);
     p.at_p = add(a.tokens * p.piecep * esz);
@@ -378,6 +502,8 @@ template <typename T>
 Rows rows_of(const T *q, int64_t ld, int64_t n) {
     return Rows{reinterpret_cast<const unsigned char *>(q), ld * static_cast<int64_t>(sizeof(T)), static_cast<int>(n)};
 }
+
+Problem problem(const Rows &A, const Rows &B, int64_t kbytes) { return Problem{A, B, kbytes, 0, 0}; }
 
 template <typename T>
 hipError_t fwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_t stream) {
@@ -399,8 +525,9 @@ hipError_t fwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_
         }
         const LossTile ep{part, a.loss, a.targets, static_cast<int>(a.tokens), static_cast<int>(words),
                           static_cast<int>(w0), part0};
-        e = product<T>(rows_of(w, p.dimp, words), rows_of(h, p.dimp, a.tokens), p.dimp * sizeof(T), ep, stream);
-        part0 += static_cast<int>(ceil_div(words, kWM));
+        e = products<T>(problem(rows_of(w, p.dimp, words), rows_of(h, p.dimp, a.tokens), p.dimp * sizeof(T)), Problem{}, ep,
+                        ep, p.shape, stream);
+        part0 += static_cast<int>(ceil_div(words, p.part_words));
     }
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(loss_join_kernel, dim3(static_cast<uint32_t>(ceil_div(a.tokens, 256))), dim3(256), 0, stream,
@@ -435,16 +562,17 @@ hipError_t bwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_
         if (e != hipSuccess) break;
         const ProbTile<T> prob{pr, pt, wordsp, p.tokp, a.targets, a.lse, a.dloss, scale, a.ignore_index, a.vocab,
                                tokens, static_cast<int>(words), static_cast<int>(w0)};
-        e = product<T>(rows_of(w, p.dimp, words), rows_of(h, p.dimp, a.tokens), p.dimp * sizeof(T), prob, stream);
+        e = products<T>(problem(rows_of(w, p.dimp, words), rows_of(h, p.dimp, a.tokens), p.dimp * sizeof(T)), Problem{}, prob,
+                        prob, p.shape, stream);
         if (e != hipSuccess) break;
         float *sum = p.piece < a.vocab ? reinterpret_cast<float *>(base + p.at_sum) : nullptr;
         const GradTile<T> dh{sum, w0 + words >= a.vocab ? static_cast<T *>(a.dhidden) : nullptr, scale, a.dim, tokens,
                              dim, w0 > 0};
-        e = product<T>(rows_of(wt, wordsp, a.dim), rows_of(pr, wordsp, a.tokens), wordsp * sizeof(T), dh, stream);
-        if (e != hipSuccess) break;
         const GradTile<T> dw{nullptr, static_cast<T *>(a.dweight) + w0 * a.dim, scale, a.dim, static_cast<int>(words),
                              dim, false};
-        e = product<T>(rows_of(ht, p.tokp, a.dim), rows_of(pt, p.tokp, words), p.tokp * sizeof(T), dw, stream);
+        e = products<T>(problem(rows_of(wt, wordsp, a.dim), rows_of(pr, wordsp, a.tokens), wordsp * sizeof(T)),
+                        problem(rows_of(ht, p.tokp, a.dim), rows_of(pt, p.tokp, words), p.tokp * sizeof(T)), dh, dw,
+                        p.grad_shape, stream);
     }
     return e;
 }
