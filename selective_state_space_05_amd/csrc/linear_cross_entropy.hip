@@ -14,9 +14,11 @@
 // only.  In bfloat16 the rounding of p (half a step, 2^-9 relative, of
 // either sign) averages over the sums it enters.
 //
-// All three products run on one kernel: C[m, n] = sum_k A[m, k] B[n, k] with
-// both operands stored along k, for which weight, hidden and p are also laid
-// out transposed.
+// All three products run on one kernel, C[m, n] = sum_k A[m, k] B[n, k], whose
+// operands are stored either along k (hidden and weight for the logits, p for
+// dhidden) or across it (weight for dhidden, hidden and p for dweight): the
+// second kind is transposed on its way from LDS to registers, so that no
+// transposed copy of anything is ever written.
 #include "device_math.h"
 #include "internal.h"
 
@@ -47,11 +49,13 @@ __device__ __forceinline__ void mma(f32x16 &c, u32x4 a, u32x4 b, float) {
     for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[j], y[j], c, 0, 0, 0);
 }
 
-// Rows of one operand: `rows` of them, `ld` bytes apart, 16-byte aligned.
+// One operand: `rows` rows of the product, 16-byte aligned, `ld` bytes apart
+// where a row's k lie side by side; where the rows lie side by side (ACROSS),
+// it is the k that are `ld` bytes apart.  k: how many there are.
 struct Rows {
     const unsigned char *p;
     int64_t ld;
-    int rows;
+    int rows, k;
 };
 
 // Row of C inside a 32 x 32 block that element e of a lane's accumulator is
@@ -89,62 +93,143 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("" : : : "memory");
 }
 
-// C[m, n] = sum_k A[m, k] B[n, k] for one tile.  Rows move from memory straight
-// into LDS, kRowBytes of every row a step, three steps ahead; a wave's operand
-// fragments are read half a step ahead of the products that use them, the
-// first ones of a step right after its barrier, under the last products of
-// the step before.
-template <typename T, typename Shape>
-__device__ __forceinline__ void product_tile(const Rows &A, const Rows &B, int64_t kbytes, int m0, int n0,
+// One operand of a tile on its way: N rows, T their type.  A step is kRowBytes of
+// k of every row: kStepK values of k.  Loads move 16 bytes a lane straight into
+// LDS, in lane order; the lanes fetch the 16-byte chunks permuted, so that the
+// fragment reads find different banks.
+template <typename T, int N, bool ACROSS>
+struct Operand {
+    static constexpr int kStepK = kRowBytes / sizeof(T);
+    static constexpr int kLoads = N * kRowBytes / 1024;              // instructions of a step
+    static constexpr int kLine = ACROSS ? N * static_cast<int>(sizeof(T)) : kRowBytes;   // bytes of a line in LDS
+    static constexpr int kLineChunks = kLine / 16, kLines = 1024 / kLine;               // lines of one instruction
+    typedef __attribute__((address_space(3))) void Lds;
+
+    const unsigned char *base;
+    int64_t left;                // bytes from the current step to the end (ACROSS)
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t ld, lane_off;
+    int chunk, chunks;           // this lane's chunk of a line; chunks of k in all (not ACROSS)
+
+    // Chunks of line l are permuted by this.  Along k, lanes read one chunk of
+    // consecutive lines; across it (bfloat16), 16 lanes read two chunks of four
+    // lines.
+    static __device__ __forceinline__ int swizzle(int l) {
+        if (!ACROSS) return (l / 2) % kChunks;
+        return sizeof(T) == 2 ? (2 * (l % 4)) & (kLineChunks - 1) : 0;
+    }
+
+    __device__ __forceinline__ void init(const Rows &R, int first, int wave, int lane) {
+        ld = static_cast<uint32_t>(R.ld);
+        const int line = lane / kLineChunks;
+        chunk = (lane % kLineChunks) ^ swizzle(wave * kLines + line);   // a wave's loads are four apart
+        lane_off = line * ld + chunk * 16;
+        if (ACROSS) {
+            base = R.p + static_cast<int64_t>(first) * sizeof(T);
+            left = static_cast<int64_t>(R.k) * R.ld - static_cast<int64_t>(first) * sizeof(T);
+            chunks = 0;
+        } else {
+            // rows past the end lie past the buffer's end and read as zero
+            // (the minimum is formed in a vector register)
+            const int n = __builtin_amdgcn_readfirstlane(min(R.rows - first, N));
+            base = R.p + first * R.ld;
+            rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char *>(base), 0, n * static_cast<int>(R.ld),
+                                                     0x00020000);
+            chunks = static_cast<int>((R.k * static_cast<int64_t>(sizeof(T)) + 15) / 16);
+        }
+    }
+    __device__ __forceinline__ void seek(int step) {
+        if (ACROSS) {
+            base += static_cast<int64_t>(step) * kStepK * ld;
+            left -= static_cast<int64_t>(step) * kStepK * ld;
+        }
+    }
+    // Load instruction q (of kLoads) of a step into `to`; k past the end reads as
+    // zero.  Across k, steps are asked for one after the other.
+    __device__ __forceinline__ void load(int step, int q, unsigned char *to) const {
+        if (ACROSS)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds *)(to + q * 1024), 16, lane_off, q * kLines * ld, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds *)(to + q * 1024), 16,
+                                                     step * kChunks + chunk < chunks ? lane_off : 0xffffffffu,
+                                                     q * kLines * ld + step * kRowBytes, 0, 0);
+    }
+    __device__ __forceinline__ void begin_step() {
+        if (ACROSS) {
+            const int64_t n = left < 0 ? 0 : left < 0x7fffffff ? left : 0x7fffffff;
+            rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char *>(base), 0, static_cast<int>(n), 0x00020000);
+        }
+    }
+    __device__ __forceinline__ void end_step() { seek(1); }
+
+    // The 16 bytes of k that this lane holds of row `row` + lane % 32 in half
+    // `half` of the step at `from`.
+    static __device__ __forceinline__ u32x4 fragment(const unsigned char *from, int row, int half, int lane) {
+        if constexpr (!ACROSS) {
+            const int c = (2 * half + lane / 32) ^ swizzle(lane % 32);
+            return *reinterpret_cast<const u32x4 *>(from + (lane % 32) * kRowBytes + c * 16 + row * kRowBytes);
+        } else if constexpr (sizeof(T) == 2) {
+            // A transposing read gives the 16 lanes of a group the columns of a
+            // 4 x 16 block whose lines lie in lanes 4 j .. 4 j + 3: lane i fetches
+            // 8 bytes of line i / 4.
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4 LdsRow;
+            const int i = lane % 16, line = 8 * (lane / 32) + i / 4, x = 2 * (lane / 16 % 2) + i % 4 / 2;
+            const int odd = row / 32 % 2;                    // rows go in pairs of 32: eight chunks
+            const int c = (row / 64) * 8 + ((4 * odd + x) ^ swizzle(line));
+            const unsigned char *at = from + (16 * half + line) * kLine + c * 16 + i % 2 * 8;
+            const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)at));
+            const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)(at + 4 * kLine)));
+            return u32x4{lo.x, lo.y, hi.x, hi.y};
+        } else {
+            const unsigned char *at = from + 4 * (2 * half + lane / 32) * kLine + (row + lane % 32) * 4;
+            u32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t *>(at + j * kLine);
+            return v;
+        }
+    }
+};
+
+// C[m, n] = sum_k A[m, k] B[n, k] for one tile and the steps [first, first + steps)
+// of k.  A step's rows move three steps ahead; a wave's operand fragments are
+// read half a step ahead of the products that use them, the first ones of a step
+// right after its barrier, under the last products of the step before.
+template <typename T, typename Shape, bool AX, bool BX>
+__device__ __forceinline__ void product_tile(const Rows &A, const Rows &B, int first, int steps, int m0, int n0,
                                              unsigned char *lds, f32x16 (&acc)[Shape::I][Shape::J]) {
     constexpr int I = Shape::I, J = Shape::J;
-    constexpr int kRowsPer = 64 / kChunks;                        // rows of one load instruction
-    constexpr int kLoads = (Shape::BM + Shape::BN) / kRowsPer;    // of a step
-    constexpr int kMine = (kLoads + kWaves - 1) / kWaves;         // of them, this wave's (the last ones may repeat)
-    const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
-    const int chunks = static_cast<int>((kbytes + 15) / 16), steps = (chunks + kChunks - 1) / kChunks;
-    // rows past the end lie past the buffer's end and read as zero
-    const auto rows_at = [](const Rows &R, int first, int most) {
-        // (the minimum is formed in a vector register)
-        const int n = __builtin_amdgcn_readfirstlane(min(R.rows - first, most));
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char *>(R.p) + first * R.ld, 0,
-                                                 n * static_cast<int>(R.ld), 0x00020000);
-    };
-    const __amdgpu_buffer_rsrc_t ra = rows_at(A, m0, Shape::BM), rb = rows_at(B, n0, Shape::BN);
-    const uint32_t lda = static_cast<uint32_t>(A.ld), ldb = static_cast<uint32_t>(B.ld);
-    // The chunks of a row are permuted by the row, so that lanes that read one
-    // chunk of consecutive rows hit different banks: LDS is filled in lane
-    // order, so the lanes fetch them permuted.
-    const int row = lane / kChunks, chunk = (lane % kChunks) ^ ((row / 2) % kChunks);
-    const uint32_t va = row * lda + chunk * 16, vb = row * ldb + chunk * 16;
-    typedef __attribute__((address_space(3))) void Lds;
+    typedef Operand<T, Shape::BM, AX> OpA;
+    typedef Operand<T, Shape::BN, BX> OpB;
+    constexpr int kMineA = OpA::kLoads / kWaves, kMineB = (OpB::kLoads + kWaves - 1) / kWaves;   // B's last may repeat
+    static_assert(OpA::kLoads % kWaves == 0, "each of a wave's loads is of one operand");
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    OpA a;
+    OpB b;
+    a.init(A, m0, wave, lane);
+    b.init(B, n0, min(wave, OpB::kLoads - 1), lane);
+    a.seek(first);
+    b.seek(first);
     const auto load = [&](int step) {
-        const bool in = step * kChunks + chunk < chunks;          // k past the end reads as zero too
-        const uint32_t oa = in ? va : 0xffffffffu, ob = in ? vb : 0xffffffffu;
         unsigned char *to = lds + (step % kStages) * Shape::stage;
+        a.begin_step();
+        b.begin_step();
 #pragma unroll
-        for (int s = 0; s < kMine; ++s) {
-            constexpr int kA = Shape::BM / kRowsPer;
-            static_assert(kA % kWaves == 0, "each of a wave's loads is of one operand");
-            const int q = min(wave + s * kWaves, kLoads - 1);
-            if (s < kA / kWaves)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (Lds *)(to + q * 1024), 16, oa,
-                                                         q * kRowsPer * lda + step * kRowBytes, 0, 0);
-            else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (Lds *)(to + q * 1024), 16, ob,
-                                                         (q - kA) * kRowsPer * ldb + step * kRowBytes, 0, 0);
-        }
+        for (int s = 0; s < kMineA; ++s) a.load(first + step, wave + s * kWaves, to);
+#pragma unroll
+        for (int s = 0; s < kMineB; ++s)
+            b.load(first + step, min(wave + s * kWaves, OpB::kLoads - 1), to + Shape::BM * kRowBytes);
+        a.end_step();
+        b.end_step();
     };
     const int wm = (wave % Shape::waves_m) * Shape::WM, wn = (wave / Shape::waves_m) * Shape::WN;
     u32x4 fa[2][I], fb[2][J];
     const auto read = [&](int step, int half) {
-        const unsigned char *from = lds + (step % kStages) * Shape::stage + (lane % 32) * kRowBytes +
-                                    (((2 * half + lane / 32) ^ ((lane / 2) % kChunks)) * 16);
+        const unsigned char *from = lds + (step % kStages) * Shape::stage;
 #pragma unroll
-        for (int i = 0; i < I; ++i) fa[half][i] = *reinterpret_cast<const u32x4 *>(from + (wm + 32 * i) * kRowBytes);
+        for (int i = 0; i < I; ++i) fa[half][i] = OpA::fragment(from, wm + 32 * i, half, lane);
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-            fb[half][j] = *reinterpret_cast<const u32x4 *>(from + (Shape::BM + wn + 32 * j) * kRowBytes);
+        for (int j = 0; j < J; ++j) fb[half][j] = OpB::fragment(from + Shape::BM * kRowBytes, wn + 32 * j, half, lane);
     };
     const auto multiply = [&](int half) {
 #pragma unroll
@@ -159,14 +244,15 @@ __device__ __forceinline__ void product_tile(const Rows &A, const Rows &B, int64
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
+    constexpr int kAhead = (kStages - 2) * (kMineA + kMineB);
     for (int s = 0; s < kStages - 1; ++s) load(s);
-    wait_and_meet<(kStages - 2) * kMine>();
+    wait_and_meet<kAhead>();
     load(kStages - 1);
     read(0, 0);
     read(0, 1);
     multiply(0);
     for (int step = 1; step < steps; ++step) {
-        wait_and_meet<(kStages - 2) * kMine>();
+        wait_and_meet<kAhead>();
         load(step + kStages - 1);
         read(step, 0);
         multiply(1);
@@ -177,31 +263,28 @@ __device__ __forceinline__ void product_tile(const Rows &A, const Rows &B, int64
     multiply(1);
 }
 
-// One grid of products of the same kind: problem 0's tiles, then problem 1's.
+// One product: the tiles of C, each `splits` times over as many runs of
+// `steps` steps of k.
 struct Problem {
     Rows A, B;
-    int64_t kbytes;
-    int mt, nt;
+    int mt, nt, splits, steps;
 };
 
-template <typename Epilogue>
-struct Pair {
-    Problem p[2];
-    Epilogue e[2];
+template <typename Epilogue, bool AX, bool BX>
+struct Job {
+    static constexpr bool kAX = AX, kBX = BX;
+    Problem p;
+    Epilogue e;
 };
 
-template <typename T, typename Shape, typename Epilogue>
-__global__ __launch_bounds__(kThreads, Shape::lds > 81920 ? 1 : 2) void product_kernel(Pair<Epilogue> both) {
-    extern __shared__ __align__(16) unsigned char lds[];
-    const int n0 = both.p[0].mt * both.p[0].nt, id = static_cast<int>(blockIdx.x);
-    const int which = id >= n0 ? 1 : 0;
-    const Problem &p = both.p[which];
-    const Epilogue &ep = both.e[which];
+template <typename T, typename Shape, typename J>
+__device__ __forceinline__ void run_tile(const J &job, int id, unsigned char *lds) {
     int mi, ni;
-    tile_of(id - (which ? n0 : 0), p.mt * p.nt, p.mt, p.nt, &mi, &ni);
-    const int m0 = __builtin_amdgcn_readfirstlane(mi * Shape::BM), t0 = __builtin_amdgcn_readfirstlane(ni * Shape::BN);
+    const int n = job.p.mt * job.p.nt, split = id / n;
+    tile_of(id - split * n, n, job.p.mt, job.p.nt, &mi, &ni);
+    const int m0 = __builtin_amdgcn_readfirstlane(mi * Shape::BM), n0 = __builtin_amdgcn_readfirstlane(ni * Shape::BN);
     f32x16 acc[Shape::I][Shape::J];
-    product_tile<T, Shape>(p.A, p.B, p.kbytes, m0, t0, lds, acc);
+    product_tile<T, Shape, J::kAX, J::kBX>(job.p.A, job.p.B, split * job.p.steps, job.p.steps, m0, n0, lds, acc);
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int wm = (wave % Shape::waves_m) * Shape::WM, wn = (wave / Shape::waves_m) * Shape::WN;
 #pragma unroll
@@ -209,8 +292,22 @@ __global__ __launch_bounds__(kThreads, Shape::lds > 81920 ? 1 : 2) void product_
         f32x16 column[Shape::I];
 #pragma unroll
         for (int i = 0; i < Shape::I; ++i) column[i] = acc[i][j];
-        ep.template column<Shape::I>(m0 + wm, t0 + wn + 32 * j + lane % 32, lane, column);
+        job.e.template column<Shape::I>(m0 + wm, n0 + wn + 32 * j + lane % 32, split, lane, column);
     }
+}
+
+// A grid of one or two kinds of product: the first one's tiles, then the second's.
+template <typename T, typename Shape, typename J0>
+__global__ __launch_bounds__(kThreads, Shape::lds > 81920 ? 1 : 2) void product_kernel(J0 j0) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    run_tile<T, Shape>(j0, static_cast<int>(blockIdx.x), lds);
+}
+template <typename T, typename Shape, typename J0, typename J1>
+__global__ __launch_bounds__(kThreads, Shape::lds > 81920 ? 1 : 2) void product2_kernel(J0 j0, J1 j1) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    const int n0 = j0.p.mt * j0.p.nt * j0.p.splits, id = static_cast<int>(blockIdx.x);
+    if (id < n0) run_tile<T, Shape>(j0, id, lds);
+    else run_tile<T, Shape>(j1, id - n0, lds);
 }
 
 // ---- forward: maximum and sum of exponentials of a token over a tile's words
@@ -221,19 +318,24 @@ struct LossTile {
     int tokens, words, word0;  // words of this piece; word0: the piece's first
     int part0;                 // first part of this piece
     template <int I>
-    __device__ __forceinline__ void column(int m, int t, int lane, const f32x16 (&acc)[I]) const {
-        if (t >= tokens) t = -1;
-        const int64_t target = t >= 0 ? targets[t] - word0 : -1;
-        float top = -INFINITY;
+    __device__ __forceinline__ void column(int m, int t, int, int lane, const f32x16 (&acc)[I]) const {
+        if (m >= words) return;
+        const bool there = t < tokens;
+        // the target's place among this lane's words, if it is one of them
+        const int64_t target = there ? targets[t] - word0 - m : -1;
+        const int mine = target >= 0 && target < min(32 * I, words - m) ? static_cast<int>(target) : -1;
+        const bool all = m + 32 * I <= words;
+        float top = -INFINITY, hit = 0.0f;
 #pragma unroll
         for (int i = 0; i < I; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const int v = m + 32 * i + acc_row(e, lane);
+                const int v = 32 * i + acc_row(e, lane);
                 const float l = acc[i][e];
-                if (v < words) top = fmaxf(top, l);
-                if (v == target && v < words) target_logit[t] = l;
+                top = fmaxf(top, all || m + v < words ? l : -INFINITY);
+                hit = v == mine ? l : hit;
             }
+        if (mine >= 0 && mine / 4 % 2 == lane / 32) target_logit[t] = hit;
         top = fmaxf(top, __shfl_xor(top, 32));
         const float ref = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
@@ -241,28 +343,35 @@ struct LossTile {
         for (int i = 0; i < I; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const int v = m + 32 * i + acc_row(e, lane);
-                if (v < words) sum += fast_exp2((acc[i][e] - ref) * kLog2e);
+                const float x = fast_exp2((acc[i][e] - ref) * kLog2e);
+                sum += all || m + 32 * i + acc_row(e, lane) < words ? x : 0.0f;
             }
         sum += __shfl_xor(sum, 32);
-        if (t >= 0 && lane < 32 && m < words) part[static_cast<int64_t>(part0 + m / (32 * I)) * tokens + t] = make_float2(top, sum);
+        if (there && lane < 32) part[static_cast<int64_t>(part0 + m / (32 * I)) * tokens + t] = make_float2(top, sum);
     }
 };
 
-__global__ __launch_bounds__(256) void loss_join_kernel(const float2 *__restrict__ part, int parts, int tokens,
-                                                        const int64_t *__restrict__ targets, int64_t ignore,
-                                                        int64_t vocab, float *__restrict__ loss,
-                                                        float *__restrict__ lse) {
-    const int t = blockIdx.x * 256 + threadIdx.x;
-    if (t >= tokens) return;
-    float m = -INFINITY, s = 0.0f;
-    for (int k = 0; k < parts; ++k) {
-        const float2 p = part[static_cast<int64_t>(k) * tokens + t];
-        const float top = fmaxf(m, p.x), ref = top == -INFINITY ? 0.0f : top;
-        s = s * fast_exp2((m - ref) * kLog2e) + p.y * fast_exp2((p.x - ref) * kLog2e);
-        m = top;
-    }
-    const float l = m + fast_log2(s) * kLn2;
+// Joins the parts of a token: 64 tokens a workgroup, 16 slices of the parts.
+constexpr int kJoinSlices = 16;
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x), ref = top == -INFINITY ? 0.0f : top;
+    return make_float2(top, a.y * fast_exp2((a.x - ref) * kLog2e) + b.y * fast_exp2((b.x - ref) * kLog2e));
+}
+__global__ __launch_bounds__(64 * kJoinSlices) void loss_join_kernel(const float2 *__restrict__ part, int parts, int tokens,
+                                                                     const int64_t *__restrict__ targets,
+                                                                     int64_t ignore, int64_t vocab,
+                                                                     float *__restrict__ loss,
+                                                                     float *__restrict__ lse) {
+    __shared__ float2 sh[kJoinSlices][64];
+    const int lane = threadIdx.x % 64, slice = threadIdx.x / 64, t = blockIdx.x * 64 + lane;
+    float2 s = make_float2(-INFINITY, 0.0f);
+    if (t < tokens)
+        for (int k = slice; k < parts; k += kJoinSlices) s = join(s, part[static_cast<int64_t>(k) * tokens + t]);
+    sh[slice][lane] = s;
+    __syncthreads();
+    if (slice > 0 || t >= tokens) return;
+    for (int k = 1; k < kJoinSlices; ++k) s = join(s, sh[k][lane]);
+    const float l = s.x + fast_log2(s.y) * kLn2;
     if (lse) lse[t] = l;
     const int64_t target = targets[t];
     loss[t] = target == ignore ? 0.0f : (target < 0 || target >= vocab) ? NAN : l - loss[t];
@@ -293,99 +402,129 @@ __global__ __launch_bounds__(1024) void grad_scale_kernel(const float *__restric
     }
 }
 
-// p of a piece, in both layouts
+// exp(l - ref).  Float32 results carry the rounding of the exponent's product with
+// log2 e as a second term; in bfloat16 it is far below p's own rounding.
+__device__ __forceinline__ float exp_of(float d, uint16_t) { return fast_exp2(d * kLog2e); }
+__device__ __forceinline__ float exp_of(float d, float) {
+    const float hi = d * kLog2e, lo = fmaf(d, kLog2e, -hi);
+    return fast_exp2(hi) * fmaf(lo, kLn2, 1.0f);
+}
+
+// Four consecutive values at p, 4 sizeof(T)-byte aligned.
+__device__ __forceinline__ void store4(float *p, const float *f) {
+    *reinterpret_cast<f32x4 *>(p) = f32x4{f[0], f[1], f[2], f[3]};
+}
+__device__ __forceinline__ void store4(uint16_t *p, const float *f) {
+    typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<uint2 *>(p) = __builtin_bit_cast(uint2, __builtin_convertvector((f32x4{f[0], f[1], f[2], f[3]}), b4));
+}
+
+// p of a piece: p[token][word], rows ldp words apart (zero past the words).
 template <typename T>
 struct ProbTile {
-    T *p, *pt;                 // p[token][word] and pt[word][token]
-    int64_t ldp, ldpt;         // elements
+    T *p;
+    int64_t ldp;
     const int64_t *targets;
     const float *lse, *dloss, *scale;
     int64_t ignore, vocab;
     int tokens, words, word0;
     template <int I>
-    __device__ __forceinline__ void column(int m, int t, int lane, const f32x16 (&acc)[I]) const {
-        if (t >= ldpt) return;
-        const int64_t target = t < tokens ? targets[t] : ignore;
+    __device__ __forceinline__ void column(int m, int t, int, int lane, const f32x16 (&acc)[I]) const {
+        if (t >= tokens) return;
+        const int64_t target = targets[t];
         const bool live = target != ignore;
         const float ref = live ? lse[t] : 0.0f;
         float g = live ? dloss[t] / *scale : 0.0f;
         if (live && (target < 0 || target >= vocab)) g = NAN;
+        const int64_t hit = target - word0 - m;
+        const int mine = hit >= 0 && hit < 32 * I ? static_cast<int>(hit) : -1;
+        T *row = p + t * ldp + m;
 #pragma unroll
         for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int v = m + 32 * i + acc_row(e, lane);
-                if (v >= ldp) continue;
-                float x = 0.0f;
-                if (live && v < words) {
-                    x = fast_exp2((acc[i][e] - ref) * kLog2e);
-                    x = (x - (v + word0 == target ? 1.0f : 0.0f)) * g;
+            for (int e = 0; e < 16; e += 4) {
+                const int v = 32 * i + acc_row(e, lane);
+                float x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    x[k] = (exp_of(acc[i][e + k] - ref, T{}) - (v + k == mine ? 1.0f : 0.0f)) * g;
+                    if (!live || m + v + k >= words) x[k] = 0.0f;
                 }
-                if (t < tokens) Io<T>::store(p, t * ldp + v, x);
-                if (v < words) Io<T>::store(pt, v * ldpt + t, x);
+                if (m + v < ldp) store4(row + v, x);
             }
     }
 };
 
-// ---- backward: rows of a gradient, [n][m]; accumulated over pieces in float32
+// Rows of a gradient, [n][m].  Sums over pieces of the vocabulary and runs of k
+// meet in float32: one array a run, sum[run][n][ldsum], to which later pieces add.
 template <typename T>
 struct GradTile {
-    float *sum;                // float32 accumulator, or null
-    T *out;                    // output, or null
-    const float *scale;        // the output is the sum times this
-    int64_t ld;
-    int rows, cols;            // of the output
-    bool add;                  // sum holds earlier pieces
+    float *sum;                // null: the sum is complete, out is written
+    int64_t ldsum;
+    T *out;
+    const float *scale;        // out is the sum times this
+    int rows, cols;            // of the gradient
+    bool add, wide;            // sum holds earlier pieces; rows of out take stores of four
     template <int I>
-    __device__ __forceinline__ void column(int m, int n, int lane, const f32x16 (&acc)[I]) const {
+    __device__ __forceinline__ void column(int m, int n, int run, int lane, const f32x16 (&acc)[I]) const {
         if (n >= rows) return;
+        const float by = sum ? 1.0f : *scale;
+        float *srow = sum + (static_cast<int64_t>(run) * rows + n) * ldsum + m;
+        T *orow = out + static_cast<int64_t>(n) * cols + m;
 #pragma unroll
         for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int d = m + 32 * i + acc_row(e, lane);
-                if (d >= cols) continue;
-                float v = acc[i][e];
-                const int64_t at = n * ld + d;
-                if (add) v += sum[at];
-                if (out) Io<T>::store(out, at, v * *scale);
-                else sum[at] = v;
+            for (int e = 0; e < 16; e += 4) {
+                const int d = 32 * i + acc_row(e, lane);
+                if (m + d >= cols) continue;
+                float x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = acc[i][e + k] * by;
+                if (sum) {
+                    if (add) {
+                        const f32x4 old = *reinterpret_cast<const f32x4 *>(srow + d);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] += old[k];
+                    }
+                    store4(srow + d, x);
+                } else if (wide) {
+                    store4(orow + d, x);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (m + d + k < cols) Io<T>::store(orow, d + k, x[k]);
+                }
             }
     }
 };
 
-// Copy of rows [0, rows) x [0, cols) with rows `ldo` elements apart, zero past
-// the columns.
+// out[n][d] = scale * sum over the runs of sum[run][n][d].
 template <typename T>
-__global__ __launch_bounds__(256) void align_rows_kernel(const T *__restrict__ in, T *__restrict__ out,
-                                                         int64_t rows, int64_t cols, int64_t ldo) {
+__global__ __launch_bounds__(256) void add_runs_kernel(const float *__restrict__ sum, int runs, int64_t rows, int cols,
+                                                       int64_t ldsum, const float *__restrict__ scale,
+                                                       T *__restrict__ out) {
+    const float by = *scale;
+    const int64_t n = rows * cols;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k < n;
+         k += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = k / cols, c = k - r * cols;
+        float x = 0.0f;
+        for (int i = 0; i < runs; ++i) x += sum[(i * rows + r) * ldsum + c];
+        Io<T>::store(out, k, x * by);
+    }
+}
+
+// Copy of rows [0, rows) x [0, cols) with rows `ldo` elements apart, zero past
+// the columns and in rows whose target is `ignore` (targets may be null).
+template <typename T>
+__global__ __launch_bounds__(256) void align_rows_kernel(const T *__restrict__ in, T *__restrict__ out, int64_t rows,
+                                                         int64_t cols, int64_t ldo,
+                                                         const int64_t *__restrict__ targets, int64_t ignore) {
     const int64_t n = rows * ldo;
     for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k < n;
          k += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t r = k / ldo, c = k - r * ldo;
-        out[k] = c < cols ? in[r * cols + c] : T{};
-    }
-}
-
-// out[c][r] = in[r][c], zero for rows past the end and for rows whose target
-// is `ignore` (targets may be null: then every row counts).
-template <typename T>
-__global__ __launch_bounds__(256) void transpose_kernel(const T *__restrict__ in, T *__restrict__ out, int rows,
-                                                        int cols, int64_t ldo,
-                                                        const int64_t *__restrict__ targets, int64_t ignore) {
-    __shared__ T tile[32][33];
-    const int c0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
-    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-    for (int k = ty; k < 32; k += 8) {
-        const int r = r0 + k, c = c0 + tx;
-        T v{};
-        if (r < rows && c < cols && !(targets && targets[r] == ignore)) v = in[static_cast<int64_t>(r) * cols + c];
-        tile[k][tx] = v;
-    }
-    __syncthreads();
-    for (int k = ty; k < 32; k += 8) {
-        const int c = c0 + k, r = r0 + tx;
-        if (c < cols && r < ldo) out[static_cast<int64_t>(c) * ldo + r] = tile[tx][k];
+        out[k] = c < cols && !(targets && targets[r] == ignore) ? in[r * cols + c] : T{};
     }
 }
 
@@ -400,66 +539,83 @@ typedef Tile<256, 256, 128, 128> Large;
 typedef Tile<128, 128, 64, 64> Medium;
 typedef Tile<256, 32, 64, 32> Narrow;    // few tokens
 
-template <typename T, typename Shape, typename Epilogue>
-hipError_t product_as(Problem p0, Problem p1, const Epilogue &e0, const Epilogue &e1, hipStream_t stream) {
-    const auto tiles = [](Problem &p) {
-        p.mt = static_cast<int>(ceil_div(p.A.rows, Shape::BM));
-        p.nt = static_cast<int>(ceil_div(p.B.rows, Shape::BN));
-        return static_cast<int64_t>(p.mt) * p.nt;
-    };
-    const int64_t n = tiles(p0) + tiles(p1);
-    const auto kernel = product_kernel<T, Shape, Epilogue>;
+// Tiles and runs of a product: `splits` runs of k, whole steps each.
+template <typename T, typename Shape>
+int64_t lay_out(Problem *p, int splits) {
+    p->mt = static_cast<int>(ceil_div(p->A.rows, Shape::BM));
+    p->nt = static_cast<int>(ceil_div(p->B.rows, Shape::BN));
+    const int64_t steps = ceil_div(p->A.k, kRowBytes / static_cast<int64_t>(sizeof(T)));
+    p->steps = static_cast<int>(ceil_div(steps, splits));
+    p->splits = splits;
+    return static_cast<int64_t>(p->mt) * p->nt * splits;
+}
+
+template <typename Kernel, typename... Args>
+hipError_t launch_tiles(Kernel kernel, int64_t n, int lds, hipStream_t stream, const Args &...args) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, Shape::lds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(n)), dim3(kThreads), Shape::lds, stream,
-                       (Pair<Epilogue>{{p0, p1}, {e0, e1}}));
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(n)), dim3(kThreads), lds, stream, args...);
     return hipGetLastError();
 }
 
-// Two products of one kind in one grid (the second may be empty).
-template <typename T, typename Epilogue>
-hipError_t products(const Problem &p0, const Problem &p1, const Epilogue &e0, const Epilogue &e1, int shape,
-                    hipStream_t stream) {
-    if (shape == 0) return product_as<T, Large>(p0, p1, e0, e1, stream);
-    if (shape == 1) return product_as<T, Medium>(p0, p1, e0, e1, stream);
-    return product_as<T, Narrow>(p0, p1, e0, e1, stream);
+template <typename T, typename Shape, typename J0>
+hipError_t product_as(J0 j0, int splits, hipStream_t stream) {
+    const int64_t n = lay_out<T, Shape>(&j0.p, splits);
+    return launch_tiles(product_kernel<T, Shape, J0>, n, Shape::lds, stream, j0);
+}
+
+enum : int { kLarge, kMedium, kNarrow };
+
+template <typename T, typename J0>
+hipError_t product(const J0 &j0, int shape, int splits, hipStream_t stream) {
+    if (shape == kLarge) return product_as<T, Large>(j0, splits, stream);
+    if (shape == kMedium) return product_as<T, Medium>(j0, splits, stream);
+    return product_as<T, Narrow>(j0, splits, stream);
+}
+
+template <typename T, typename Shape, typename J0, typename J1>
+hipError_t product2_as(J0 j0, int splits, J1 j1, hipStream_t stream) {
+    const int64_t n = lay_out<T, Shape>(&j0.p, splits) + lay_out<T, Shape>(&j1.p, 1);
+    return launch_tiles(product2_kernel<T, Shape, J0, J1>, n, Shape::lds, stream, j0, j1);
 }
 
 template <typename T>
-hipError_t align_rows(const T *in, T *out, int64_t rows, int64_t cols, int64_t ldo, hipStream_t stream) {
+hipError_t align_rows(const T *in, T *out, int64_t rows, int64_t cols, int64_t ldo, const int64_t *targets,
+                      int64_t ignore, hipStream_t stream) {
     const int64_t blocks = ceil_div(rows * ldo, 256 * 4);
     hipLaunchKernelGGL(align_rows_kernel<T>, dim3(static_cast<uint32_t>(blocks < 65536 ? blocks : 65536)),
-                       dim3(256), 0, stream, in, out, rows, cols, ldo);
+                       dim3(256), 0, stream, in, out, rows, cols, ldo, targets, ignore);
     return hipGetLastError();
 }
 
-template <typename T>
-hipError_t transpose(const T *in, T *out, int64_t rows, int64_t cols, int64_t ldo, const int64_t *targets,
-                     int64_t ignore, hipStream_t stream) {
-    hipLaunchKernelGGL(transpose_kernel<T>,
-                       dim3(static_cast<uint32_t>(ceil_div(cols, 32)), static_cast<uint32_t>(ceil_div(ldo, 32))),
-                       dim3(256), 0, stream, in, out, static_cast<int>(rows), static_cast<int>(cols), ldo, targets,
-                       ignore);
-    return hipGetLastError();
-}
-
-// Words of the vocabulary in one piece: p of the piece has at most 2^27
-// elements, and a piece at least 1024 words.
-int64_t piece_words(int64_t rows, int64_t vocab) {
-    int64_t n = (int64_t(1) << 27) / (rows < 1 ? 1 : rows) / 1024 * 1024;
+// Words of the vocabulary in one piece, a multiple of 1024 below the whole.
+// Backward: p of the piece has at most 2^27 elements.  Forward: with copies,
+// the copied piece likewise; else the grid's workgroups stay below 2^23.
+int64_t piece_words(int64_t elements, int64_t rows, int64_t vocab) {
+    int64_t n = elements / rows / 1024 * 1024;
     if (n < 1024) n = 1024;
     return n < vocab ? n : vocab;
 }
 
+// Tiles of 256 x 256 reach the highest rate (a fragment read from LDS feeds
+// four products) where there is one for every compute unit; below that tiles of
+// 128 x 128, two workgroups a compute unit; few tokens take tiles of 256 x 32,
+// which stream the other operand.
+int shape_of(int64_t tiles, int64_t tokens) {
+    return tokens <= Narrow::BN ? kNarrow : tiles >= 256 ? kLarge : kMedium;
+}
+
 // Sizes of a call and its workspace, cut into 256-byte aligned arrays.
 struct Plan {
-    bool copy;                 // rows of hidden and weight are copied to aligned ones
-    int64_t dimp, tokp;        // padded row lengths (elements)
+    bool copy;                 // rows of weight (forward: of hidden too) are copied to aligned ones
+    int64_t dimp, ldsum;       // padded row lengths (elements)
     int64_t piece, piecep;     // words of a piece
     int64_t parts, part_words;
     int shape, grad_shape;     // of the logits' and the gradients' tiles
-    size_t at_part, at_h, at_w, at_ht, at_wt, at_p, at_pt, at_sum, at_scale, bytes;
+    int runs;                  // of k in dhidden's product
+    bool sums;                 // dhidden is summed in float32 over pieces and runs
+    size_t at_part, at_h, at_w, at_p, at_sum, at_scale, bytes;
 };
 
 Plan make_plan(const LossArgs &a, bool bwd, bool aligned) {
@@ -467,43 +623,51 @@ Plan make_plan(const LossArgs &a, bool bwd, bool aligned) {
     const int64_t esz = a.io == IO_F32 ? 4 : 2, unit = 16 / esz;
     p.copy = !aligned || a.dim % unit != 0;
     p.dimp = round_up(a.dim, unit);
-    p.tokp = round_up(a.tokens, unit);
     const auto add = [&](int64_t bytes) {
         const size_t at = p.bytes;
         p.bytes += static_cast<size_t>(round_up(bytes, 256));
         return at;
     };
-    p.piece = piece_words(bwd || a.tokens > p.dimp ? a.tokens : p.dimp, a.vocab);
-    p.piecep = round_up(p.piece, unit);
-    if (p.copy) {
-        p.at_h = add(a.tokens * p.dimp * esz);
-        p.at_w = add(p.piece * p.dimp * esz);
-    }
+    const auto tiles = [](int64_t m, int64_t n) { return ceil_div(m, Large::BM) * ceil_div(n, Large::BN); };
     if (!bwd) {
-        p.shape = a.tokens <= 32 ? 2 : ceil_div(a.vocab, 256) * ceil_div(a.tokens, 256) >= 256 ? 0 : 1;
-        p.part_words = p.shape == 0 ? Large::WM : p.shape == 1 ? Medium::WM : Narrow::WM;
+        p.piece = p.copy ? piece_words(int64_t(1) << 27, p.dimp, a.vocab)
+                         : piece_words(int64_t(1) << 37, a.tokens + 128, a.vocab);
+        p.shape = shape_of(tiles(p.piece, a.tokens), a.tokens);
+        p.part_words = p.shape == kLarge ? Large::WM : p.shape == kMedium ? Medium::WM : Narrow::WM;
         p.parts = a.vocab / p.piece * ceil_div(p.piece, p.part_words) + ceil_div(a.vocab % p.piece, p.part_words);
         p.at_part = add(p.parts * a.tokens * 8);
+        p.at_h = add(p.copy ? a.tokens * p.dimp * esz : 0);
+        p.at_w = add(p.copy ? p.piece * p.dimp * esz : 0);
         return p;
     }
-    const auto tiles = [](int64_t m, int64_t n) { return ceil_div(m, 256) * ceil_div(n, 256); };
-    p.shape = tiles(p.piece, a.tokens) >= 256 ? 0 : 1;
-    p.grad_shape = tiles(a.dim, a.tokens) + tiles(a.dim, p.piece) >= 256 ? 0 : 1;
-    p.at_ht = add(a.dim * p.tokp * esz);
-    p.at_wt = add(a.dim * p.piecep * esz);
+    p.piece = piece_words(int64_t(1) << 27, a.tokens, a.vocab);
+    p.piecep = round_up(p.piece, unit);
+    p.shape = shape_of(tiles(p.piece, a.tokens), a.tokens);
+    p.grad_shape = shape_of(tiles(a.dim, a.tokens) + tiles(a.dim, p.piece), a.tokens);
+    // A tile of dhidden sums over the piece's words, one of dweight over the
+    // tokens: dhidden's k is cut into runs about twice as long as dweight's.
+    const int64_t run = 2 * a.tokens > 1024 ? 2 * a.tokens : 1024;
+    p.runs = static_cast<int>(ceil_div(p.piece, run) < 32 ? ceil_div(p.piece, run) : 32);
+    p.sums = p.runs > 1 || p.piece < a.vocab;
+    p.ldsum = round_up(a.dim, 4);
+    p.at_h = add(a.tokens * p.dimp * esz);
+    p.at_w = add(p.copy ? p.piece * p.dimp * esz : 0);
     p.at_p = add(a.tokens * p.piecep * esz);
-    p.at_pt = add(p.piece * p.tokp * esz);
     p.at_scale = add(4);
-    if (p.piece < a.vocab) p.at_sum = add(a.tokens * a.dim * 4);
+    p.at_sum = add(p.sums ? p.runs * a.tokens * p.ldsum * 4 : 0);
     return p;
 }
 
 template <typename T>
-Rows rows_of(const T *q, int64_t ld, int64_t n) {
-    return Rows{reinterpret_cast<const unsigned char *>(q), ld * static_cast<int64_t>(sizeof(T)), static_cast<int>(n)};
+Rows rows_of(const T *q, int64_t ld, int64_t n, int64_t k) {
+    return Rows{reinterpret_cast<const unsigned char *>(q), ld * static_cast<int64_t>(sizeof(T)), static_cast<int>(n),
+                static_cast<int>(k)};
 }
 
-Problem problem(const Rows &A, const Rows &B, int64_t kbytes) { return Problem{A, B, kbytes, 0, 0}; }
+template <bool AX, bool BX, typename Epilogue>
+Job<Epilogue, AX, BX> job_of(const Rows &A, const Rows &B, const Epilogue &e) {
+    return Job<Epilogue, AX, BX>{Problem{A, B, 0, 0, 0, 0}, e};
+}
 
 template <typename T>
 hipError_t fwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_t stream) {
@@ -511,7 +675,7 @@ hipError_t fwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_
     const T *h = static_cast<const T *>(a.hidden);
     hipError_t e = hipSuccess;
     if (p.copy) {
-        e = align_rows(h, reinterpret_cast<T *>(base + p.at_h), a.tokens, a.dim, p.dimp, stream);
+        e = align_rows(h, reinterpret_cast<T *>(base + p.at_h), a.tokens, a.dim, p.dimp, nullptr, 0, stream);
         h = reinterpret_cast<const T *>(base + p.at_h);
     }
     int part0 = 0;
@@ -519,60 +683,75 @@ hipError_t fwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_
         const int64_t words = a.vocab - w0 < p.piece ? a.vocab - w0 : p.piece;
         const T *w = static_cast<const T *>(a.weight) + w0 * a.dim;
         if (p.copy) {
-            e = align_rows(w, reinterpret_cast<T *>(base + p.at_w), words, a.dim, p.dimp, stream);
+            e = align_rows(w, reinterpret_cast<T *>(base + p.at_w), words, a.dim, p.dimp, nullptr, 0, stream);
             w = reinterpret_cast<const T *>(base + p.at_w);
             if (e != hipSuccess) break;
         }
         const LossTile ep{part, a.loss, a.targets, static_cast<int>(a.tokens), static_cast<int>(words),
                           static_cast<int>(w0), part0};
-        e = products<T>(problem(rows_of(w, p.dimp, words), rows_of(h, p.dimp, a.tokens), p.dimp * sizeof(T)), Problem{}, ep,
-                        ep, p.shape, stream);
+        e = product<T>(job_of<false, false>(rows_of(w, p.dimp, words, p.dimp), rows_of(h, p.dimp, a.tokens, p.dimp), ep),
+                       p.shape, 1, stream);
         part0 += static_cast<int>(ceil_div(words, p.part_words));
     }
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(loss_join_kernel, dim3(static_cast<uint32_t>(ceil_div(a.tokens, 256))), dim3(256), 0, stream,
-                       part, part0, static_cast<int>(a.tokens), a.targets, a.ignore_index, a.vocab, a.loss, a.lse);
+    hipLaunchKernelGGL(loss_join_kernel, dim3(static_cast<uint32_t>(ceil_div(a.tokens, 64))), dim3(64 * kJoinSlices), 0,
+                       stream, part, part0, static_cast<int>(a.tokens), a.targets, a.ignore_index, a.vocab, a.loss,
+                       a.lse);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t bwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_t stream) {
-    T *pr = reinterpret_cast<T *>(base + p.at_p), *pt = reinterpret_cast<T *>(base + p.at_pt);
-    T *ht = reinterpret_cast<T *>(base + p.at_ht), *wt = reinterpret_cast<T *>(base + p.at_wt);
-    float *scale = reinterpret_cast<float *>(base + p.at_scale);
-    const T *h = static_cast<const T *>(a.hidden);
+    T *pr = reinterpret_cast<T *>(base + p.at_p), *h = reinterpret_cast<T *>(base + p.at_h);
+    float *scale = reinterpret_cast<float *>(base + p.at_scale), *sum = reinterpret_cast<float *>(base + p.at_sum);
     const int tokens = static_cast<int>(a.tokens), dim = static_cast<int>(a.dim);
+    const auto wide = [&](const void *q) {
+        return a.dim % 4 == 0 && reinterpret_cast<uintptr_t>(q) % (4 * sizeof(T)) == 0;
+    };
     hipLaunchKernelGGL(grad_scale_kernel, dim3(1), dim3(1024), 0, stream, a.dloss, a.targets, a.ignore_index, tokens,
                        scale);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess) e = transpose(h, ht, a.tokens, a.dim, p.tokp, a.targets, a.ignore_index, stream);
-    if (e == hipSuccess && p.copy) {
-        e = align_rows(h, reinterpret_cast<T *>(base + p.at_h), a.tokens, a.dim, p.dimp, stream);
-        h = reinterpret_cast<const T *>(base + p.at_h);
-    }
+    // hidden with the ignored tokens' rows zero: whatever they hold, times their
+    // p of 0, adds nothing to dweight
+    if (e == hipSuccess)
+        e = align_rows(static_cast<const T *>(a.hidden), h, a.tokens, a.dim, p.dimp, a.targets, a.ignore_index, stream);
     for (int64_t w0 = 0; w0 < a.vocab && e == hipSuccess; w0 += p.piece) {
         const int64_t words = a.vocab - w0 < p.piece ? a.vocab - w0 : p.piece;
         const int64_t wordsp = round_up(words, 16 / sizeof(T));
         const T *w = static_cast<const T *>(a.weight) + w0 * a.dim;
-        e = transpose<T>(w, wt, words, a.dim, wordsp, nullptr, 0, stream);
-        if (e == hipSuccess && p.copy) {
-            e = align_rows(w, reinterpret_cast<T *>(base + p.at_w), words, a.dim, p.dimp, stream);
+        if (p.copy) {
+            e = align_rows(w, reinterpret_cast<T *>(base + p.at_w), words, a.dim, p.dimp, nullptr, 0, stream);
             w = reinterpret_cast<const T *>(base + p.at_w);
+            if (e != hipSuccess) break;
         }
-        if (e != hipSuccess) break;
-        const ProbTile<T> prob{pr, pt, wordsp, p.tokp, a.targets, a.lse, a.dloss, scale, a.ignore_index, a.vocab,
+        const ProbTile<T> prob{pr, wordsp, a.targets, a.lse, a.dloss, scale, a.ignore_index, a.vocab,
                                tokens, static_cast<int>(words), static_cast<int>(w0)};
-        e = products<T>(problem(rows_of(w, p.dimp, words), rows_of(h, p.dimp, a.tokens), p.dimp * sizeof(T)), Problem{}, prob,
-                        prob, p.shape, stream);
+        e = product<T>(job_of<false, false>(rows_of(w, p.dimp, words, p.dimp), rows_of(h, p.dimp, a.tokens, p.dimp), prob),
+                       p.shape, 1, stream);
         if (e != hipSuccess) break;
-        float *sum = p.piece < a.vocab ? reinterpret_cast<float *>(base + p.at_sum) : nullptr;
-        const GradTile<T> dh{sum, w0 + words >= a.vocab ? static_cast<T *>(a.dhidden) : nullptr, scale, a.dim, tokens,
-                             dim, w0 > 0};
-        const GradTile<T> dw{nullptr, static_cast<T *>(a.dweight) + w0 * a.dim, scale, a.dim, static_cast<int>(words),
-                             dim, false};
-        e = products<T>(problem(rows_of(wt, wordsp, a.dim), rows_of(pr, wordsp, a.tokens), wordsp * sizeof(T)),
-                        problem(rows_of(ht, p.tokp, a.dim), rows_of(pt, p.tokp, words), p.tokp * sizeof(T)), dh, dw,
-                        p.grad_shape, stream);
+        // dhidden: weight across k (the words), p along it; dweight: hidden and p
+        // across k (the tokens)
+        T *dwp = static_cast<T *>(a.dweight) + w0 * a.dim;
+        const GradTile<T> dh{p.sums ? sum : nullptr, p.ldsum, static_cast<T *>(a.dhidden), scale, tokens, dim,
+                             w0 > 0, wide(a.dhidden)};
+        const GradTile<T> dw{nullptr, 0, dwp, scale, static_cast<int>(words), dim, false, wide(dwp)};
+        const auto jh = job_of<true, false>(rows_of(w, p.dimp, a.dim, words), rows_of(pr, wordsp, a.tokens, words), dh);
+        const auto jw = job_of<true, true>(rows_of(h, p.dimp, a.dim, a.tokens), rows_of(pr, wordsp, words, a.tokens), dw);
+        // a last, shorter piece keeps the runs, so that they add to the same sums
+        if (p.grad_shape == kNarrow) {
+            e = product_as<T, Narrow>(jh, p.runs, stream);
+            if (e == hipSuccess) e = product_as<T, Medium>(jw, 1, stream);
+        } else if (p.grad_shape == kLarge) {
+            e = product2_as<T, Large>(jh, p.runs, jw, stream);
+        } else {
+            e = product2_as<T, Medium>(jh, p.runs, jw, stream);
+        }
+    }
+    if (e == hipSuccess && p.sums) {
+        const int64_t blocks = ceil_div(a.tokens * a.dim, 256 * 4);
+        hipLaunchKernelGGL(add_runs_kernel<T>, dim3(static_cast<uint32_t>(blocks < 8192 ? blocks : 8192)), dim3(256), 0,
+                           stream, sum, p.runs, a.tokens, dim, p.ldsum, scale, static_cast<T *>(a.dhidden));
+        e = hipGetLastError();
     }
     return e;
 }
