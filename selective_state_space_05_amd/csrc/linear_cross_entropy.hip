@@ -103,6 +103,7 @@ struct Operand {
     static constexpr int kLoads = N * kRowBytes / 1024;              // instructions of a step
     static constexpr int kLine = ACROSS ? N * static_cast<int>(sizeof(T)) : kRowBytes;   // bytes of a line in LDS
     static constexpr int kLineChunks = kLine / 16, kLines = 1024 / kLine;               // lines of one instruction
+    static constexpr int kFragmentReads = !ACROSS ? 1 : sizeof(T) == 2 ? 2 : 4;
     typedef __attribute__((address_space(3))) void Lds;
 
     const unsigned char *base;
@@ -111,12 +112,13 @@ struct Operand {
     uint32_t ld, lane_off;
     int chunk, chunks;           // this lane's chunk of a line; chunks of k in all (not ACROSS)
 
-    // Chunks of line l are permuted by this.  Along k, lanes read one chunk of
-    // consecutive lines; across it (bfloat16), 16 lanes read two chunks of four
-    // lines.
+    // Chunks of line l are permuted by this, so that the lanes served together (256
+    // bytes a cycle) cover all 64 banks.  Along k, 16 lanes read one chunk of 16
+    // lines, four to 256 bytes; across it (bfloat16), 32 lanes read four chunks of
+    // four lines.
     static __device__ __forceinline__ int swizzle(int l) {
-        if (!ACROSS) return (l / 2) % kChunks;
-        return sizeof(T) == 2 ? (2 * (l % 4)) & (kLineChunks - 1) : 0;
+        if (!ACROSS) return (l / 4) % kChunks;
+        return sizeof(T) == 2 ? (4 * (l % 4)) & (kLineChunks - 1) : 0;
     }
 
     __device__ __forceinline__ void init(const Rows &R, int first, int wave, int lane) {
@@ -146,7 +148,7 @@ struct Operand {
     }
     // Load instruction q (of kLoads) of a step into `to`; k past the end reads as
     // zero.  Across k, steps are asked for one after the other.
-    __device__ __forceinline__ void load(int step, int q, unsigned char *to) const {
+    __device__ __forceinline__ void load(int step, int q, unsigned char *__restrict__ to) const {
         if (ACROSS)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds *)(to + q * 1024), 16, lane_off, q * kLines * ld, 0, 0);
         else
@@ -163,8 +165,10 @@ struct Operand {
     __device__ __forceinline__ void end_step() { seek(1); }
 
     // The 16 bytes of k that this lane holds of row `row` + lane % 32 in half
-    // `half` of the step at `from`.
-    static __device__ __forceinline__ u32x4 fragment(const unsigned char *from, int row, int half, int lane) {
+    // `half` of the step at `from`.  __restrict__ here and in load(): a stage is
+    // read only after its loads were waited for, and without the promise the
+    // compiler waits for every load under way before a transposing read.
+    static __device__ __forceinline__ u32x4 fragment(const unsigned char *__restrict__ from, int row, int half, int lane) {
         if constexpr (!ACROSS) {
             const int c = (2 * half + lane / 32) ^ swizzle(lane % 32);
             return *reinterpret_cast<const u32x4 *>(from + (lane % 32) * kRowBytes + c * 16 + row * kRowBytes);
@@ -175,8 +179,7 @@ struct Operand {
             typedef short s16x4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s16x4 LdsRow;
             const int i = lane % 16, line = 8 * (lane / 32) + i / 4, x = 2 * (lane / 16 % 2) + i % 4 / 2;
-            const int odd = row / 32 % 2;                    // rows go in pairs of 32: eight chunks
-            const int c = (row / 64) * 8 + ((4 * odd + x) ^ swizzle(line));
+            const int c = row / 128 * 16 + ((row / 32 % 4 * 4 + x) ^ swizzle(line));   // 32 rows: four chunks
             const unsigned char *at = from + (16 * half + line) * kLine + c * 16 + i % 2 * 8;
             const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)at));
             const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)(at + 4 * kLine)));
@@ -251,14 +254,30 @@ __device__ __forceinline__ void product_tile(const Rows &A, const Rows &B, int f
     read(0, 0);
     read(0, 1);
     multiply(0);
+    // The compiler would sink the fragment reads to just before their products
+    // (fewer registers, and every wait shows): they go first, then the products
+    // with the loads among them.
+    constexpr int kReads = I * OpA::kFragmentReads + J * OpB::kFragmentReads;
+    constexpr int kProducts = I * J * (sizeof(T) == 2 ? 1 : 4), kMine = kMineA + kMineB;
+    enum { kMfma = 0x8, kVmem = 0x20, kDsRead = 0x100 };
     for (int step = 1; step < steps; ++step) {
         wait_and_meet<kAhead>();
-        load(step + kStages - 1);
         read(step, 0);
+        load(step + kStages - 1);
         multiply(1);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, kReads, 0);
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            __builtin_amdgcn_sched_group_barrier(kMfma, kProducts / kMine, 0);
+            __builtin_amdgcn_sched_group_barrier(kVmem, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(kMfma, kProducts, 0);
         __builtin_amdgcn_sched_barrier(0);
         read(step, 1);
         multiply(0);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, kReads, 1);
+        __builtin_amdgcn_sched_group_barrier(kMfma, kProducts, 1);
+        __builtin_amdgcn_sched_barrier(0);
     }
     multiply(1);
 }
