@@ -302,11 +302,13 @@ __device__ __forceinline__ void run_tile(const J &job, int id, unsigned char *ld
     const int n = job.p.mt * job.p.nt, split = id / n;
     tile_of(id - split * n, n, job.p.mt, job.p.nt, &mi, &ni);
     const int m0 = __builtin_amdgcn_readfirstlane(mi * Shape::BM), n0 = __builtin_amdgcn_readfirstlane(ni * Shape::BN);
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wm = (wave % Shape::waves_m) * Shape::WM, wn = (wave / Shape::waves_m) * Shape::WN;
+    // what the epilogue reads of its columns is loaded before the products
+    const auto columns = job.e.template begin<Shape>(m0 + wm, n0 + wn, lane);
     f32x16 acc[Shape::I][Shape::J];
     product_tile<T, Shape, J::kAX, J::kBX>(job.p.A, job.p.B, split * job.p.steps, job.p.steps, m0, n0, lds, acc);
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int wm = (wave % Shape::waves_m) * Shape::WM, wn = (wave / Shape::waves_m) * Shape::WN;
-    job.e.template tile<Shape>(m0 + wm, n0 + wn, split, lane, acc, lds + wave * (Shape::lds / kWaves));
+    job.e.template tile<Shape>(m0 + wm, n0 + wn, split, lane, columns, acc, lds + wave * (Shape::lds / kWaves));
 }
 
 // A grid of one or two kinds of product: the first one's tiles, then the second's.
@@ -344,44 +346,62 @@ struct LossTile {
     const int64_t *targets;
     int tokens, words, word0;  // words of this piece; word0: the piece's first
     int part0;                 // first part of this piece
+    // The target's place among a wave's words, or -1.
+    template <int J>
+    struct Columns {
+        int mine[J];
+    };
     template <typename Shape>
-    __device__ __forceinline__ void tile(int m, int n, int, int lane, f32x16 (&acc)[Shape::I][Shape::J], unsigned char *) const {
-        each_column<Shape>(acc, [&](int j, const f32x16(&c)[Shape::I]) { column(m, n + 32 * j + lane % 32, lane, c); });
-    }
-    template <int I>
-    __device__ __forceinline__ void column(int m, int t, int lane, const f32x16 (&acc)[I]) const {
-        if (m >= words) return;
-        const bool there = t < tokens;
-        // the target's place among this lane's words, if it is one of them
-        const int64_t target = there ? targets[t] - word0 - m : -1;
-        const int mine = target >= 0 && target < min(32 * I, words - m) ? static_cast<int>(target) : -1;
-        const bool all = m + 32 * I <= words;
-        float top = -INFINITY;
+    __device__ __forceinline__ Columns<Shape::J> begin(int m, int n, int lane) const {
+        Columns<Shape::J> c;
 #pragma unroll
-        for (int i = 0; i < I; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                top = fmaxf(top, all || m + 32 * i + acc_row(e, lane) < words ? acc[i][e] : -INFINITY);
-        if (__any(mine >= 0)) {
-            float hit = 0.0f;
-#pragma unroll
-            for (int i = 0; i < I; ++i)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) hit = 32 * i + acc_row(e, lane) == mine ? acc[i][e] : hit;
-            if (mine >= 0 && mine / 4 % 2 == lane / 32) target_logit[t] = hit;
+        for (int j = 0; j < Shape::J; ++j) {
+            const int t = n + 32 * j + lane % 32;
+            const int64_t target = t < tokens ? targets[t] - word0 - m : -1;
+            c.mine[j] = target >= 0 && target < min(Shape::WM, words - m) ? static_cast<int>(target) : -1;
         }
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float ref = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f;
+        return c;
+    }
+    template <typename Shape>
+    __device__ __forceinline__ void tile(int m, int n, int, int lane, const Columns<Shape::J> &columns,
+                                         f32x16 (&acc)[Shape::I][Shape::J], unsigned char *) const {
+        if (m >= words) return;
+        const bool all = m + Shape::WM <= words;
 #pragma unroll
-        for (int i = 0; i < I; ++i)
+        for (int j = 0; j < Shape::J; ++j) {
+            const int t = n + 32 * j + lane % 32, mine = columns.mine[j];
+            if (!all) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float x = fast_exp2((acc[i][e] - ref) * kLog2e);
-                sum += all || m + 32 * i + acc_row(e, lane) < words ? x : 0.0f;
+                for (int i = 0; i < Shape::I; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (m + 32 * i + acc_row(e, lane) >= words) acc[i][j][e] = -INFINITY;
             }
-        sum += __shfl_xor(sum, 32);
-        if (there && lane < 32) part[static_cast<int64_t>(part0 + m / (32 * I)) * tokens + t] = make_float2(top, sum);
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < Shape::I; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
+            if (__any(mine >= 0)) {
+                float hit = 0.0f;
+#pragma unroll
+                for (int i = 0; i < Shape::I; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) hit = 32 * i + acc_row(e, lane) == mine ? acc[i][j][e] : hit;
+                if (mine >= 0 && mine / 4 % 2 == lane / 32) target_logit[t] = hit;
+            }
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < Shape::I; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sum[e % 4] += fast_exp2((acc[i][j][e] - ref) * kLog2e);
+            float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            s += __shfl_xor(s, 32);
+            if (t < tokens && lane < 32)
+                part[static_cast<int64_t>(part0 + m / Shape::WM) * tokens + t] = make_float2(top, s);
+        }
     }
 };
 
@@ -466,22 +486,40 @@ struct ProbTile {
     // neighbours'; through the wave's part of LDS (whose loads are done) whole
     // rows of the tile go out instead: 646 us against 1046 us for 8192 x 16384
     // logits of width 2560 with 8-byte stores.
+    // A token's reference, factor and, if it is among a wave's words, its target.
+    template <int J>
+    struct Columns {
+        float ref[J], g[J];
+        int mine[J];
+        bool live[J];
+    };
     template <typename Shape>
-    __device__ __forceinline__ void tile(int m, int n, int, int lane, f32x16 (&acc)[Shape::I][Shape::J],
-                                         unsigned char *lds) const {
+    __device__ __forceinline__ Columns<Shape::J> begin(int m, int n, int lane) const {
+        Columns<Shape::J> c;
+        const float by = *scale;
+#pragma unroll
+        for (int j = 0; j < Shape::J; ++j) {
+            const int t = n + 32 * j + lane % 32, at = min(t, tokens - 1);
+            const int64_t target = targets[at], hit = target - word0 - m;
+            c.live[j] = t < tokens && target != ignore;
+            c.ref[j] = c.live[j] ? lse[at] : 0.0f;
+            c.g[j] = c.live[j] ? dloss[at] / by : 0.0f;
+            if (c.live[j] && (target < 0 || target >= vocab)) c.g[j] = NAN;
+            c.mine[j] = hit >= 0 && hit < Shape::WM ? static_cast<int>(hit) : -1;
+        }
+        return c;
+    }
+    template <typename Shape>
+    __device__ __forceinline__ void tile(int m, int n, int, int lane, const Columns<Shape::J> &columns,
+                                         f32x16 (&acc)[Shape::I][Shape::J], unsigned char *lds) const {
         constexpr bool kStaged = sizeof(T) == 2;
         constexpr int kRow = Shape::WM * 2, kRowChunks = kRow / 16;
         if (kStaged) wait_and_meet<0>();
         each_column<Shape>(acc, [&](int j, const f32x16(&c)[Shape::I]) {
             const int r = 32 * j + lane % 32, t = n + r;
-            const bool there = t < tokens;
-            const int64_t target = there ? targets[t] : ignore;
-            const bool live = target != ignore;
-            const float ref = live ? lse[t] : 0.0f;
-            float g = live ? dloss[t] / *scale : 0.0f;
-            if (live && (target < 0 || target >= vocab)) g = NAN;
-            const int64_t hit = target - word0 - m;
-            const int mine = hit >= 0 && hit < Shape::WM ? static_cast<int>(hit) : -1;
+            const bool there = t < tokens, live = columns.live[j];
+            const float ref = columns.ref[j], g = columns.g[j];
+            const int mine = columns.mine[j];
             T *row = p + static_cast<int64_t>(t) * ldp + m;
 #pragma unroll
             for (int i = 0; i < Shape::I; ++i)
@@ -525,8 +563,11 @@ struct GradTile {
     const float *scale;        // out is the sum times this
     int rows, cols;            // of the gradient
     bool add, wide;            // sum holds earlier pieces; rows of out take stores of four
+    struct Nothing {};
     template <typename Shape>
-    __device__ __forceinline__ void tile(int m, int n, int run, int lane, f32x16 (&acc)[Shape::I][Shape::J],
+    __device__ __forceinline__ Nothing begin(int, int, int) const { return {}; }
+    template <typename Shape>
+    __device__ __forceinline__ void tile(int m, int n, int run, int lane, Nothing, f32x16 (&acc)[Shape::I][Shape::J],
                                          unsigned char *) const {
         each_column<Shape>(acc, [&](int j, const f32x16(&c)[Shape::I]) { column(m, n + 32 * j + lane % 32, run, lane, c); });
     }
