@@ -484,7 +484,7 @@ struct ProbTile {
     int tokens, words, word0;
     // bfloat16: a lane's four words of a token are 8 bytes, 32 tokens apart from its
     // neighbours'; through the wave's part of LDS (whose loads are done) whole
-    // rows of the tile go out instead: 646 us against 1046 us for 8192 x 16384
+    // rows of the tile go out instead: 682 us against 1046 us for 8192 x 16384
     // logits of width 2560 with 8-byte stores.
     // A token's reference, factor and, if it is among a wave's words, its target.
     template <int J>
