@@ -405,26 +405,36 @@ struct LossTile {
     }
 };
 
-// Joins the parts of a token: 64 tokens a workgroup, 16 slices of the parts.
-constexpr int kJoinSlices = 16;
+// Joins the parts of a token: 16 tokens a workgroup, 64 slices of the parts (a
+// slice is a quarter wave; few tokens have many parts).
+constexpr int kJoinTokens = 16, kJoinSlices = 64;
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
     const float top = fmaxf(a.x, b.x), ref = top == -INFINITY ? 0.0f : top;
     return make_float2(top, a.y * fast_exp2((a.x - ref) * kLog2e) + b.y * fast_exp2((b.x - ref) * kLog2e));
 }
-__global__ __launch_bounds__(64 * kJoinSlices) void loss_join_kernel(const float2 *__restrict__ part, int parts, int tokens,
-                                                                     const int64_t *__restrict__ targets,
-                                                                     int64_t ignore, int64_t vocab,
-                                                                     float *__restrict__ loss,
-                                                                     float *__restrict__ lse) {
-    __shared__ float2 sh[kJoinSlices][64];
-    const int lane = threadIdx.x % 64, slice = threadIdx.x / 64, t = blockIdx.x * 64 + lane;
+__global__ __launch_bounds__(kJoinTokens * kJoinSlices) void loss_join_kernel(
+    const float2 *__restrict__ part, int parts, int tokens, const int64_t *__restrict__ targets, int64_t ignore,
+    int64_t vocab, float *__restrict__ loss, float *__restrict__ lse) {
+    __shared__ float2 sh[kJoinSlices / 4][kJoinTokens];
+    const int lane = threadIdx.x % kJoinTokens, slice = threadIdx.x / kJoinTokens;
+    const int t = blockIdx.x * kJoinTokens + lane, at = min(t, tokens - 1);
     float2 s = make_float2(-INFINITY, 0.0f);
-    if (t < tokens)
-        for (int k = slice; k < parts; k += kJoinSlices) s = join(s, part[static_cast<int64_t>(k) * tokens + t]);
-    sh[slice][lane] = s;
+    constexpr int kAhead = 4;   // loads under way at a time
+    for (int k = slice; k < parts; k += kAhead * kJoinSlices) {
+        float2 f[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            f[u] = part[static_cast<int64_t>(min(k + u * kJoinSlices, parts - 1)) * tokens + at];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (k + u * kJoinSlices < parts) s = join(s, f[u]);
+    }
+#pragma unroll
+    for (int m = kJoinTokens; m < 64; m *= 2) s = join(s, make_float2(__shfl_xor(s.x, m), __shfl_xor(s.y, m)));
+    if (threadIdx.x % 64 < kJoinTokens) sh[slice / 4][lane] = s;
     __syncthreads();
     if (slice > 0 || t >= tokens) return;
-    for (int k = 1; k < kJoinSlices; ++k) s = join(s, sh[k][lane]);
+    for (int k = 1; k < kJoinSlices / 4; ++k) s = join(s, sh[k][lane]);
     const float l = s.x + fast_log2(s.y) * kLn2;
     if (lse) lse[t] = l;
     const int64_t target = targets[t];
@@ -604,33 +614,74 @@ struct GradTile {
     }
 };
 
-// out[n][d] = scale * sum over the runs of sum[run][n][d].
+// out[r][c] = scale * sum over the runs of sum[run][r][c]: a wave per row and 64
+// vectors of four.
 template <typename T>
 __global__ __launch_bounds__(256) void add_runs_kernel(const float *__restrict__ sum, int runs, int64_t rows, int cols,
                                                        int64_t ldsum, const float *__restrict__ scale,
-                                                       T *__restrict__ out) {
+                                                       T *__restrict__ out, bool wide) {
+    const int c = (blockIdx.x * 64 + threadIdx.x % 64) * 4;
+    if (c >= cols) return;
     const float by = *scale;
-    const int64_t n = rows * cols;
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k < n;
-         k += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = k / cols, c = k - r * cols;
-        float x = 0.0f;
-        for (int i = 0; i < runs; ++i) x += sum[(i * rows + r) * ldsum + c];
-        Io<T>::store(out, k, x * by);
+    for (int64_t r = blockIdx.y * 4 + threadIdx.x / 64; r < rows; r += 4 * gridDim.y) {
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+        constexpr int kAhead = 8;   // loads under way at a time
+        for (int i = 0; i < runs; i += kAhead) {
+            f32x4 f[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                f[u] = *reinterpret_cast<const f32x4 *>(sum + (min(i + u, runs - 1) * rows + r) * ldsum + c);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (i + u < runs)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] += f[u][e];
+        }
+        const float y[4] = {x[0] * by, x[1] * by, x[2] * by, x[3] * by};
+        T *to = out + r * cols + c;
+        if (wide) {
+            store4(to, y);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < cols) Io<T>::store(to, e, y[e]);
+        }
     }
 }
 
-// Copy of rows [0, rows) x [0, cols) with rows `ldo` elements apart, zero past
-// the columns and in rows whose target is `ignore` (targets may be null).
+// Copy of rows [0, rows) x [0, cols) with rows `ldo` elements apart (whole
+// chunks of 16 bytes), zero past the columns and in rows whose target is
+// `ignore` (targets may be null): a wave per row, four chunks of a lane under
+// way at a time, read unaligned.
 template <typename T>
 __global__ __launch_bounds__(256) void align_rows_kernel(const T *__restrict__ in, T *__restrict__ out, int64_t rows,
-                                                         int64_t cols, int64_t ldo,
+                                                         int cols, int64_t ldo,
                                                          const int64_t *__restrict__ targets, int64_t ignore) {
-    const int64_t n = rows * ldo;
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k < n;
-         k += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = k / ldo, c = k - r * ldo;
-        out[k] = c < cols && !(targets && targets[r] == ignore) ? in[r * cols + c] : T{};
+    constexpr int kUnit = 16 / sizeof(T), kAhead = 4;
+    typedef u32x4 Any __attribute__((aligned(2)));
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64; r < rows;
+         r += static_cast<int64_t>(gridDim.x) * 4) {
+        const int n = targets && targets[r] == ignore ? 0 : cols;
+        const T *from = in + r * cols;
+        T *to = out + r * ldo;
+        for (int c = threadIdx.x % 64 * kUnit; c < ldo; c += kAhead * 64 * kUnit) {
+            u32x4 f[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int at = c + u * 64 * kUnit;
+                f[u] = u32x4{0, 0, 0, 0};
+                if (at + kUnit <= n) {
+                    f[u] = *reinterpret_cast<const Any *>(from + at);
+                } else {
+                    T part[kUnit] = {};
+                    for (int e = 0; at + e < n; ++e) part[e] = from[at + e];
+                    f[u] = __builtin_bit_cast(u32x4, part);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (c + u * 64 * kUnit < ldo) *reinterpret_cast<u32x4 *>(to + c + u * 64 * kUnit) = f[u];
+        }
     }
 }
 
@@ -643,7 +694,11 @@ bool on_16(const LossArgs &a) {
 
 typedef Tile<256, 256, 128, 128> Large;
 typedef Tile<128, 128, 64, 64> Medium;
-typedef Tile<256, 32, 64, 32> Narrow;    // few tokens
+typedef Tile<128, 64, 64, 32> Small;
+#ifndef NR
+#define NR 128, 32, 32, 32
+#endif
+typedef Tile<NR> Narrow;    // few tokens
 
 // Tiles and runs of a product: `splits` runs of k, whole steps each.
 template <typename T, typename Shape>
@@ -671,12 +726,16 @@ hipError_t product_as(J0 j0, int splits, hipStream_t stream) {
     return launch_tiles(product_kernel<T, Shape, J0>, n, Shape::lds, stream, j0);
 }
 
-enum : int { kLarge, kMedium, kNarrow };
+enum : int { kLarge, kMedium, kSmall, kNarrow };
 
 template <typename T, typename J0>
 hipError_t product(const J0 &j0, int shape, int splits, hipStream_t stream) {
-    if (shape == kLarge) return product_as<T, Large>(j0, splits, stream);
-    if (shape == kMedium) return product_as<T, Medium>(j0, splits, stream);
+    if constexpr (sizeof(T) == 4) {
+        if (shape == kSmall) return product_as<T, Small>(j0, splits, stream);
+    } else {
+        if (shape == kLarge) return product_as<T, Large>(j0, splits, stream);
+        if (shape == kMedium) return product_as<T, Medium>(j0, splits, stream);
+    }
     return product_as<T, Narrow>(j0, splits, stream);
 }
 
@@ -689,9 +748,9 @@ hipError_t product2_as(J0 j0, int splits, J1 j1, hipStream_t stream) {
 template <typename T>
 hipError_t align_rows(const T *in, T *out, int64_t rows, int64_t cols, int64_t ldo, const int64_t *targets,
                       int64_t ignore, hipStream_t stream) {
-    const int64_t blocks = ceil_div(rows * ldo, 256 * 4);
+    const int64_t blocks = ceil_div(rows, 4);
     hipLaunchKernelGGL(align_rows_kernel<T>, dim3(static_cast<uint32_t>(blocks < 65536 ? blocks : 65536)),
-                       dim3(256), 0, stream, in, out, rows, cols, ldo, targets, ignore);
+                       dim3(256), 0, stream, in, out, rows, static_cast<int>(cols), ldo, targets, ignore);
     return hipGetLastError();
 }
 
@@ -704,12 +763,10 @@ int64_t piece_words(int64_t elements, int64_t rows, int64_t vocab) {
     return n < vocab ? n : vocab;
 }
 
-// Tiles of 256 x 256 reach the highest rate (a fragment read from LDS feeds
-// four products) where there is one for every compute unit; below that tiles of
-// 128 x 128, two workgroups a compute unit; few tokens take tiles of 256 x 32,
-// which stream the other operand.
-int shape_of(int64_t tiles, int64_t tokens) {
-    return tokens <= Narrow::BN ? kNarrow : tiles >= 256 ? kLarge : kMedium;
+int shape_of(int io, int64_t tiles, int64_t tokens) {
+    if (tokens <= Narrow::BN) return kNarrow;
+    if (io == IO_F32) return kSmall;
+    return tiles >= 192 ? kLarge : kMedium;
 }
 
 // Sizes of a call and its workspace, cut into 256-byte aligned arrays.
@@ -738,8 +795,8 @@ Plan make_plan(const LossArgs &a, bool bwd, bool aligned) {
     if (!bwd) {
         p.piece = p.copy ? piece_words(int64_t(1) << 27, p.dimp, a.vocab)
                          : piece_words(int64_t(1) << 37, a.tokens + 128, a.vocab);
-        p.shape = shape_of(tiles(p.piece, a.tokens), a.tokens);
-        p.part_words = p.shape == kLarge ? Large::WM : p.shape == kMedium ? Medium::WM : Narrow::WM;
+        p.shape = shape_of(a.io, tiles(p.piece, a.tokens), a.tokens);
+        p.part_words = p.shape == kLarge ? Large::WM : p.shape == kMedium ? Medium::WM : p.shape == kSmall ? Small::WM : Narrow::WM;
         p.parts = a.vocab / p.piece * ceil_div(p.piece, p.part_words) + ceil_div(a.vocab % p.piece, p.part_words);
         p.at_part = add(p.parts * a.tokens * 8);
         p.at_h = add(p.copy ? a.tokens * p.dimp * esz : 0);
@@ -748,8 +805,8 @@ Plan make_plan(const LossArgs &a, bool bwd, bool aligned) {
     }
     p.piece = piece_words(int64_t(1) << 27, a.tokens, a.vocab);
     p.piecep = round_up(p.piece, unit);
-    p.shape = shape_of(tiles(p.piece, a.tokens), a.tokens);
-    p.grad_shape = shape_of(tiles(a.dim, a.tokens) + tiles(a.dim, p.piece), a.tokens);
+    p.shape = shape_of(a.io, tiles(p.piece, a.tokens), a.tokens);
+    p.grad_shape = shape_of(a.io, a.tokens > 512 ? tiles(a.dim, a.tokens) + tiles(a.dim, p.piece) : 0, a.tokens);
     // A tile of dhidden sums over the piece's words, one of dweight over the
     // tokens: dhidden's k is cut into runs about twice as long as dweight's.
     const int64_t run = 2 * a.tokens > 1024 ? 2 * a.tokens : 1024;
@@ -800,7 +857,8 @@ hipError_t fwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_
         part0 += static_cast<int>(ceil_div(words, p.part_words));
     }
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(loss_join_kernel, dim3(static_cast<uint32_t>(ceil_div(a.tokens, 64))), dim3(64 * kJoinSlices), 0,
+    hipLaunchKernelGGL(loss_join_kernel, dim3(static_cast<uint32_t>(ceil_div(a.tokens, kJoinTokens))),
+                       dim3(kJoinTokens * kJoinSlices), 0,
                        stream, part, part0, static_cast<int>(a.tokens), a.targets, a.ignore_index, a.vocab, a.loss,
                        a.lse);
     return hipGetLastError();
@@ -844,19 +902,30 @@ hipError_t bwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_
         const auto jh = job_of<true, false>(rows_of(w, p.dimp, a.dim, words), rows_of(pr, wordsp, a.tokens, words), dh);
         const auto jw = job_of<true, true>(rows_of(h, p.dimp, a.dim, a.tokens), rows_of(pr, wordsp, words, a.tokens), dw);
         // a last, shorter piece keeps the runs, so that they add to the same sums
-        if (p.grad_shape == kNarrow) {
-            e = product_as<T, Narrow>(jh, p.runs, stream);
-            if (e == hipSuccess) e = product_as<T, Medium>(jw, 1, stream);
-        } else if (p.grad_shape == kLarge) {
-            e = product2_as<T, Large>(jh, p.runs, jw, stream);
+        if constexpr (sizeof(T) == 4) {
+            if (p.grad_shape == kNarrow) {
+                e = product_as<T, Narrow>(jh, p.runs, stream);
+                if (e == hipSuccess) e = product_as<T, Small>(jw, 1, stream);
+            } else {
+                e = product2_as<T, Small>(jh, p.runs, jw, stream);
+            }
         } else {
-            e = product2_as<T, Medium>(jh, p.runs, jw, stream);
+            if (p.grad_shape == kNarrow) {
+                e = product_as<T, Narrow>(jh, p.runs, stream);
+                if (e == hipSuccess) e = product_as<T, Medium>(jw, 1, stream);
+            } else if (p.grad_shape == kLarge) {
+                e = product2_as<T, Large>(jh, p.runs, jw, stream);
+            } else {
+                e = product2_as<T, Medium>(jh, p.runs, jw, stream);
+            }
         }
     }
     if (e == hipSuccess && p.sums) {
-        const int64_t blocks = ceil_div(a.tokens * a.dim, 256 * 4);
-        hipLaunchKernelGGL(add_runs_kernel<T>, dim3(static_cast<uint32_t>(blocks < 8192 ? blocks : 8192)), dim3(256), 0,
-                           stream, sum, p.runs, a.tokens, dim, p.ldsum, scale, static_cast<T *>(a.dhidden));
+        const int64_t blocks = ceil_div(a.tokens, 4);
+        hipLaunchKernelGGL(add_runs_kernel<T>, dim3(static_cast<uint32_t>(ceil_div(dim, 256)),
+                                                    static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)),
+                           dim3(256), 0, stream, sum, p.runs, a.tokens, dim, p.ldsum, scale,
+                           static_cast<T *>(a.dhidden), wide(a.dhidden));
         e = hipGetLastError();
     }
     return e;
