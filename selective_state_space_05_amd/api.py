@@ -61,7 +61,7 @@ def _need_shape(t, name, shape):
     """Caller-supplied output buffers must have exactly the output's shape:
     the C ABI sees only their addresses, so a smaller buffer would be written
     past its end on the device."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
@@ -444,6 +444,15 @@ def _workspace(nbytes, dev):
     return t, t.data_ptr(), nbytes
 
 
+def _output(out, x):
+    """The caller's output like x, or a new one."""
+    if out is None:
+        return torch.empty_like(x)
+    _need_shape(out, "out", x.shape)
+    _need(out, "out", x.dtype, x.device)
+    return out
+
+
 def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
     """Layer norm over the last dimension on the GPU.
 
@@ -461,11 +470,9 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
     rows = x.numel() // dim if dim else 0
     for name, t in (("weight", weight), ("bias", bias)):
         _need(t, name, torch.float32, dev)
-        if t is not None and tuple(t.shape) != (dim,):
+        if t is not None and t.shape != (dim,):
             raise ValueError("%s must be (dim,)" % name)
-    _need_shape(out, "out", x.shape)
-    y = out if out is not None else torch.empty_like(x)
-    _need(y, "out", x.dtype, dev)
+    y = _output(out, x)
     mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
     rstd = torch.empty_like(mean)
     with _on_device(dev):
@@ -546,9 +553,7 @@ def gated_recurrence_fwd(x, r, i, lam, scale=8.0, h0=None, return_last_state=Tru
     for name, t in (("h0", h0), ("h_out", h_out)):
         _need(t, name, torch.float32, dev)
         _need_shape(t, name, (batch, dim))
-    _need_shape(out, "out", x.shape)
-    y = out if out is not None else torch.empty_like(x)
-    _need(y, "out", x.dtype, dev)
+    y = _output(out, x)
     h_last = None
     if return_last_state:
         h_last = h_out if h_out is not None else torch.empty(
@@ -603,9 +608,7 @@ def gated_recurrence_update(state, x, r, i, lam, scale=8.0, out=None):
         raise ValueError("state is required")
     _need(state, "state", torch.float32, dev)
     _need_shape(state, "state", x.shape)
-    _need_shape(out, "out", x.shape)
-    y = out if out is not None else torch.empty_like(x)
-    _need(y, "out", x.dtype, dev)
+    y = _output(out, x)
     with _on_device(dev):
         st = L.mssm_gated_recurrence_update(
             _ptr(state), _ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(scale), _ptr(y),
