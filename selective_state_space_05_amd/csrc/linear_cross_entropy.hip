@@ -486,6 +486,50 @@ __device__ __forceinline__ void store4(uint16_t *p, const float *f) {
     typedef __bf16 b4 __attribute__((ext_vector_type(4)));
     *reinterpret_cast<uint2 *>(p) = __builtin_bit_cast(uint2, __builtin_convertvector((f32x4{f[0], f[1], f[2], f[3]}), b4));
 }
+// The first n of a chunk's values at p, aligned as T is.
+template <typename T>
+__device__ __forceinline__ void store_chunk(T *p, u32x4 x, int n) {
+    typedef u32x4 Any __attribute__((aligned(2)));
+    constexpr int kUnit = 16 / sizeof(T);
+    if (n >= kUnit) {
+        *reinterpret_cast<Any *>(p) = x;
+    } else {
+        struct Values { T v[kUnit]; };
+        const Values y = __builtin_bit_cast(Values, x);
+#pragma unroll
+        for (int e = 0; e < kUnit; ++e)
+            if (e < n) p[e] = y.v[e];
+    }
+}
+
+// 32 columns of a wave's part of C on their way to rows of memory, through the
+// wave's part of LDS.  From the accumulator a lane would store four values of
+// its column, far from its neighbours'; out of LDS whole rows go, 16 bytes a lane.
+// (p in bfloat16, 8192 x 16384 logits of width 2560: 682 us against 1046 us.)
+template <typename T, typename Shape>
+struct Staged {
+    static constexpr int kUnit = 16 / sizeof(T), kRow = Shape::WM * sizeof(T), kRowChunks = kRow / 16;
+    static constexpr int kRows = 64 / kRowChunks;        // rows one store instruction covers
+    static_assert(32 * kRow <= Shape::lds / Shape::waves, "the wave's part holds them");
+    // Values v .. v + 3 of column r.  Chunks are permuted, so that the columns of
+    // the lanes served together fall into different banks.
+    static __device__ __forceinline__ void put(unsigned char *lds, int r, int v, const float *x) {
+        const int c = (v / kUnit) ^ (r % kRowChunks);
+        store4(reinterpret_cast<T *>(lds + r * kRow + c * 16) + v % kUnit, x);
+    }
+    // f(r, v, values v .. of column r) for the 16-byte chunks.
+    template <typename F>
+    static __device__ __forceinline__ void each(const unsigned char *lds, int lane, const F &f) {
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        const int c = lane % kRowChunks;
+#pragma unroll
+        for (int s = 0; s < 32 / kRows; ++s) {
+            const int r = s * kRows + lane / kRowChunks;
+            f(r, c * kUnit, *reinterpret_cast<const u32x4 *>(lds + r * kRow + (c ^ (r % kRowChunks)) * 16));
+        }
+        asm volatile("" : : : "memory");   // the next columns' writes stay behind
+    }
+};
 
 // p of a piece: p[token][word], rows ldp words apart (zero past the words).
 template <typename T>
@@ -496,10 +540,6 @@ struct ProbTile {
     const float *lse, *dloss, *scale;
     int64_t ignore, vocab;
     int tokens, words, word0;
-    // bfloat16: a lane's four words of a token are 8 bytes, 32 tokens apart from its
-    // neighbours'; through the wave's part of LDS (whose loads are done) whole
-    // rows of the tile go out instead: 682 us against 1046 us for 8192 x 16384
-    // logits of width 2560 with 8-byte stores.
     // A token's reference, factor and, if it is among a wave's words, its target.
     template <int J>
     struct Columns {
@@ -526,15 +566,12 @@ struct ProbTile {
     template <typename Shape>
     __device__ __forceinline__ void tile(int m, int n, int, int lane, const Columns<Shape::J> &columns,
                                          f32x16 (&acc)[Shape::I][Shape::J], unsigned char *lds) const {
-        constexpr bool kStaged = sizeof(T) == 2;
-        constexpr int kRow = Shape::WM * 2, kRowChunks = kRow / 16;
-        if (kStaged) wait_and_meet<0>();
+        typedef Staged<T, Shape> Out;
+        wait_and_meet<0>();
         each_column<Shape>(acc, [&](int j, const f32x16(&c)[Shape::I]) {
-            const int r = 32 * j + lane % 32, t = n + r;
-            const bool there = t < tokens, live = columns.live[j];
+            const bool live = columns.live[j];
             const float ref = columns.ref[j], g = columns.g[j];
             const int mine = columns.mine[j];
-            T *row = p + static_cast<int64_t>(t) * ldp + m;
 #pragma unroll
             for (int i = 0; i < Shape::I; ++i)
 #pragma unroll
@@ -546,24 +583,13 @@ struct ProbTile {
                         x[k] = (exp_of(c[i][e + k] - ref, T{}) - (v + k == mine ? 1.0f : 0.0f)) * g;
                         if (!live || m + v + k >= words) x[k] = 0.0f;
                     }
-                    if constexpr (kStaged)
-                        store4(reinterpret_cast<T *>(lds + r * kRow + ((v / 8) ^ (r % kRowChunks)) * 16 + v % 8 * 2), x);
-                    else if (there && m + v < ldp)
-                        store4(row + v, x);
+                    Out::put(lds, lane % 32, v, x);
                 }
+            Out::each(lds, lane, [&](int r, int v, u32x4 x) {
+                const int t = n + 32 * j + r;
+                if (t < tokens && m + v < ldp) *reinterpret_cast<u32x4 *>(p + static_cast<int64_t>(t) * ldp + m + v) = x;
+            });
         });
-        if constexpr (kStaged) {
-            constexpr int kRows = 64 / kRowChunks;       // rows one store instruction covers
-            const int c = lane % kRowChunks;
-            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-#pragma unroll
-            for (int s = 0; s < Shape::WN / kRows; ++s) {
-                const int r = s * kRows + lane / kRowChunks;
-                const u32x4 x = *reinterpret_cast<const u32x4 *>(lds + r * kRow + (c ^ (r % kRowChunks)) * 16);
-                if (n + r < tokens && m + 8 * c < ldp)
-                    *reinterpret_cast<u32x4 *>(p + static_cast<int64_t>(n + r) * ldp + m + 8 * c) = x;
-            }
-        }
     }
 };
 
@@ -576,45 +602,47 @@ struct GradTile {
     T *out;
     const float *scale;        // out is the sum times this
     int rows, cols;            // of the gradient
-    bool add, wide;            // sum holds earlier pieces; rows of out take stores of four
+    bool add;                  // sum holds earlier pieces
     struct Nothing {};
     template <typename Shape>
     __device__ __forceinline__ Nothing begin(int, int, int) const { return {}; }
     template <typename Shape>
     __device__ __forceinline__ void tile(int m, int n, int run, int lane, Nothing, f32x16 (&acc)[Shape::I][Shape::J],
-                                         unsigned char *) const {
-        each_column<Shape>(acc, [&](int j, const f32x16(&c)[Shape::I]) { column(m, n + 32 * j + lane % 32, run, lane, c); });
-    }
-    template <int I>
-    __device__ __forceinline__ void column(int m, int n, int run, int lane, const f32x16 (&acc)[I]) const {
-        if (n >= rows) return;
+                                         unsigned char *lds) const {
+        wait_and_meet<0>();
         const float by = sum ? 1.0f : *scale;
-        float *srow = sum + (static_cast<int64_t>(run) * rows + n) * ldsum + m;
-        T *orow = out + static_cast<int64_t>(n) * cols + m;
+        const auto put = [&](auto out, const f32x16(&c)[Shape::I]) {
 #pragma unroll
-        for (int i = 0; i < I; ++i)
+            for (int i = 0; i < Shape::I; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const int d = 32 * i + acc_row(e, lane);
-                if (m + d >= cols) continue;
-                float x[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = acc[i][e + k] * by;
-                if (sum) {
-                    if (add) {
-                        const f32x4 old = *reinterpret_cast<const f32x4 *>(srow + d);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) x[k] += old[k];
-                    }
-                    store4(srow + d, x);
-                } else if (wide) {
-                    store4(orow + d, x);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (m + d + k < cols) Io<T>::store(orow, d + k, x[k]);
+                for (int e = 0; e < 16; e += 4) {
+                    const float x[4] = {c[i][e] * by, c[i][e + 1] * by, c[i][e + 2] * by, c[i][e + 3] * by};
+                    decltype(out)::put(lds, lane % 32, 32 * i + acc_row(e, lane), x);
                 }
+        };
+        each_column<Shape>(acc, [&](int j, const f32x16(&c)[Shape::I]) {
+            if (sum) {
+                typedef Staged<float, Shape> Out;
+                put(Out(), c);
+                Out::each(lds, lane, [&](int r, int d, u32x4 x) {
+                    if (n + 32 * j + r >= rows || m + d >= cols) return;
+                    f32x4 *to = reinterpret_cast<f32x4 *>(sum + (static_cast<int64_t>(run) * rows + n + 32 * j + r) * ldsum + m + d);
+                    f32x4 y = __builtin_bit_cast(f32x4, x);
+                    if (add) {
+                        const f32x4 old = *to;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y[k] += old[k];
+                    }
+                    *to = y;
+                });
+            } else {
+                typedef Staged<T, Shape> Out;
+                put(Out(), c);
+                Out::each(lds, lane, [&](int r, int d, u32x4 x) {
+                    if (n + 32 * j + r < rows) store_chunk(out + static_cast<int64_t>(n + 32 * j + r) * cols + m + d, x, cols - m - d);
+                });
             }
+        });
     }
 };
 
@@ -623,7 +651,7 @@ struct GradTile {
 template <typename T>
 __global__ __launch_bounds__(256) void add_runs_kernel(const float *__restrict__ sum, int runs, int64_t rows, int cols,
                                                        int64_t ldsum, const float *__restrict__ scale,
-                                                       T *__restrict__ out, bool wide) {
+                                                       T *__restrict__ out) {
     const int c = (blockIdx.x * 64 + threadIdx.x % 64) * 4;
     if (c >= cols) return;
     const float by = *scale;
@@ -643,7 +671,7 @@ __global__ __launch_bounds__(256) void add_runs_kernel(const float *__restrict__
         }
         const float y[4] = {x[0] * by, x[1] * by, x[2] * by, x[3] * by};
         T *to = out + r * cols + c;
-        if (wide) {
+        if (cols % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0) {
             store4(to, y);
         } else {
 #pragma unroll
@@ -764,16 +792,15 @@ int64_t piece_words(int64_t elements, int64_t rows, int64_t vocab) {
     return n < vocab ? n : vocab;
 }
 
-// Bfloat16: tiles of 256 x 256 reach the highest rate (a fragment read from LDS
-// feeds four products: 8192 tokens forward 1.86 ms, in tiles of 128 x 128 2.50
-// ms) where they fill three quarters of the 256 compute units (252 of them 51
-// us against 58 us, 196 the same); below that tiles of 128 x 128, two
-// workgroups a compute unit.  Float32: one product takes eight times as long
-// for the same bytes, so that tiles of 128 x 64 feed it too, waste less at the
-// ends and run three workgroups a compute unit (517 tokens x 769 x 32003
-// backward 844 us, 128 x 128 939 us, 256 x 256 1222 us; 2048 tokens 3.05, 2.95
-// and 2.98 ms).  Few tokens take tiles of 128 x 32, which stream the other
-// operand.
+// Bfloat16: tiles of 256 x 256 reach the highest rate (8192 tokens x 2560 x 50021
+// forward 1.87 ms, in tiles of 128 x 128 2.50 ms) where they fill three quarters
+// of the 256 compute units (252 of them 51 us against 58 us, 196 the same); below
+// that tiles of 128 x 128, two workgroups a compute unit.  Float32: one product
+// takes eight times as long for the same bytes, so that tiles of 128 x 64 feed it
+// too, waste less at the ends and run three workgroups a compute unit (517 tokens
+// x 769 x 32003 backward 844 us, 128 x 128 939 us, 256 x 256 1222 us; 2048 tokens
+// 3.05, 2.95 and 2.98 ms).  Few tokens take tiles of 128 x 32, which stream the
+// other operand.
 int shape_of(int io, int64_t tiles, int64_t tokens) {
     if (tokens <= Narrow::BN) return kNarrow;
     if (io == IO_F32) return kSmall;
@@ -883,9 +910,6 @@ hipError_t bwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_
     T *pr = reinterpret_cast<T *>(base + p.at_p), *h = reinterpret_cast<T *>(base + p.at_h);
     float *scale = reinterpret_cast<float *>(base + p.at_scale), *sum = reinterpret_cast<float *>(base + p.at_sum);
     const int tokens = static_cast<int>(a.tokens), dim = static_cast<int>(a.dim);
-    const auto wide = [&](const void *q) {
-        return a.dim % 4 == 0 && reinterpret_cast<uintptr_t>(q) % (4 * sizeof(T)) == 0;
-    };
     hipLaunchKernelGGL(grad_scale_kernel, dim3(1), dim3(1024), 0, stream, a.dloss, a.targets, a.ignore_index, tokens,
                        scale);
     hipError_t e = hipGetLastError();
@@ -911,8 +935,8 @@ hipError_t bwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_
         // across k (the tokens)
         T *dwp = static_cast<T *>(a.dweight) + w0 * a.dim;
         const GradTile<T> dh{p.sums ? sum : nullptr, p.ldsum, static_cast<T *>(a.dhidden), scale, tokens, dim,
-                             w0 > 0, wide(a.dhidden)};
-        const GradTile<T> dw{nullptr, 0, dwp, scale, static_cast<int>(words), dim, false, wide(dwp)};
+                             w0 > 0};
+        const GradTile<T> dw{nullptr, 0, dwp, scale, static_cast<int>(words), dim, false};
         const auto jh = job_of<true, false>(rows_of(w, p.dimp, a.dim, words), rows_of(pr, wordsp, a.tokens, words), dh);
         const auto jw = job_of<true, true>(rows_of(h, p.dimp, a.dim, a.tokens), rows_of(pr, wordsp, words, a.tokens), dw);
         // a last, shorter piece keeps the runs, so that they add to the same sums
@@ -939,7 +963,7 @@ hipError_t bwd(const LossArgs &a, const Plan &p, unsigned char *base, hipStream_
         hipLaunchKernelGGL(add_runs_kernel<T>, dim3(static_cast<uint32_t>(ceil_div(dim, 256)),
                                                     static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)),
                            dim3(256), 0, stream, sum, p.runs, a.tokens, dim, p.ldsum, scale,
-                           static_cast<T *>(a.dhidden), wide(a.dhidden));
+                           static_cast<T *>(a.dhidden));
         e = hipGetLastError();
     }
     return e;
