@@ -423,7 +423,7 @@ __global__ __launch_bounds__(kJoinTokens * kJoinSlices) void loss_join_kernel(
     const int lane = threadIdx.x % kJoinTokens, slice = threadIdx.x / kJoinTokens;
     const int t = blockIdx.x * kJoinTokens + lane, at = min(t, tokens - 1);
     float2 s = make_float2(-INFINITY, 0.0f);
-    constexpr int kAhead = 4;   // loads under way at a time
+    constexpr int kAhead = 8;   // loads under way at a time
     for (int k = slice; k < parts; k += kAhead * kJoinSlices) {
         float2 f[kAhead];
 #pragma unroll
