@@ -471,9 +471,10 @@ typedef struct {
  * for bit.
  * Errors as for mssm_selective_scan_fwd; also MSSM_ERR_INVALID_ARG for a scale
  * that is negative or not finite, MSSM_ERR_UNSUPPORTED for dim >= 2^21, for
- * another size or batch * dim >= 2^31, or where the sequences' segments of
- * 128 steps by 32 channels reach 2^30.  batch == 0 or dim == 0: nothing to do, MSSM_OK.  L == 0:
- * h_last receives h0 (or zeros), y is empty.
+ * another size or batch * dim >= 2^31, or where the sequences hold 2^30 or more
+ * segments of 64 channels by 88 steps (66 for float32 or an odd dim).
+ * batch == 0 or dim == 0: nothing to do, MSSM_OK.  L == 0: h_last receives h0
+ * (or zeros), y is empty.
  */
 MSSM_API mssm_status mssm_gated_recurrence_fwd(const void *x, const void *r,
                                 const void *i, const float *lam, float scale,
@@ -504,8 +505,8 @@ MSSM_API int64_t mssm_gated_recurrence_workspace(mssm_recurrence_dims dims,
  *   dlam        (dim) float32                 nullable (output)
  *   dh0         (batch, dim) float32          nullable (output)
  * dlam is summed in a fixed order (repeatable bit for bit), through partial
- * sums in the workspace.  L == 0: dlam is zero, dh0 = dh_last.  Errors as for the forward; no output may overlap an input
- * or another output.
+ * sums in the workspace.  L == 0: dlam is zero, dh0 = dh_last.  Errors as for
+ * the forward; no output may overlap an input or another output.
  */
 MSSM_API mssm_status mssm_gated_recurrence_bwd(const void *x, const void *r,
                                 const void *i, const float *lam, float scale,
