@@ -94,35 +94,49 @@ __device__ __forceinline__ int group_of() {
     return S::G < 64 ? g : __builtin_amdgcn_readfirstlane(g);
 }
 
-// Sum over a row's lanes, the same value in all of them.  sh: a float per wave
-// of the row, not written again until the lanes have met at another barrier.
-template <typename S>
-__device__ __forceinline__ float row_sum(float v, float *sh) {
+// Sums of N values over a row's lanes, the same in all of them.  sh: N floats per
+// wave of the row, not written again until the lanes have met at another barrier.
+template <typename S, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float *sh) {
     constexpr int G = S::G;
     auto dpp = [](float x, auto ctrl) {
         return __builtin_bit_cast(
             float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
     };
-    v += dpp(v, std::integral_constant<int, 0xb1>());    // quad_perm 1 0 3 2
-    v += dpp(v, std::integral_constant<int, 0x4e>());    // quad_perm 2 3 0 1
-    v += dpp(v, std::integral_constant<int, 0x141>());   // halves of 8 mirrored
-    if constexpr (G >= 16) v += dpp(v, std::integral_constant<int, 0x140>());   // rows of 16 mirrored
-    if constexpr (G >= 32) {
-        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    }
-    if constexpr (G >= 64) {
-        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float x = v[i];
+        x += dpp(x, std::integral_constant<int, 0xb1>());    // quad_perm 1 0 3 2
+        x += dpp(x, std::integral_constant<int, 0x4e>());    // quad_perm 2 3 0 1
+        x += dpp(x, std::integral_constant<int, 0x141>());   // halves of 8 mirrored
+        if constexpr (G >= 16) x += dpp(x, std::integral_constant<int, 0x140>());   // rows of 16 mirrored
+        if constexpr (G >= 32) {
+            const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+            x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+        }
+        if constexpr (G >= 64) {
+            const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+            x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+        }
+        v[i] = x;
+        if constexpr (S::kWaves > 1)
+            if (threadIdx.x % 64 == 0) sh[i * S::kWaves + threadIdx.x / 64] = x;
     }
     if constexpr (S::kWaves > 1) {
-        if (threadIdx.x % 64 == 0) sh[threadIdx.x / 64] = v;
         __syncthreads();
-        v = sh[0];
 #pragma unroll
-        for (int w = 1; w < S::kWaves; ++w) v += sh[w];
+        for (int i = 0; i < N; ++i) {
+            v[i] = sh[i * S::kWaves];
+#pragma unroll
+            for (int w = 1; w < S::kWaves; ++w) v[i] += sh[i * S::kWaves + w];
+        }
     }
-    return v;
+}
+template <typename S>
+__device__ __forceinline__ float row_sum(float v, float *sh) {
+    float x[1] = {v};
+    row_sums<S, 1>(x, sh);
+    return x[0];
 }
 
 // Values of the lane's columns, `other` where there is no vector.
@@ -285,7 +299,8 @@ struct NormBwd {
         load_row<T, S>(x + row * dim, lane, dim, h.x);
         load_row<T, S>(dy + row * dim, lane, dim, h.dy);
     }
-    // Finishes a row and loads the next into the registers that it leaves.
+    // Finishes a row and, with RELOAD, loads the next into the registers that it leaves.
+    template <bool RELOAD>
     __device__ __forceinline__ void finish(int64_t row, int64_t step, int lane, Held &h, const float *weights,
                                            float (&dw)[S::K][S::VEC], float (&db)[S::K][S::VEC], float *sh) const {
         // the weights are read anew for every row: held, they would not leave room for the next row
@@ -309,10 +324,11 @@ struct NormBwd {
             }
             __builtin_amdgcn_sched_barrier(0);   // one vector after the other: fewer registers
         }
-        float s0 = p0[0], s1 = p1[0];
+        float s[2] = {p0[0], p1[0]};
 #pragma unroll
-        for (int k = 1; k < S::K; ++k) s0 += p0[k], s1 += p1[k];
-        const float m0 = row_sum<S>(s0, sh) / dim, m1 = row_sum<S>(s1, sh + S::kWaves) / dim;
+        for (int k = 1; k < S::K; ++k) s[0] += p0[k], s[1] += p1[k];
+        row_sums<S, 2>(s, sh);
+        const float m0 = s[0] / dim, m1 = s[1] / dim;
         // from here on x and dy are unpacked again, not kept as floats meanwhile
 #pragma unroll
         for (int k = 0; k < S::K; ++k) asm volatile("" : "+v"(h.x[k].v), "+v"(h.dy[k].v));
@@ -321,8 +337,10 @@ struct NormBwd {
         int none = 0;
         asm("" : "+v"(none));   // as vector loads: a scalar one would be waited for with the next LDS read
         const float mu = h.mu, r = h.r;
-        h.mu = mean[next + none];
-        h.r = rstd[next + none];
+        if (RELOAD) {
+            h.mu = mean[next + none];
+            h.r = rstd[next + none];
+        }
 #pragma unroll
         for (int k = 0; k < S::K; ++k) {
             const Place<S> place(k, lane, dim);
@@ -334,8 +352,10 @@ struct NormBwd {
                 f[e] = r * (h.dy[k].get(e) * w[e] - m0 - xh * m1);
             }
             if (there && (k < S::FULL || place.skip < S::VEC)) Vec<T, S::VEC>::store(dx + row * dim + place.at, f);
-            h.x[k].load(x + next * dim + place.at);
-            h.dy[k].load(dy + next * dim + place.at);
+            if (RELOAD) {
+                h.x[k].load(x + next * dim + place.at);
+                h.dy[k].load(dy + next * dim + place.at);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -368,7 +388,7 @@ struct NormBwd {
 template <typename T, typename S>
 __global__ __launch_bounds__((NormBwd<T, S>::kThreads)) void norm_bwd_kernel(NormBwd<T, S> n) {
     extern __shared__ __align__(16) float lds[];   // weights; then the waves' column sums
-    __shared__ float sh[2 * S::kWaves];
+    __shared__ float sh[4 * S::kWaves];
     const int lane = threadIdx.x % S::G, group = group_of<S>();
     // a workgroup's groups take rows far apart, so that few rows still reach every workgroup
     const int64_t step = static_cast<int64_t>(gridDim.x) * n.kRows;
@@ -395,7 +415,24 @@ __global__ __launch_bounds__((NormBwd<T, S>::kThreads)) void norm_bwd_kernel(Nor
     int left = __builtin_amdgcn_readfirstlane(static_cast<int>(n.rows - lead));
     const int stride = static_cast<int>(step);
     float dw[S::K][S::VEC] = {}, db[S::K][S::VEC] = {};
-    for (; left > 0; left -= stride, row += step) n.finish(row, step, lane, a, lds, dw, db, sh);
+    if constexpr (S::G == 256) {
+        // the waves of a row wait for one another: the next row comes in meanwhile
+        // (4096 x 8192 in bfloat16 51 us against 59 us; 16 waves have no registers for it)
+        typename NormBwd<T, S>::Held b;
+        while (left > 0) {
+            n.load(row + step, lane, b);
+            n.template finish<false>(row, step, lane, a, lds, dw, db, sh);
+            row += step;
+            if ((left -= stride) <= 0) break;
+            n.load(row + step, lane, a);
+            n.template finish<false>(row, step, lane, b, lds, dw, db, sh + 2 * S::kWaves);
+            row += step;
+            left -= stride;
+        }
+    } else {
+        for (int k = 0; left > 0; left -= stride, row += step, k ^= 1)
+            n.template finish<true>(row, step, lane, a, lds, dw, db, sh + 2 * S::kWaves * k);
+    }
     if (!n.part) return;
     __syncthreads();
     float *out = n.part + static_cast<int64_t>(blockIdx.x) * 2 * n.dim;
@@ -512,16 +549,21 @@ __global__ __launch_bounds__(256) void norm_wide_part_kernel(
 
 // ---- launches ------------------------------------------------------------------
 
-constexpr int64_t kMostHeld = 24576;
+// The longest rows that registers hold.  The backward of 16 waves a row has no
+// registers for 24 elements a lane with their column sums (1500 x 24000 in
+// bfloat16 141 us, going over the rows again 125 us; forward 29 us and 84 us).
+constexpr int64_t kMostHeldFwd = 24576, kMostHeldBwd = 16384;
 
 // Calls f with the shape for rows of `dim` elements; false if there is none.
-// A lane holds 8 elements, or as many as keep a row within one wave up to 40,
-// above that within 4 waves, above that within 16 waves up to 24 (a workgroup
-// of 16 waves leaves each half the registers).  Below 8 elements a lane holds
-// one.
-template <typename T, typename F>
+// A lane holds 8 elements, or as many as keep a row within one wave up to 40
+// (the float32 backward, two vectors for one, 32: 8192 x 2560 47 us against 58 us),
+// above that within 4 waves, above that within 16 waves up to 16 or, forward, 24
+// (a workgroup of 16 waves leaves each half the registers).  Below 8 elements a
+// lane holds one.
+template <typename T, bool BWD, typename F>
 bool with_shape(int64_t dim, F f) {
     constexpr int V = 16 / sizeof(T), U = 8 / V;   // elements of a vector, vectors of 8 elements
+    constexpr bool kLong = !(BWD && sizeof(T) == 4);
     if (dim < 8) f(Shape<1, 1, 0, 8>());
     else if (dim <= 64) f(Shape<V, U, 0, 8>());
     else if (dim <= 128) f(Shape<V, U, 0, 16>());
@@ -530,21 +572,29 @@ bool with_shape(int64_t dim, F f) {
     else if (dim <= 1024) f(Shape<V, 2 * U, U, 64>());
     else if (dim <= 1536) f(Shape<V, 3 * U, 2 * U, 64>());
     else if (dim <= 2048) f(Shape<V, 4 * U, 3 * U, 64>());
-    else if (dim <= 2560) f(Shape<V, 5 * U, 4 * U, 64>());
+    else if (dim <= (kLong ? 2560 : 2048)) {
+        if constexpr (kLong) f(Shape<V, 5 * U, 4 * U, 64>());
+    }
     else if (dim <= 4096) f(Shape<V, 2 * U, U, 256>());
     else if (dim <= 6144) f(Shape<V, 3 * U, 2 * U, 256>());
     else if (dim <= 8192) f(Shape<V, 4 * U, 3 * U, 256>());
     else if (dim <= 10240) f(Shape<V, 5 * U, 4 * U, 256>());
-    else if (dim <= 16384) f(Shape<V, 2 * U, U, 1024>());
-    else if (dim <= kMostHeld) f(Shape<V, 3 * U, 2 * U, 1024>());
-    else return false;
+    else if (dim <= kMostHeldBwd) f(Shape<V, 2 * U, U, 1024>());
+    else {
+        if constexpr (!BWD)
+            if (dim <= kMostHeldFwd) {
+                f(Shape<V, 3 * U, 2 * U, 1024>());
+                return true;
+            }
+        return false;
+    }
     return true;
 }
 
 template <typename T>
 hipError_t fwd(const NormArgs &a, hipStream_t stream) {
     const int dim = static_cast<int>(a.dim);
-    const bool held = with_shape<T>(a.dim, [&](auto shape) {
+    const bool held = with_shape<T, false>(a.dim, [&](auto shape) {
         using S = decltype(shape);
         using N = NormFwd<T, S>;
         const N n{static_cast<const T *>(a.x), a.weight, a.bias, a.eps, static_cast<T *>(a.y), a.mean, a.rstd, a.rows, dim};
@@ -567,7 +617,7 @@ hipError_t fwd(const NormArgs &a, hipStream_t stream) {
 // Partial column sums of the backward, one per workgroup, one workgroup per
 // compute unit: with two, the column sums cost more than the second hides
 // (8192 x 2560 in bfloat16: 43 us against 33 us).  Slices of wide rows.
-int64_t parts_of(const NormArgs &a) { return std::min<int64_t>(a.rows, a.dim > kMostHeld ? 64 : 256); }
+int64_t parts_of(const NormArgs &a) { return std::min<int64_t>(a.rows, a.dim > kMostHeldBwd ? 64 : 256); }
 
 template <typename T>
 hipError_t bwd(const NormArgs &a, void *workspace, hipStream_t stream) {
@@ -580,7 +630,7 @@ hipError_t bwd(const NormArgs &a, void *workspace, hipStream_t stream) {
     const T *dy = static_cast<const T *>(a.dy), *x = static_cast<const T *>(a.x);
     T *dx = static_cast<T *>(a.dx);
     hipError_t e = hipSuccess;
-    const bool held = with_shape<T>(a.dim, [&](auto shape) {
+    const bool held = with_shape<T, true>(a.dim, [&](auto shape) {
         using S = decltype(shape);
         using N = NormBwd<T, S>;
         const N n{dy, x, a.mean, a.rstd, a.weight, dx, part, a.rows, dim};
