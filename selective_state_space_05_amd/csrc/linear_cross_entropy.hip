@@ -19,6 +19,13 @@
 // dhidden) or across it (weight for dhidden, hidden and p for dweight): the
 // second kind is transposed on its way from LDS to registers, so that no
 // transposed copy of anything is ever written.
+//
+// Bound by the matrix cores and, at their full rate, by the clock that the card
+// holds under them (1.75 to 2.0 GHz); few tokens by the read of weight.  Measured at
+// width 2560 and 50021 words in bfloat16: 8192 tokens forward 1.80 to 1.87 ms (1.12
+// to 1.17 PFLOP/s), backward 5.65 to 5.77 ms (1.09 to 1.11), 16 tokens forward 66 us
+// (58 us of it reading weight at 4.4 TB/s); float32, 2048 tokens of width 1024 and
+// 32000 words, forward 1.0 ms (134 TFLOP/s).
 #include "device_math.h"
 #include "internal.h"
 
@@ -135,8 +142,8 @@ struct Operand {
             left = static_cast<int64_t>(R.k) * R.ld - static_cast<int64_t>(first) * sizeof(T);
             chunks = 0;
         } else {
-            // rows past the end lie past the buffer's end and read as zero
-            // (the minimum is formed in a vector register)
+            // rows past the end lie past the buffer's end and read as zero (the
+            // scalar offset is checked too; the minimum is formed in a vector register)
             const int n = __builtin_amdgcn_readfirstlane(min(R.rows - first, N));
             base = R.p + first * R.ld;
             rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char *>(base), 0, n * static_cast<int>(R.ld),

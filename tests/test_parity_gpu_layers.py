@@ -663,3 +663,23 @@ def test_layers_in_a_graph(dev, mssm):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), k
+
+
+# ---- sizes at which another kernel or tile takes over ---------------------------
+
+@pytest.mark.parametrize("shape", [(700, 2600), (520, 6001), (3, 9999), (2, 12001), (2, 16384), (2, 20011), (2, 24577)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_layer_norm_wide_rows(dev, mssm, shape, io):
+    """Rows held by several waves, with more rows than workgroups, and rows that
+    no workgroup holds; the bounds are those of the other sizes."""
+    test_layer_norm_forward(dev, mssm, shape, io)
+    test_layer_norm_backward(dev, mssm, shape, io)
+
+
+@pytest.mark.parametrize("shape", [(600, 264, 25001), (24, 136, 20000), (17, 2560, 130), (200, 72, 33000)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_linear_cross_entropy_tiles(dev, mssm, shape, io):
+    """The largest tiles, the narrow ones and those between, with ends that no
+    tile divides; the bounds are those of the other sizes."""
+    test_linear_cross_entropy_forward(dev, mssm, shape, io)
+    test_linear_cross_entropy_backward(dev, mssm, shape, io)
