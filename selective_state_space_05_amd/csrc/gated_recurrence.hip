@@ -224,7 +224,8 @@ __device__ __forceinline__ void exchange(int lane, int seg, int group, const flo
     float s = span == 0 && init ? init[min(lane, valid - 1)] : 0.0f;
     if (ex.nseg > 1) {
         const bool more = seg < ex.nseg - 1;
-        const int64_t stride = static_cast<int64_t>(ex.groups) * kChannels, here = group * kChannels + lane;
+        const int64_t stride = static_cast<int64_t>(ex.groups) * kChannels,
+                      here = static_cast<int64_t>(group) * kChannels + lane;   // groups may pass 2^25
         asm volatile("" : "+v"(s) : : "memory");   // has arrived
         if (more) put(ex.pairs[0] + seg * stride + here, own.x, own.y);
         // n[l] values of level l: pairs since the last whole run, runs since
