@@ -46,3 +46,120 @@ def test_gated_recurrence_more_than_2_25_groups(dev, mssm):
         within(ys, yo, bound + base.half_step(yo, ys) * 1.01, "y")
     del x, y, xs, ys
     torch.cuda.empty_cache()
+
+
+# ---- gated linear recurrence: gates that are almost closed, decays that are fast --
+
+FLUSH, STEP = 2.0 ** -126, 2.0 ** -149   # smallest normal and subnormal float32
+
+
+def gate_bounds(r, lam, scale=8.0):
+    """log a, a, m, sigmoid(r) in float64 and how far the float32 ones are off.
+
+    sigmoid: the exponent's rounding times |r| and three operations; a hardware
+    reciprocal gives 0 for a result below FLUSH.  softplus, its product with the
+    scale and log a round to a multiple of STEP where they are subnormal.  a: the
+    rounding of 1 + (a - 1) or, below log a = -0.35, an exponential whose argument
+    is rounded twice.  m is a root: off by half its radicand's relative error or,
+    where that is large, by the root of its error."""
+    la, a, m, sr, _ = layers.gates(r, r, lam, scale)
+    rate = scale * layers.softplus(lam.double())
+    d_la = la.abs() * (3 * r.double().abs() + 24) * U32 + torch.where(sr < 2 * FLUSH, rate * FLUSH, 0 * la)
+    d_la = d_la + scale * 2 * STEP * sr + STEP
+    far = a * (d_la + (3 * la.abs() + 8) * U32) + FLUSH
+    d_a = torch.where(la < -0.34, far, d_la + 2 * U32)
+    d_em = 2 * a * a * (d_la + (3 * la.abs() + 8) * U32 * (la < -0.34)) + 8 * U32 * m * m + 2 * STEP
+    d_m = torch.minimum(d_em.sqrt(), d_em / m.clamp(min=1e-300)) + 4 * U32 * m
+    return la, a, m, sr, d_la, d_a, d_m
+
+
+def walk_back(a, dy, d_a, dh_last):
+    """g_t = dy_t + a_{t+1} g_{t+1}: bounds of its error and of its size, and of
+    what leaves the first step (test_gated_recurrence_backward's)."""
+    e = torch.zeros_like(a[:, 0])
+    size = e if dh_last is None else dh_last.double().abs()
+    d_g, g_size = torch.empty_like(a), torch.empty_like(a)
+    for t in range(a.shape[1] - 1, -1, -1):
+        size = dy[:, t].double().abs() + size
+        e = e + 2 * U32 * size
+        d_g[:, t], g_size[:, t] = e, size
+        e = a[:, t] * e + 2 * (d_a[:, t] + U32 * a[:, t]) * size
+        size = a[:, t] * size
+    return d_g, e + U32 * size
+
+
+def check_gates_forward(mssm, x, r, i, lam, h0):
+    _, a, m, _, _, d_a, d_m = gate_bounds(r, lam)
+    si, ax = torch.sigmoid(i.double()), x.double().abs()
+    b = m * si * ax
+    d_b = si * ax * d_m + b * (3 * i.double().abs() + 20) * U32
+    e = torch.zeros_like(a[:, 0])
+    size = e if h0 is None else h0.double().abs()
+    bound = torch.empty_like(a)
+    for t in range(a.shape[1]):
+        new = a[:, t] * size + b[:, t]
+        e = a[:, t] * e + 2 * ((d_a[:, t] + U32 * a[:, t]) * size + d_b[:, t] + 2 * U32 * new)
+        size = new
+        bound[:, t] = e
+    y, last = mssm.gated_recurrence_fwd(x, r, i, lam, 8.0, h0=h0)
+    yo, lo = layers.gated_recurrence(x, r, i, lam, 8.0, h0)
+    within(last, lo, bound[:, -1] + FLUSH, "h_last")
+    within(y, yo, bound + base.half_step(yo, y) * 1.01, "y")
+
+
+def check_gates_backward(mssm, x, r, i, lam, h0, dh_last, names=("dx", "di", "dr", "dh0", "dlam")):
+    y = layers.gated_recurrence(x, r, i, lam, 8.0, h0)[0].to(x.dtype)
+    dy = randn(x.device, *x.shape, seed=11, dtype=x.dtype)
+    got = mssm.gated_recurrence_bwd(x, r, i, lam, y, dy, 8.0, h0=h0, dh_last=dh_last)
+    want = layers.gated_recurrence_grad(x, r, i, lam, y, dy, 8.0, h0, dh_last)
+    la, a, m, sr, d_la, d_a, d_m = gate_bounds(r, lam)
+    si, ax = torch.sigmoid(i.double()), x.double().abs()
+    d_g, d_h0 = walk_back(a, dy, d_a, dh_last)
+    g = want["g"].abs()
+    rel_s = (3 * i.double().abs() + 12) * U32
+    d_gm = d_g * m + g * d_m + 2 * U32 * g * m
+    start = torch.zeros_like(a[:, :1]) if h0 is None else h0.double()[:, None]
+    before = torch.cat([start, y.double()[:, :-1]], 1).abs()
+    # w = a g log a (h_{t-1} - u a / m), u = sigmoid(i) x.  log a / m is about the
+    # root of -log a / 2.  a g log a may round to a multiple of STEP, and 1 / m
+    # reaches at most 2^74.
+    u = si * ax
+    q = torch.where(m > 0, la / m, 0 * m).abs()
+    d_q = torch.minimum(d_la.sqrt(), 1.1 * q * d_la / la.abs().clamp(min=1e-300)) + 10 * U32 * q
+    one, two = a * la.abs() * before, a * a * u * q
+    inverse = (1 / m.clamp(min=2.0 ** -74))
+    d_w = (d_g * (one + two) + g * (a * before * d_la + a * a * u * d_q + d_a * (before * la.abs() + 2 * a * u * q)
+                                    + (one + two) * (rel_s + 10 * U32)) + STEP * (before + u * a * inverse))
+    bounds = {"dx": si * d_gm + g * m * si * rel_s,
+              "di": u * (1 - si) * d_gm + g * m * u * ((1 - si) * (rel_s + 2 * U32) + si * rel_s + U32),
+              "dr": d_w * (1 - sr) + want["w"].abs() * (sr * (3 * r.double().abs() + 24) * U32 + 2 * U32),
+              "dh0": d_h0 + FLUSH}
+    ratio = torch.sigmoid(lam.double()) / layers.softplus(lam.double())
+    n = (a.shape[0] * a.shape[1] + 16) * U32
+    bounds["dlam"] = ratio * (d_w.sum((0, 1)) + n * want["w"].abs().sum((0, 1))) + want["dlam"].abs() * 16 * U32 + FLUSH
+    for key in names:
+        extra = base.half_step(want[key], got[key]) * 1.01 if key in ("dx", "di", "dr") else 0
+        within(got[key], want[key], bounds[key] + extra, key)
+    return got
+
+
+CLOSED = [0.0, -70.0, -80.0, -83.0, -85.0, -86.0, -86.5, -87.0, -87.5, -88.0, -95.0, -104.0]
+
+
+def closed_inputs(dev, steps, value, io):
+    shape = (2, steps, 66)
+    x, i = (randn(dev, *shape, seed=k, dtype=IO[io]) for k in (1, 2))
+    return x, torch.full(shape, value, device=dev, dtype=IO[io]), i, torch.linspace(-100.0, -2.0, 66, device=dev)
+
+
+@pytest.mark.parametrize("value", CLOSED)
+@pytest.mark.parametrize("steps", [5, 300])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gated_recurrence_almost_closed_gates(dev, mssm, value, steps, io):
+    """1 - a^2 through the subnormals down to 0: what little enters and every
+    gradient keep float32's relative precision as far as log a itself does."""
+    announce("almost closed", value, steps, io)
+    x, r, i, lam = closed_inputs(dev, steps, value, io)
+    check_gates_forward(mssm, x, r, i, lam, None)
+    got = check_gates_backward(mssm, x, r, i, lam, None, randn(dev, 2, 66, seed=12), ("dx", "di", "dr", "dh0"))
+    assert torch.isfinite(got["dlam"]).all()
