@@ -456,7 +456,7 @@ typedef struct {
  *   y[b,t,d]  = h;   h_last[b,d] = h after t = L-1
  *
  * 1 - a_t^2 is formed from a_t - 1 = expm1(log a_t), so that decays next to 1
- * lose nothing.
+ * lose nothing; fast decays keep their relative precision too.
  *
  * Arguments (device pointers unless stated):
  *   x, r, i  (batch, L, dim), dtype `io`   required (r, i before the sigmoid)

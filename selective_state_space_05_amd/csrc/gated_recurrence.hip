@@ -49,8 +49,8 @@
 // the wait for stores that a flag needs (0.56 us from a store to a load that
 // sees it).  The marks are cleared by a kernel in front.
 //
-// Measured (2 x 4096 steps of 5120 channels, bfloat16): forward 87 us (3.9
-// TB/s), backward 163 us (4.1 TB/s); float32 forward 135 us (5.0 TB/s).
+// Measured (2 x 4096 steps of 5120 channels, bfloat16): forward 88 us (3.8
+// TB/s), backward 164 us (4.1 TB/s); float32 forward 135 us (5.0 TB/s).
 #include "device_math.h"
 #include "internal.h"
 
@@ -78,10 +78,8 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-x * kLog2e));
 }
 
-// e^x - 1 for x <= 0.  From -0.35 up the Taylor series (its remainder is below
-// 2e-8 of the value), below that 2^y - 1, where the subtraction loses at most
-// a factor 3.4.  a = 1 + expm1 is then rounded once, and 1 - a^2 =
-// -expm1 (2 + expm1) loses nothing as a nears 1.
+// e^x - 1 for -0.35 <= x <= 0: the Taylor series, its remainder below 2e-8 of
+// the value.
 __device__ __forceinline__ float expm1_series(float x) {
     float p = 1.0f / 5040.0f;
     p = fmaf(p, x, 1.0f / 720.0f);
@@ -91,11 +89,37 @@ __device__ __forceinline__ float expm1_series(float x) {
     p = fmaf(p, x, 0.5f);
     return fmaf(p * x, x, x);
 }
+
+// Below -0.35 a decay a = e^x is taken from the exponential (1 + (a - 1) would
+// leave a fast one few digits), from there up from the series (a - 1, of which
+// 1 - a^2 is formed, would lose what matters as a nears 1).
+__device__ __forceinline__ bool is_far(float x) { return x < -kSeriesLimit; }
+
+// a and a - 1 for x = log a <= 0.  NEAR: x is known to be -0.35 or more.  (A wave
+// knows where all its channels' rates are: decays from 0.9 a step take the layer's
+// forward 89.9 us and its backward 163.7 us, decays from 0.3, which mix both
+// ranges, 91.8 and 165.7 us, one call after the other.)
+struct Decay {
+    float a, p;
+};
 template <bool NEAR>
-__device__ __forceinline__ float expm1_neg(float x) {
+__device__ __forceinline__ Decay decay(float x) {
     const float p = expm1_series(x);
-    if (NEAR) return p;
-    return x >= -kSeriesLimit ? p : fast_exp2(x * kLog2e) - 1.0f;
+    Decay d{1.0f + p, p};
+    if (!NEAR) {
+        const float a = fast_exp2(x * kLog2e);
+        d = is_far(x) ? Decay{a, a - 1.0f} : d;
+    }
+    return d;
+}
+
+// A decay as the one number that has its digits, and back.  (The backward's walk of
+// the layer tells the two apart in 1 us; a walk of its own where none is far spills
+// and takes 393 us.)
+template <bool NEAR>
+__device__ __forceinline__ float kept_of(float x, const Decay &d) { return !NEAR && is_far(x) ? d.a : d.p; }
+__device__ __forceinline__ Decay decay_of_kept(float x, float kept) {
+    return is_far(x) ? Decay{kept, kept - 1.0f} : Decay{1.0f + kept, kept};
 }
 
 // 1 - a^2 = -(a - 1)(a - 1 + 2), times 2^64: next to a closed gate it is
@@ -173,8 +197,8 @@ __global__ __launch_bounds__(kRowThreads) void row_fwd_kernel(const T *__restric
     const float rate = -scale * softplus_libm(lam[d]);
     int64_t at = b * L * dim + d;
     for (int t = 0; t < L; ++t, at += dim) {
-        const float p = expm1_neg<false>(rate * sigmoid(Io<T>::load(r, at)));
-        h = fmaf(1.0f + p, h, input_scale(p) * sigmoid(Io<T>::load(i, at)) * Io<T>::load(x, at));
+        const Decay c = decay<false>(rate * sigmoid(Io<T>::load(r, at)));
+        h = fmaf(c.a, h, input_scale(c.p) * sigmoid(Io<T>::load(i, at)) * Io<T>::load(x, at));
         Io<T>::store(y, at, h);
     }
     if (h_last) h_last[row] = h;
@@ -414,10 +438,10 @@ struct Fwd {
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float p = expm1_neg<NEAR>(raw.rate[v] * sigmoid(raw.r[k].get(v)));
-                float in = input_scale(p) * sigmoid(raw.i[k].get(v)) * raw.x[k].get(v);
-                if (!NEAR && k >= pt.steps) p = 0.0f, in = 0.0f;
-                t.a[k][v] = 1.0f + p;
+                const Decay d = decay<NEAR>(raw.rate[v] * sigmoid(raw.r[k].get(v)));
+                float a = d.a, in = input_scale(d.p) * sigmoid(raw.i[k].get(v)) * raw.x[k].get(v);
+                if (!NEAR && k >= pt.steps) a = 1.0f, in = 0.0f;
+                t.a[k][v] = a;
                 t.b[k][v] = in;
                 pair[v] = then(pair[v], make_float2(t.a[k][v], in));
             }
@@ -439,16 +463,16 @@ struct Fwd {
 struct Grad {
     float dx, dr, di, w;
 };
-__device__ __forceinline__ Grad grad_step(float la, float sr, float p, float x, float i, float dy, float before,
+__device__ __forceinline__ Grad grad_step(float la, float sr, const Decay &d, float x, float i, float dy, float before,
                                           float *G) {
-    const float em = one_minus_square(p);
+    const float em = one_minus_square(d.p);
     const float rs = em > 0.0f ? __builtin_amdgcn_rsqf(em) : 0.0f;   // log a / m -> 0 with log a
     const float rm = rs * kRoot;
-    const float a = 1.0f + p, si = sigmoid(i), u = si * x;
+    const float si = sigmoid(i), u = si * x;
     const float g = dy + *G, gm = g * (em * rs * (1.0f / kRoot));
-    *G = a * g;
+    *G = d.a * g;
     Grad o;
-    o.w = *G * la * fmaf(-u * a, rm, before);
+    o.w = *G * la * fmaf(-u * d.a, rm, before);
     o.dx = gm * si;
     o.di = gm * u * (1.0f - si);
     o.dr = o.w * (1.0f - sr);
@@ -456,7 +480,7 @@ __device__ __forceinline__ Grad grad_step(float la, float sr, float p, float x, 
 }
 
 // A backward item: the inputs are kept as they are stored, with sigmoid(r) and
-// a - 1.  y: the state before each row.
+// the decay.  y: the state before each row.
 template <typename T, int V, int K>
 struct Bwd {
     static constexpr int kWavesPerSimd = 3, kLanes = kChannels / V, kSlots = 64 * kComputeWaves / kLanes, kSteps = kSlots * K;
@@ -470,7 +494,7 @@ struct Bwd {
     };
     struct Terms {
         Pack<T, V> x[K], i[K], y[K], dy[K];
-        float sr[K][V], p[K][V], rate[V], start[V];
+        float sr[K][V], kept[K][V], rate[V], start[V];
     };
     static __device__ __forceinline__ Item item(const Place &p, const Walk &w) {
         return bwd_item(p, w, kSteps, sizeof(T));
@@ -519,9 +543,10 @@ struct Bwd {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 t.sr[k][v] = sigmoid(raw.r[k].get(v));
-                t.p[k][v] = expm1_neg<NEAR>(raw.rate[v] * t.sr[k][v]);
-                const float a = 1.0f + t.p[k][v];
-                if (NEAR || k < pt.steps) pair[v] = make_float2(pair[v].x * a, a * (raw.dy[k].get(v) + pair[v].y));
+                const float la = raw.rate[v] * t.sr[k][v];
+                const Decay d = decay<NEAR>(la);
+                t.kept[k][v] = kept_of<NEAR>(la, d);
+                if (NEAR || k < pt.steps) pair[v] = make_float2(pair[v].x * d.a, d.a * (raw.dy[k].get(v) + pair[v].y));
             }
         }
     }
@@ -539,8 +564,9 @@ struct Bwd {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float before = k == first ? t.start[v] : t.y[k].get(v);
-                const Grad g = grad_step(t.rate[v] * t.sr[k][v], t.sr[k][v], t.p[k][v], t.x[k].get(v), t.i[k].get(v),
-                                         t.dy[k].get(v), before, &G[v]);
+                const float la = t.rate[v] * t.sr[k][v];
+                const Grad g = grad_step(la, t.sr[k][v], decay_of_kept(la, t.kept[k][v]), t.x[k].get(v),
+                                         t.i[k].get(v), t.dy[k].get(v), before, &G[v]);
                 ox[v] = g.dx;
                 og[v] = g.dr;
                 oi[v] = g.di;

@@ -163,3 +163,18 @@ def test_gated_recurrence_almost_closed_gates(dev, mssm, value, steps, io):
     check_gates_forward(mssm, x, r, i, lam, None)
     got = check_gates_backward(mssm, x, r, i, lam, None, randn(dev, 2, 66, seed=12), ("dx", "di", "dr", "dh0"))
     assert torch.isfinite(got["dlam"]).all()
+
+
+@pytest.mark.parametrize("log_a", [-0.3, -0.36, -1.0, -5.0, -8.0, -12.0, -17.0, -25.0, -40.0, -60.0])
+@pytest.mark.parametrize("steps", [5, 300])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gated_recurrence_fast_decays(dev, mssm, log_a, steps, io):
+    """A decay far below one keeps its relative precision: it is a factor of
+    dr, dlam and dh0.  log a lies around the value given."""
+    announce("fast decays", log_a, steps, io)
+    shape = (2, steps, 66)
+    x, i, r = (randn(dev, *shape, seed=k, dtype=IO[io], scale=s) for k, s in ((1, 1.0), (2, 1.0), (3, 0.2)))
+    lam = torch.full((66,), -log_a / 4, dtype=torch.float64, device=dev).expm1().log().float()
+    h0, dh_last = randn(dev, 2, 66, seed=4), randn(dev, 2, 66, seed=12)
+    check_gates_forward(mssm, x, r, i, lam, h0)
+    check_gates_backward(mssm, x, r, i, lam, h0, dh_last)
