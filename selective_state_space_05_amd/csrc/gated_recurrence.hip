@@ -741,8 +741,9 @@ __global__ __launch_bounds__(kThreads, Op::kWavesPerSimd) void segment_kernel(Op
     if (SUM) __syncthreads();
 }
 
-// dlam = sum of the parts, times sigmoid(lam) / softplus(lam) (which tends to
-// 1 as lam falls).  32 channels and 16 slices of the parts a workgroup.
+// dlam = sum of the parts, times sigmoid(lam) / softplus(lam).  The ratio is 1 -
+// e^lam / 2 + ... as lam falls: 1 in float32 below -17 (further down both its parts
+// leave float32's range).  32 channels and 16 slices of the parts a workgroup.
 constexpr int kSlices = 16;
 __global__ __launch_bounds__(32 * kSlices) void dlam_kernel(const float *__restrict__ part,
                                                             const float *__restrict__ lam,
@@ -759,8 +760,8 @@ __global__ __launch_bounds__(32 * kSlices) void dlam_kernel(const float *__restr
         s = 0.0f;
 #pragma unroll
         for (int k = 0; k < kSlices; ++k) s += sh[k][c];
-        const float sp = softplus_libm(lam[d]), sg = 1.0f / (1.0f + expf(-lam[d]));
-        dlam[d] = s * (sp > 0.0f ? sg / sp : 1.0f);
+        const float x = lam[d];
+        dlam[d] = x > -17.0f ? s / (1.0f + expf(-x)) / softplus_libm(x) : s;
     }
 }
 

@@ -178,3 +178,15 @@ def test_gated_recurrence_fast_decays(dev, mssm, log_a, steps, io):
     h0, dh_last = randn(dev, 2, 66, seed=4), randn(dev, 2, 66, seed=12)
     check_gates_forward(mssm, x, r, i, lam, h0)
     check_gates_backward(mssm, x, r, i, lam, h0, dh_last)
+
+
+@pytest.mark.parametrize("steps", [5, 300])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gated_recurrence_lam_far_out(dev, mssm, steps, io):
+    """dlam's factor sigmoid(lam) / softplus(lam), where both leave float32's
+    range (below -87 and -104) and where it is steep."""
+    announce("lam far out", steps, io)
+    shape = (2, steps, 130)
+    x, i, r = (randn(dev, *shape, seed=k, dtype=IO[io]) for k in (1, 2, 3))
+    lam = torch.linspace(-100.0, 29.0, 130, device=dev)
+    check_gates_backward(mssm, x, r, i, lam, randn(dev, 2, 130, seed=4), randn(dev, 2, 130, seed=12))
