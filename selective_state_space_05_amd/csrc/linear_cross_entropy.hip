@@ -478,9 +478,12 @@ __global__ __launch_bounds__(1024) void grad_scale_kernel(const float *__restric
 }
 
 // exp(l - ref).  Float32 results carry the rounding of the exponent's product with
-// log2 e as a second term; in bfloat16 it is far below p's own rounding.
+// log2 e as a second term (which has no value where the product is infinite, so
+// that what vanishes anyway is cut at e^-200); in bfloat16 it is far below p's own
+// rounding.
 __device__ __forceinline__ float exp_of(float d, uint16_t) { return fast_exp2(d * kLog2e); }
 __device__ __forceinline__ float exp_of(float d, float) {
+    d = d < -200.0f ? -200.0f : d;   // a NaN stays
     const float hi = d * kLog2e, lo = fmaf(d, kLog2e, -hi);
     return fast_exp2(hi) * fmaf(lo, kLn2, 1.0f);
 }

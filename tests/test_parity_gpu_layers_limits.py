@@ -190,3 +190,39 @@ def test_gated_recurrence_lam_far_out(dev, mssm, steps, io):
     x, i, r = (randn(dev, *shape, seed=k, dtype=IO[io]) for k in (1, 2, 3))
     lam = torch.linspace(-100.0, 29.0, 130, device=dev)
     check_gates_backward(mssm, x, r, i, lam, randn(dev, 2, 130, seed=4), randn(dev, 2, 130, seed=12))
+
+
+# ---- projected cross entropy: logits without bounds -------------------------------
+
+def far_logit_inputs(dev, io, tokens):
+    """Words 50 and 51 have logits around -3e38 and, in float32, -infinity (sums
+    of finite products); the other words' are of order one."""
+    hidden, weight, targets = base.loss_inputs(dev, (tokens, 72, 300), io)
+    hidden[:, 0], hidden[:, 1] = 1.0, 1.0
+    weight[50:52] = 0
+    weight[50, 0] = weight[51, 0] = weight[51, 1] = -3e38
+    targets = torch.where((targets == 50) | (targets == 51), 7, targets)
+    return hidden, weight, targets
+
+
+@pytest.mark.parametrize("tokens", [20, 150])
+def test_linear_cross_entropy_words_far_below(dev, mssm, tokens):
+    """A word whose logit is very negative or overflows to -infinity has p = 0: it
+    adds nothing to any gradient and its own is 0.  The other words and the hidden
+    states keep the bounds of the call without these words."""
+    announce("words far below", tokens)
+    hidden, weight, targets = far_logit_inputs(dev, "f32", tokens)
+    keep = torch.ones(300, dtype=torch.bool, device=dev)
+    keep[50:52] = False
+    fewer = targets - 2 * ((targets > 51).long())
+    _, lse = mssm.linear_cross_entropy_fwd(hidden, weight, targets)
+    _, want_lse = layers.linear_cross_entropy(hidden, weight[keep], fewer)
+    d = base.logit_bound(hidden, weight[keep]).amax(1) + 400 * U32 + 4 * U32 * want_lse.abs()
+    within(lse, want_lse, d, "lse")
+    dloss = randn(dev, tokens, seed=3)
+    got = mssm.linear_cross_entropy_bwd(hidden, weight, targets, lse, dloss)
+    want = layers.linear_cross_entropy_grad(hidden, weight[keep], fewer, lse, dloss)
+    bh, bw = base.loss_grad_bounds(hidden, weight[keep], lse, dloss, want, U32)
+    within(got["dhidden"], want["dhidden"], bh + base.half_step(want["dhidden"], hidden) * 1.01, "dhidden")
+    within(got["dweight"][keep], want["dweight"], bw + base.half_step(want["dweight"], weight) * 1.01, "dweight")
+    assert (got["dweight"][50:52] == 0).all()
