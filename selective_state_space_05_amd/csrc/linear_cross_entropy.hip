@@ -350,6 +350,11 @@ __device__ __forceinline__ void each_column(const f32x16 (&acc)[Shape::I][Shape:
     }
 }
 
+// What exponentials are taken relative to: the maximum where it is finite.  (An
+// infinite one would make NaN of itself; against 0 it gives a sum of 0 or infinity,
+// and so the log sum exp that it should.)
+__device__ __forceinline__ float reference(float top) { return fabsf(top) == INFINITY ? 0.0f : top; }
+
 // ---- forward: maximum and sum of exponentials of a token over a tile's words
 struct LossTile {
     float2 *part;              // [32 I words][token]
@@ -402,7 +407,7 @@ struct LossTile {
                 if (mine >= 0 && mine / 4 % 2 == lane / 32) target_logit[t] = hit;
             }
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float ref = top == -INFINITY ? 0.0f : top;
+            const float ref = reference(top);
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < Shape::I; ++i)
@@ -420,7 +425,7 @@ struct LossTile {
 // slice is a quarter wave; few tokens have many parts).
 constexpr int kJoinTokens = 16, kJoinSlices = 64;
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
-    const float top = fmaxf(a.x, b.x), ref = top == -INFINITY ? 0.0f : top;
+    const float top = fmaxf(a.x, b.x), ref = reference(top);
     return make_float2(top, a.y * fast_exp2((a.x - ref) * kLog2e) + b.y * fast_exp2((b.x - ref) * kLog2e));
 }
 __global__ __launch_bounds__(kJoinTokens * kJoinSlices) void loss_join_kernel(

@@ -226,3 +226,38 @@ def test_linear_cross_entropy_words_far_below(dev, mssm, tokens):
     within(got["dhidden"], want["dhidden"], bh + base.half_step(want["dhidden"], hidden) * 1.01, "dhidden")
     within(got["dweight"][keep], want["dweight"], bw + base.half_step(want["dweight"], weight) * 1.01, "dweight")
     assert (got["dweight"][50:52] == 0).all()
+
+
+@pytest.mark.parametrize("tokens", [20, 150])
+@pytest.mark.parametrize("vocab", [3, 300, 20000])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_linear_cross_entropy_infinite_logits(dev, mssm, tokens, vocab, io):
+    """A logit of infinity makes lse and the loss of another word infinite and its
+    own word's NaN; one of -infinity is as if the word were not there; a token
+    whose logits all are has lse -infinity."""
+    announce("infinite logits", tokens, vocab, io)
+    hidden, weight, targets = base.loss_inputs(dev, (tokens, 72, vocab), io)
+    targets[targets == -100] = 0
+    weight[1] = 0
+    weight[1, 0] = float("inf")
+    hidden[:, 0] = torch.where(torch.arange(tokens, device=dev) % 2 == 0, 1.0, -1.0)
+    targets[:4] = torch.tensor([1, 0, 2, 0], device=dev)
+    loss, lse = mssm.linear_cross_entropy_fwd(hidden, weight, targets)
+    lo, so = layers.linear_cross_entropy(hidden, weight, targets)
+    up = hidden[:, 0] > 0
+    assert (lse[up] == float("inf")).all() and (so[up] == float("inf")).all()
+    assert torch.equal(torch.isnan(loss), torch.isnan(lo)) and torch.isnan(loss[0])
+    assert (loss[up & (targets != 1)] == float("inf")).all()
+    fine = ~up & (targets != 1)
+    finite = weight.clone()
+    finite[1] = 0
+    logits = hidden.double() @ finite.double().t()
+    d = base.logit_bound(hidden, finite).amax(1) + (vocab + 16 + 2 * (logits.amax(1) - logits.amin(1))) * U32
+    d = d + 4 * U32 * torch.where(fine, so.abs(), 0)
+    within(lse[fine], so[fine], d[fine], "lse")
+    within(loss[fine], lo[fine], (2 * d + 2 * U32 * (so.abs() + logits.abs().amax(1)))[fine], "loss")
+    assert (loss[~up & (targets == 1)] == float("inf")).all()
+    weight[:] = 0
+    weight[:, 0] = float("inf")
+    loss, lse = mssm.linear_cross_entropy_fwd(hidden, weight, targets)
+    assert (lse[up] == float("inf")).all() and (lse[~up] == -float("inf")).all() and torch.isnan(loss).all()
