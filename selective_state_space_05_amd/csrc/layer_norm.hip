@@ -447,7 +447,7 @@ __global__ __launch_bounds__(64 * kSumSlices) void norm_sum_kernel(const float *
                                                                    float *dweight, float *dbias, int dim) {
     __shared__ float sh[kSumSlices][64];
     const int lane = threadIdx.x % 64, slice = threadIdx.x / 64;
-    const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+    const int64_t d = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 64 + lane;
     float v = 0.0f;
     if (d < 2 * static_cast<int64_t>(dim)) {
         constexpr int kAhead = 8;   // loads under way at a time
@@ -648,9 +648,12 @@ hipError_t bwd(const NormArgs &a, void *workspace, hipStream_t stream) {
             hipLaunchKernelGGL(norm_wide_part_kernel<T>, dim3(static_cast<uint32_t>((a.dim + 255) / 256), parts),
                                dim3(256), 0, stream, dy, x, a.mean, a.rstd, part, a.rows, dim);
     }
-    if (part && e == hipSuccess)
-        hipLaunchKernelGGL(norm_sum_kernel, dim3(static_cast<uint32_t>((2 * a.dim + 63) / 64)), dim3(64 * kSumSlices),
-                           0, stream, part, parts, a.dweight, a.dbias, dim);
+    if (part && e == hipSuccess) {
+        // one dimension of a grid holds less than 2^32 threads
+        const int64_t blocks = (2 * a.dim + 63) / 64, x = std::min<int64_t>(blocks, int64_t(1) << 20);
+        hipLaunchKernelGGL(norm_sum_kernel, dim3(static_cast<uint32_t>(x), static_cast<uint32_t>((blocks + x - 1) / x)),
+                           dim3(64 * kSumSlices), 0, stream, part, parts, a.dweight, a.dbias, dim);
+    }
     if (e == hipSuccess) e = hipGetLastError();
     if (part && !workspace) {
         const hipError_t f = scratch_free(ws, stream);

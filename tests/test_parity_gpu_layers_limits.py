@@ -261,3 +261,13 @@ def test_linear_cross_entropy_infinite_logits(dev, mssm, tokens, vocab, io):
     weight[:, 0] = float("inf")
     loss, lse = mssm.linear_cross_entropy_fwd(hidden, weight, targets)
     assert (lse[up] == float("inf")).all() and (lse[~up] == -float("inf")).all() and torch.isnan(loss).all()
+
+
+# ---- layer norm: very wide rows --------------------------------------------------
+
+@pytest.mark.parametrize("dim", [(1 << 25) + 21, (1 << 27) + 5])
+def test_layer_norm_backward_of_millions_of_columns(dev, mssm, dim):
+    """The columns' sums are added by more workgroups than one dimension of their
+    grid holds (from 2^27 columns on more threads than one could)."""
+    base.test_layer_norm_backward(dev, mssm, (2, dim), "bf16")
+    torch.cuda.empty_cache()
