@@ -436,9 +436,7 @@ def _workspace(nbytes, dev):
     """Scratch of a call from torch's allocator, whose blocks are 512-byte
     aligned and stay with the stream (and the graph capture) they are
     allocated on.  Returns (tensor or None, address or None, bytes)."""
-    if nbytes < 0:      # sizes the call itself refuses, with the reason
-        return None, None, 0
-    if nbytes == 0:
+    if nbytes <= 0:     # none needed, or sizes that the call refuses, with the reason
         return None, None, 0
     t = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
     return t, t.data_ptr(), nbytes
@@ -458,7 +456,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
 
     x: (..., dim) float32 or bfloat16; weight, bias: (dim,) float32 (None: 1
     and 0).  Returns ``(y, mean, rstd)``: y like x, mean and rstd (...)
-    float32, which the backward takes.
+    float32, which the backward takes (NaN where dim is 0).
     """
     L = _lib.lib()
     dev = _on_gpu(x)
@@ -475,6 +473,9 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
     y = _output(out, x)
     mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
     rstd = torch.empty_like(mean)
+    if dim == 0:    # of no values, and the library has nothing to do
+        mean.fill_(float("nan"))
+        rstd.fill_(float("nan"))
     with _on_device(dev):
         st = L.mssm_layer_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), float(eps), _ptr(y),
                                    _ptr(mean), _ptr(rstd), _lib.NormDims(rows, dim),

@@ -271,3 +271,14 @@ def test_layer_norm_backward_of_millions_of_columns(dev, mssm, dim):
     grid holds (from 2^27 columns on more threads than one could)."""
     base.test_layer_norm_backward(dev, mssm, (2, dim), "bf16")
     torch.cuda.empty_cache()
+
+
+def test_layer_norm_without_columns(dev, mssm):
+    """The mean of no values is NaN; nothing that memory held before is returned."""
+    for io in IO.values():
+        torch.full((5,), 3.0, device=dev)    # freed: what an unwritten result would hold
+        y, mean, rstd = mssm.layer_norm_fwd(torch.empty(5, 0, dtype=io, device=dev))
+        assert y.shape == (5, 0) and mean.shape == rstd.shape == (5,)
+        assert torch.isnan(mean).all() and torch.isnan(rstd).all()
+        g = mssm.layer_norm_bwd(y, y.clone(), mean, rstd)
+        assert g["dx"].shape == (5, 0) and g["dweight"].shape == g["dbias"].shape == (0,)
