@@ -112,9 +112,16 @@ def check_gates_backward(mssm, x, r, i, lam, h0, dh_last, names=("dx", "di", "dr
     dy = randn(x.device, *x.shape, seed=11, dtype=x.dtype)
     got = mssm.gated_recurrence_bwd(x, r, i, lam, y, dy, 8.0, h0=h0, dh_last=dh_last)
     want = layers.gated_recurrence_grad(x, r, i, lam, y, dy, 8.0, h0, dh_last)
+    _, a, _, _, _, d_a, _ = gate_bounds(r, lam)
+    d_g, d_h0 = walk_back(a, dy, d_a, dh_last)
+    within_grads(got, want, x, r, i, lam, y, h0, d_g, d_h0, names)
+    return got
+
+
+def within_grads(got, want, x, r, i, lam, y, h0, d_g, d_h0, names=("dx", "di", "dr", "dh0", "dlam")):
+    """d_g, d_h0: how far g and what leaves the first step are off."""
     la, a, m, sr, d_la, d_a, d_m = gate_bounds(r, lam)
     si, ax = torch.sigmoid(i.double()), x.double().abs()
-    d_g, d_h0 = walk_back(a, dy, d_a, dh_last)
     g = want["g"].abs()
     rel_s = (3 * i.double().abs() + 12) * U32
     d_gm = d_g * m + g * d_m + 2 * U32 * g * m
@@ -140,7 +147,6 @@ def check_gates_backward(mssm, x, r, i, lam, h0, dh_last, names=("dx", "di", "dr
     for key in names:
         extra = base.half_step(want[key], got[key]) * 1.01 if key in ("dx", "di", "dr") else 0
         within(got[key], want[key], bounds[key] + extra, key)
-    return got
 
 
 CLOSED = [0.0, -70.0, -80.0, -83.0, -85.0, -86.0, -86.5, -87.0, -87.5, -88.0, -95.0, -104.0]
@@ -282,3 +288,92 @@ def test_layer_norm_without_columns(dev, mssm):
         assert torch.isnan(mean).all() and torch.isnan(rstd).all()
         g = mssm.layer_norm_bwd(y, y.clone(), mean, rstd)
         assert g["dx"].shape == (5, 0) and g["dweight"].shape == g["dbias"].shape == (0,)
+
+
+# ---- gated linear recurrence: more segments than one published state covers --------
+
+def walk(a, b, start):
+    """s_t = a_t s_{t-1} + b_t along dim 1 in 64 bits: stretches side by side, then
+    what enters each."""
+    batch, steps, dim = a.shape
+    width = 512
+    count = -(-steps // width)
+    s = torch.zeros(batch, count * width, dim, dtype=torch.float64, device=a.device)
+    p = torch.ones_like(s)
+    s[:, :steps], p[:, :steps] = b, a
+    s, p = s.view(batch, count, width, dim), p.view(batch, count, width, dim)
+    for k in range(1, width):
+        s[:, :, k] += p[:, :, k] * s[:, :, k - 1]
+        p[:, :, k] *= p[:, :, k - 1]
+    for k in range(count):
+        s[:, k] += p[:, k] * start[:, None]
+        start = s[:, k, -1]
+    return s.view(batch, -1, dim)[:, :steps]
+
+
+def before_of(s, start):
+    return torch.cat([start[:, None], s[:, :-1]], 1)
+
+
+# io, dim, steps, steps of a span of 512 segments forward
+SPANS = [("bf16", 2, 200003, 512 * 176), ("f32", 3, 120007, 512 * 110), ("bf16", 3, 120007, 512 * 110)]
+
+
+def span_inputs(dev, io, dim, steps, span):
+    """Decays that remember most of a span, and inputs of one sign that swell and
+    fade over part of one: a state that is missing, late or of another span shows,
+    and the bound, relative to sums of magnitudes, is relative to the states."""
+    t = torch.arange(steps, device=dev, dtype=torch.float64)[None, :, None]
+    phase = torch.arange(dim, device=dev, dtype=torch.float64)[None, None]
+    swell = (1 + 0.9 * torch.sin(t * (6.28 / (0.6 * span)) + phase)).float()
+    x, dy = (randn(dev, 2, steps, dim, seed=k).abs().mul(swell).to(IO[io]) for k in (1, 5))
+    i = randn(dev, 2, steps, dim, seed=2, dtype=IO[io])
+    r = randn(dev, 2, steps, dim, seed=3, dtype=IO[io], scale=0.2)
+    lam = torch.full((dim,), 2 / (0.7 * span) / 8, dtype=torch.float64, device=dev).expm1().log().float()
+    return x, r, i, lam, dy
+
+
+@pytest.mark.parametrize("io,dim,steps,span", SPANS)
+def test_gated_recurrence_forward_over_spans(dev, mssm, io, dim, steps, span):
+    announce("spans fwd", io, dim, steps)
+    assert steps > 2 * span
+    x, r, i, lam, _ = span_inputs(dev, io, dim, steps, span)
+    h0 = randn(dev, 2, dim, seed=4).abs() * 300
+    y, last = mssm.gated_recurrence_fwd(x, r, i, lam, 8.0, h0=h0)
+    _, a, m, _, _, d_a, d_m = gate_bounds(r, lam)
+    si = torch.sigmoid(i.double())
+    b = m * si * x.double()
+    d_b = si * x.double() * d_m + b * (3 * i.double().abs() + 20) * U32
+    yo = walk(a, b, h0.double())
+    bound = walk(a, 2 * ((d_a + U32 * a) * before_of(yo, h0.double()) + d_b + 2 * U32 * yo), 0 * h0.double())
+    assert (bound / yo).max() < 0.1
+    within(last, yo[:, -1], bound[:, -1], "h_last")
+    within(y, yo, bound + base.half_step(yo, y) * 1.01, "y")
+
+
+@pytest.mark.parametrize("io,dim,steps,span", SPANS)
+def test_gated_recurrence_backward_over_spans(dev, mssm, io, dim, steps, span):
+    """The backward's segments are shorter: three spans and more."""
+    announce("spans bwd", io, dim, steps)
+    x, r, i, lam, dy = span_inputs(dev, io, dim, steps, span)
+    h0, dh_last = randn(dev, 2, dim, seed=4).abs() * 300, randn(dev, 2, dim, seed=6).abs() * 1e4
+    la, a, m, sr, _, d_a, _ = gate_bounds(r, lam)
+    si, X = torch.sigmoid(i.double()), x.double()
+    y = walk(a, m * si * X, h0.double()).to(IO[io])
+    got = mssm.gated_recurrence_bwd(x, r, i, lam, y, dy, 8.0, h0=h0, dh_last=dh_last)
+    # from the end, the carry G' = a (dy + G): everything is positive, so that
+    # sizes are the values
+    back = lambda v: v.flip(1)  # noqa: E731
+    out = walk(back(a), back(a * dy.double()), dh_last.double())
+    carry = before_of(out, dh_last.double())
+    g = dy.double() + back(carry)
+    # an error that enters at a step: of the sum, then of its product with the decay
+    e = walk(back(a), back(a) * 2 * U32 * back(g) + 2 * (back(d_a) + U32 * back(a)) * back(g), 0 * dh_last.double())
+    d_g = back(before_of(e, 0 * dh_last.double())) + 2 * U32 * g
+    assert (d_g / g).max() < 0.1
+    before = before_of(y.double(), h0.double())
+    w = g * before * a * la - g * si * X * a * a * la / m
+    lam64 = lam.double()
+    want = {"g": g, "w": w, "dx": g * m * si, "dr": w * (1 - sr), "di": g * m * si * X * (1 - si), "dh0": out[:, -1],
+            "dlam": w.sum((0, 1)) * torch.sigmoid(lam64) / layers.softplus(lam64)}
+    within_grads(got, want, x, r, i, lam, y, h0, d_g, e[:, -1] + 2 * U32 * out[:, -1])
