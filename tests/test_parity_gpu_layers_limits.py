@@ -377,3 +377,17 @@ def test_gated_recurrence_backward_over_spans(dev, mssm, io, dim, steps, span):
     want = {"g": g, "w": w, "dx": g * m * si, "dr": w * (1 - sr), "di": g * m * si * X * (1 - si), "dh0": out[:, -1],
             "dlam": w.sum((0, 1)) * torch.sigmoid(lam64) / layers.softplus(lam64)}
     within_grads(got, want, x, r, i, lam, y, h0, d_g, e[:, -1] + 2 * U32 * out[:, -1])
+
+
+# ---- layer norm: every group of lanes goes over several rows -----------------------
+
+@pytest.mark.parametrize("shape", [(70001, 5), (70001, 40), (40009, 128), (20011, 250), (9001, 513), (6145, 2560),
+                                   (6149, 2048), (2100, 2600), (1100, 9999), (600, 12001)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_layer_norm_rows_in_turn(dev, mssm, shape, io):
+    """Rows held by 8 to 1024 lanes, at least two of them and mostly three or more
+    in turn in each direction, the last turn not full; the bounds are those of the
+    other sizes."""
+    announce("norm rows in turn", shape, io)
+    base.test_layer_norm_forward(dev, mssm, shape, io)
+    base.test_layer_norm_backward(dev, mssm, shape, io)
