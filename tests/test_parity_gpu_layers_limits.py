@@ -391,3 +391,33 @@ def test_layer_norm_rows_in_turn(dev, mssm, shape, io):
     announce("norm rows in turn", shape, io)
     base.test_layer_norm_forward(dev, mssm, shape, io)
     base.test_layer_norm_backward(dev, mssm, shape, io)
+
+
+# ---- projected cross entropy: several pieces of the vocabulary, rows copied ---------
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_linear_cross_entropy_forward_over_copied_pieces(dev, mssm, io):
+    """An odd width: weight is copied to aligned rows in two pieces of the
+    vocabulary (52224 words, then 7789), with targets at both pieces' ends."""
+    tokens, dim, vocab = 40, 2557, 60013
+    announce("loss fwd, copied pieces", io)
+    hidden, weight, targets = base.loss_inputs(dev, (tokens, dim, vocab), io)
+    targets[:8] = torch.tensor([0, 1, 52222, 52223, 52224, 52225, vocab - 2, vocab - 1], device=dev)
+    loss, lse = mssm.linear_cross_entropy_fwd(hidden, weight, targets)
+    lo, so = layers.linear_cross_entropy(hidden, weight, targets)
+    logits = hidden.double() @ weight.double().t()
+    # as test_linear_cross_entropy_forward
+    d = base.logit_bound(hidden, weight).amax(1) + (vocab + 16 + 2 * (logits.amax(1) - logits.amin(1))) * U32
+    d = d + 4 * U32 * so.abs()
+    within(lse, so, d, "lse")
+    within(loss, lo, 2 * d + 2 * U32 * (so.abs() + logits.abs().amax(1)), "loss")
+    assert (loss[targets == -100] == 0).all()
+
+
+@pytest.mark.parametrize("shape", [(4099, 41, 40001), (2500, 33, 60000)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_linear_cross_entropy_backward_over_copied_pieces(dev, mssm, shape, io):
+    """The backward with copied rows over pieces of which the last is shorter."""
+    announce("loss bwd, copied pieces", shape, io)
+    base.test_linear_cross_entropy_backward(dev, mssm, shape, io)
+    torch.cuda.empty_cache()
