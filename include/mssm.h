@@ -549,7 +549,8 @@ typedef struct {
  *   loss[t] = lse[t] - l[targets[t]]      0 where targets[t] == ignore_index
  *
  * A target outside [0, vocab) that is not ignore_index reads nothing out of
- * range: its loss is NaN.
+ * range: its loss is NaN.  A logit of +infinity makes lse, and the loss of every
+ * other word, infinite.
  *
  * Arguments (device pointers unless stated):
  *   hidden   (tokens, dim), dtype `io`     required

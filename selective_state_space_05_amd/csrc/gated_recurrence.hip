@@ -13,8 +13,8 @@
 // b = a dy), so a run of steps composes into one pair (A, H): s <- A s + H.
 // The operator reads three tensors and writes one (backward: five and three),
 // so it is bound by HBM if it reads them once; in bfloat16 the forward's
-// vector work (36 instructions an element, six of them transcendental) takes
-// 42 us where its 8 bytes an element take 54 us (2 x 4096 steps of 5120
+// vector work (37 instructions an element, six of them transcendental) takes
+// 43 us where its 8 bytes an element take 54 us (2 x 4096 steps of 5120
 // channels).  Hence one pass, in which loads, arithmetic and the passing of
 // carries all go on at the same time, one workgroup of twelve waves a compute
 // unit:

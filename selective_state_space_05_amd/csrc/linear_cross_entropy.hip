@@ -22,8 +22,8 @@
 //
 // Bound by the matrix cores and, at their full rate, by the clock that the card
 // holds under them (1.75 to 2.0 GHz); few tokens by the read of weight.  Measured at
-// width 2560 and 50021 words in bfloat16: 8192 tokens forward 1.80 to 1.87 ms (1.12
-// to 1.17 PFLOP/s), backward 5.65 to 5.77 ms (1.09 to 1.11), 16 tokens forward 66 us
+// width 2560 and 50021 words in bfloat16: 8192 tokens forward 1.76 to 1.87 ms (1.12
+// to 1.19 PFLOP/s), backward 5.65 to 5.77 ms (1.09 to 1.11), 16 tokens forward 66 us
 // (58 us of it reading weight at 4.4 TB/s); float32, 2048 tokens of width 1024 and
 // 32000 words, forward 1.0 ms (134 TFLOP/s).
 #include "device_math.h"
