@@ -606,6 +606,239 @@ MSSM_API mssm_status mssm_linear_cross_entropy_bwd(const void *hidden,
                                 int64_t workspace_bytes, mssm_loss_dims dims,
                                 mssm_dtypes dtypes, void *stream);
 
+/* Largest head of the norm with rotation and of the linear attention, most
+ * beams of an entry and most candidates of a selection. */
+#define MSSM_MAX_HEAD_DIM 256
+#define MSSM_MAX_BEAMS 32
+#define MSSM_MAX_BEAM_COUNT 64
+
+/* Sizes of a norm of queries and keys with their rotation. */
+typedef struct {
+    int64_t tokens;   /* >= 0 */
+    int64_t q_heads;  /* >= 0 */
+    int64_t k_heads;  /* >= 0 */
+    int64_t dim;      /* of a head, 1 <= dim <= MSSM_MAX_HEAD_DIM */
+    int64_t rotary;   /* values of a head that are rotated: even, 0 <= rotary <= dim */
+} mssm_head_norm_dims;
+
+/*
+ * Norm of queries and keys for each head, with their rotation by position in
+ * the same pass.  For every token and head x, with R = rotary:
+ *
+ *   n[d]       = x[d] * weight[d] / sqrt(sum_d x[d]^2 / dim + eps)
+ *   a[j]       = positions[token] * base^(-2 j / R)            j < R/2
+ *   y[j]       = n[j] cos a[j] - n[j + R/2] sin a[j]
+ *   y[j + R/2] = n[j + R/2] cos a[j] + n[j] sin a[j];   y[d] = n[d] for d >= R
+ *
+ * Angles are formed in float64 and reduced to a fraction of a turn, so far
+ * positions keep their digits.
+ *
+ * Arguments (device pointers unless stated):
+ *   q          (tokens, q_heads, dim), dtype `io`   required
+ *   k          (tokens, k_heads, dim), dtype `io`   required
+ *   positions  (tokens) int64                       required (any value) if
+ *                                                   rotary > 0
+ *   q_weight, k_weight  (dim) float32               nullable -> 1
+ *   base       (host) > 0 and finite
+ *   eps        (host) >= 0 and finite
+ *   q_out, k_out  like q and k                      required (outputs)
+ * Operands with no elements may be null.
+ * Errors: MSSM_ERR_INVALID_ARG for a null required pointer, a negative size,
+ * dim < 1, a rotary that is odd or outside [0, dim], an unknown dtype, a bad
+ * base or eps, or an output overlapping an input or another output;
+ * MSSM_ERR_UNSUPPORTED for param dtype != F32, dim > MSSM_MAX_HEAD_DIM or
+ * tokens * heads >= 2^31.  No elements: nothing to do, MSSM_OK.
+ */
+MSSM_API mssm_status mssm_qk_norm_rotary_fwd(const void *q, const void *k,
+                                const int64_t *positions,
+                                const float *q_weight, const float *k_weight,
+                                double base, float eps, void *q_out,
+                                void *k_out, mssm_head_norm_dims dims,
+                                mssm_dtypes dtypes, void *stream);
+
+/*
+ * Backward of the norm with rotation, for the gradients dq_out and dk_out of
+ * its outputs; the norms are formed again.  With dn the gradient turned back by
+ * the token's angles, r = 1 / sqrt(mean(x^2) + eps) and e = dn * weight, per head:
+ *
+ *   dx[d]      = r * (e[d] - x[d] * r^2 * mean_d(e * x))
+ *   dweight[d] = sum over tokens and heads of dn[d] * x[d] * r
+ *
+ *   dq_out, dk_out  like q and k                    required
+ *   dq, dk          like q and k                    required (outputs)
+ *   dq_weight, dk_weight  (dim) float32             nullable (outputs)
+ * The weights' gradients are summed in an order that depends on the sizes
+ * alone (repeatable bit for bit), through partial sums in the workspace; they
+ * are zero without tokens.  Errors as for the forward.
+ */
+MSSM_API mssm_status mssm_qk_norm_rotary_bwd(const void *dq_out, const void *dk_out,
+                                const void *q, const void *k,
+                                const int64_t *positions,
+                                const float *q_weight, const float *k_weight,
+                                double base, float eps, void *dq, void *dk,
+                                float *dq_weight, float *dk_weight,
+                                void *workspace, int64_t workspace_bytes,
+                                mssm_head_norm_dims dims, mssm_dtypes dtypes,
+                                void *stream);
+MSSM_API int64_t mssm_qk_norm_rotary_bwd_workspace(mssm_head_norm_dims dims,
+                                mssm_dtypes dtypes);
+
+/* Sizes of a linear attention. */
+typedef struct {
+    int64_t seqs;    /* sequences >= 0 */
+    int64_t seqlen;  /* steps of each >= 0; with cu_seqlens the longest one's,
+                        or an estimate: longer ones come out right, slower */
+    int64_t total;   /* rows of q, k, v: seqs * seqlen, or of the packed tensors */
+    int64_t heads;   /* >= 0 */
+    int64_t key;     /* values of a query or key head, 1 <= key <= MSSM_MAX_HEAD_DIM */
+    int64_t value;   /* values of a value head, 1 <= value <= MSSM_MAX_HEAD_DIM */
+} mssm_attention_dims;
+
+/*
+ * Linear attention with a decay per head.  For every sequence and head, from
+ * S = h0:
+ *
+ *   S   = exp(log_decay[h]) * S + k[t] v[t]^T          (key, value)
+ *   o[t] = scale * S^T q[t];   h_last = S after the last step
+ *
+ * Arguments (device pointers unless stated):
+ *   q, k       (total, heads, key), dtype `io`      required
+ *   v          (total, heads, value), dtype `io`    required
+ *   log_decay  (heads) float32                      required, expected <= 0
+ *   scale      (host) finite
+ *   h0         (seqs, heads, key, value) float32    nullable -> 0; may be the
+ *                                                   very buffer passed as h_last
+ *   cu_seqlens (seqs + 1) int64                     nullable: sequence b is rows
+ *              cu_seqlens[b] .. cu_seqlens[b + 1] - 1; null: rows b * seqlen on.
+ *              Offsets have to rise from 0 or more to at most total; others are
+ *              held to that range, so that nothing outside is read or written.
+ *   o          (total, heads, value), dtype `io`    required (output); rows in
+ *              front of the first and behind the last sequence are set to 0
+ *   h_last     (seqs, heads, key, value) float32    nullable (output)
+ * A sequence of no steps has h_last = h0.  Sequences are walked in chunks whose
+ * products run on the matrix cores: float32 sums of exact products of bfloat16
+ * values; inside a chunk the decayed products q.k, and the state as it meets q,
+ * enter as bfloat16 where `io` is bfloat16 (float32 otherwise), while the state
+ * itself is carried in float32.  Results are repeatable bit for bit.
+ * Errors as for mssm_selective_scan_fwd; also MSSM_ERR_INVALID_ARG for a scale
+ * that is not finite, key or value < 1, or total != seqs * seqlen without
+ * cu_seqlens; MSSM_ERR_UNSUPPORTED for key or value > MSSM_MAX_HEAD_DIM,
+ * seqs * heads >= 2^20 or total >= 2^31.  seqs == 0 or heads == 0: o is zeroed.
+ */
+MSSM_API mssm_status mssm_linear_attention_fwd(const void *q, const void *k,
+                                const void *v, const float *log_decay,
+                                float scale, const float *h0,
+                                const int64_t *cu_seqlens, void *o,
+                                float *h_last, void *workspace,
+                                int64_t workspace_bytes,
+                                mssm_attention_dims dims, mssm_dtypes dtypes,
+                                void *stream);
+/* For the forward (backward == 0) or the backward. */
+MSSM_API int64_t mssm_linear_attention_workspace(mssm_attention_dims dims,
+                                mssm_dtypes dtypes, int backward);
+
+/*
+ * Backward of the linear attention, for the gradients d_o of o and dh_last of
+ * h_last.  With R_t = scale * q_t d_o_t^T + exp(log_decay) R_{t+1} (dh_last added
+ * at the last step):
+ *
+ *   dq_t = scale * S_t d_o_t,   dk_t = R_t v_t,   dv_t = R_t^T k_t
+ *   dh0  = exp(log_decay) R_0
+ *
+ * The states are formed again.  The decays are constants of the model and have
+ * no gradient.
+ *   d_o      (total, heads, value), dtype `io`      required
+ *   dh_last  (seqs, heads, key, value) float32      nullable -> 0
+ *   dq, dk   like q; dv like v                      required (outputs); rows of
+ *            no sequence as for o
+ *   dh0      (seqs, heads, key, value) float32      nullable (output)
+ * Rounding as in the forward.  Errors as for the forward; no output may overlap
+ * an input or another output.
+ */
+MSSM_API mssm_status mssm_linear_attention_bwd(const void *q, const void *k,
+                                const void *v, const float *log_decay,
+                                float scale, const float *h0,
+                                const int64_t *cu_seqlens, const void *d_o,
+                                const float *dh_last, void *dq, void *dk,
+                                void *dv, float *dh0, void *workspace,
+                                int64_t workspace_bytes,
+                                mssm_attention_dims dims, mssm_dtypes dtypes,
+                                void *stream);
+
+/*
+ * One decode step of the linear attention on a cached state, in place: the
+ * forward at one step with h0 = h_last = state, in float32 throughout.
+ *
+ *   state    (seqs, heads, key, value) float32      required, read and overwritten
+ *   q, k     (seqs, heads, key), v, o (seqs, heads, value), dtype `io`  required
+ * `seqlen` and `total` are ignored.  Errors as for the forward; state and o must
+ * not overlap any input or each other.
+ */
+MSSM_API mssm_status mssm_linear_attention_update(float *state, const void *q,
+                                const void *k, const void *v,
+                                const float *log_decay, float scale, void *o,
+                                mssm_attention_dims dims, mssm_dtypes dtypes,
+                                void *stream);
+
+/* Sizes of a selection of beams. */
+typedef struct {
+    int64_t batch;   /* entries >= 0 */
+    int64_t beams;   /* of an entry, 1 <= beams <= MSSM_MAX_BEAMS */
+    int64_t vocab;   /* >= 1 */
+    int64_t count;   /* candidates, 1 <= count <= min(MSSM_MAX_BEAM_COUNT, beams * vocab) */
+} mssm_beam_dims;
+
+/*
+ * A beam search's selection over beams and vocabulary.  For every entry, the
+ * `count` largest of
+ *
+ *   value[j, v] = scores[j] + logits[j, v] - log sum_v exp(logits[j, v])
+ *
+ * in order, equal ones by the lowest j * vocab + v.  A beam whose score or
+ * log sum exp is not finite (a finished or empty beam, NaN or +infinity among
+ * its logits, no finite logit) counts as -infinity for every word.
+ *
+ *   logits   (batch, beams, vocab), dtype `io`      required
+ *   scores   (batch, beams) float32                 required
+ *   out_scores  (batch, count) float32              required (output): the values
+ *   out_tokens, out_beams  (batch, count) int64     required (outputs): v and j
+ * Values are compared in float64, logits exactly; the sum of the exponentials is
+ * float32.  Errors: as for mssm_layer_norm_fwd; also MSSM_ERR_INVALID_ARG for
+ * beams, vocab or count < 1 or count > beams * vocab, MSSM_ERR_UNSUPPORTED for
+ * beams > MSSM_MAX_BEAMS, count > MSSM_MAX_BEAM_COUNT, vocab >= 2^30 or
+ * batch * beams * vocab >= 2^36.  batch == 0: nothing to do, MSSM_OK.
+ */
+MSSM_API mssm_status mssm_beam_select(const void *logits, const float *scores,
+                                float *out_scores, int64_t *out_tokens,
+                                int64_t *out_beams, void *workspace,
+                                int64_t workspace_bytes, mssm_beam_dims dims,
+                                mssm_dtypes dtypes, void *stream);
+MSSM_API int64_t mssm_beam_select_workspace(mssm_beam_dims dims, mssm_dtypes dtypes);
+
+/*
+ * Reorders the states of beams in place: for every state and entry b,
+ *
+ *   row (b, j) <- row (b, origins[b, j])       j < beams
+ *
+ * all rows at once, so beams may continue one another in any way.  Beams with
+ * origins[b, j] == j are neither read nor written; an origin outside [0, beams)
+ * leaves its beam as it is.
+ *
+ *   states     (host) array of `count` device pointers: (batch, beams, row_bytes[i])
+ *              bytes each, of any alignment
+ *   row_bytes  (host) array of `count` sizes >= 0
+ *   origins    (batch, beams) int64, device                required
+ * The host arrays may be reused when the call returns.  dims.vocab and
+ * dims.count are ignored.  Errors: MSSM_ERR_INVALID_ARG for a null pointer, a
+ * negative size or states that overlap each other or origins;
+ * MSSM_ERR_UNSUPPORTED for beams > MSSM_MAX_BEAMS or a state whose entries have
+ * 2^24 or more pieces of 256 times 16 bytes (4 or 1, where its address or row is
+ * not a multiple of 16 or 4 bytes).  batch == 0 or count == 0: nothing to do.
+ */
+MSSM_API mssm_status mssm_state_reorder(void *const *states, const int64_t *row_bytes,
+                                int64_t count, const int64_t *origins,
+                                mssm_beam_dims dims, void *stream);
+
 /* Force a kernel variant for subsequent calls made by THIS thread
  * (MSSM_VARIANT_AUTO restores the shape-based choice).  A variant that does
  * not apply to the entry point or shape makes that call return

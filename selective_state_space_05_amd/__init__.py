@@ -10,24 +10,33 @@ call raises -- there is no CPU fallback.
 """
 from .api import (  # noqa: F401
     MssmError,
+    beam_select,
     gated_recurrence_bwd,
     gated_recurrence_fwd,
     gated_recurrence_update,
     layer_norm_bwd,
     layer_norm_fwd,
+    linear_attention_bwd,
+    linear_attention_fwd,
+    linear_attention_update,
     linear_cross_entropy_bwd,
     linear_cross_entropy_fwd,
+    qk_norm_rotary_bwd,
+    qk_norm_rotary_fwd,
     selective_scan_bwd,
     selective_scan_conv_fwd,
     selective_scan_fwd,
     selective_scan_fwd_noalloc,
     selective_state_update,
     ssd_scalar_fwd,
+    state_reorder,
     version,
 )
 
-__all__ = ["MssmError", "gated_recurrence_bwd", "gated_recurrence_fwd", "gated_recurrence_update",
-           "layer_norm_bwd", "layer_norm_fwd", "linear_cross_entropy_bwd",
-           "linear_cross_entropy_fwd", "selective_scan_bwd", "selective_scan_conv_fwd",
-           "selective_scan_fwd", "selective_scan_fwd_noalloc", "selective_state_update",
-           "ssd_scalar_fwd", "version"]
+__all__ = ["MssmError", "beam_select", "gated_recurrence_bwd", "gated_recurrence_fwd",
+           "gated_recurrence_update", "layer_norm_bwd", "layer_norm_fwd", "linear_attention_bwd",
+           "linear_attention_fwd", "linear_attention_update", "linear_cross_entropy_bwd",
+           "linear_cross_entropy_fwd", "qk_norm_rotary_bwd", "qk_norm_rotary_fwd",
+           "selective_scan_bwd", "selective_scan_conv_fwd", "selective_scan_fwd",
+           "selective_scan_fwd_noalloc", "selective_state_update", "ssd_scalar_fwd",
+           "state_reorder", "version"]

@@ -67,6 +67,16 @@ EXPORTED = (
     "mssm_linear_cross_entropy_workspace",
     "mssm_linear_cross_entropy_fwd",
     "mssm_linear_cross_entropy_bwd",
+    "mssm_qk_norm_rotary_fwd",
+    "mssm_qk_norm_rotary_bwd",
+    "mssm_qk_norm_rotary_bwd_workspace",
+    "mssm_linear_attention_fwd",
+    "mssm_linear_attention_bwd",
+    "mssm_linear_attention_update",
+    "mssm_linear_attention_workspace",
+    "mssm_beam_select",
+    "mssm_beam_select_workspace",
+    "mssm_state_reorder",
 )
 # Every symbol include/mssm_probes.h declares (measurement probes).
 EXPORTED_PROBES = (
@@ -107,6 +117,23 @@ class RecurrenceDims(ctypes.Structure):
 class LossDims(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("vocab", ctypes.c_int64)]
+
+
+class HeadNormDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+                ("k_heads", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("rotary", ctypes.c_int64)]
+
+
+class AttentionDims(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("total", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("key", ctypes.c_int64), ("value", ctypes.c_int64)]
+
+
+class BeamDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("beams", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("count", ctypes.c_int64)]
 
 
 class DTypes(ctypes.Structure):
@@ -175,6 +202,30 @@ def _declare(L):
     L.mssm_gated_recurrence_workspace.restype = i64
     L.mssm_linear_cross_entropy_workspace.argtypes = [LossDims, DTypes, ctypes.c_int, ctypes.c_int]
     L.mssm_linear_cross_entropy_workspace.restype = i64
+    f64 = ctypes.c_double
+    L.mssm_qk_norm_rotary_fwd.argtypes = [vp, vp, vp, fp, fp, f64, f32, vp, vp, HeadNormDims, DTypes, vp]
+    L.mssm_qk_norm_rotary_fwd.restype = ctypes.c_int
+    L.mssm_qk_norm_rotary_bwd.argtypes = [vp, vp, vp, vp, vp, fp, fp, f64, f32, vp, vp, fp, fp, vp,
+                                          i64, HeadNormDims, DTypes, vp]
+    L.mssm_qk_norm_rotary_bwd.restype = ctypes.c_int
+    L.mssm_qk_norm_rotary_bwd_workspace.argtypes = [HeadNormDims, DTypes]
+    L.mssm_qk_norm_rotary_bwd_workspace.restype = i64
+    L.mssm_linear_attention_fwd.argtypes = [vp, vp, vp, fp, f32, fp, vp, vp, fp, vp, i64,
+                                            AttentionDims, DTypes, vp]
+    L.mssm_linear_attention_fwd.restype = ctypes.c_int
+    L.mssm_linear_attention_bwd.argtypes = [vp, vp, vp, fp, f32, fp, vp, vp, fp, vp, vp, vp, fp, vp,
+                                            i64, AttentionDims, DTypes, vp]
+    L.mssm_linear_attention_bwd.restype = ctypes.c_int
+    L.mssm_linear_attention_update.argtypes = [fp, vp, vp, vp, fp, f32, vp, AttentionDims, DTypes, vp]
+    L.mssm_linear_attention_update.restype = ctypes.c_int
+    L.mssm_linear_attention_workspace.argtypes = [AttentionDims, DTypes, ctypes.c_int]
+    L.mssm_linear_attention_workspace.restype = i64
+    L.mssm_beam_select.argtypes = [vp, fp, fp, vp, vp, vp, i64, BeamDims, DTypes, vp]
+    L.mssm_beam_select.restype = ctypes.c_int
+    L.mssm_beam_select_workspace.argtypes = [BeamDims, DTypes]
+    L.mssm_beam_select_workspace.restype = i64
+    L.mssm_state_reorder.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(i64), i64, vp, BeamDims, vp]
+    L.mssm_state_reorder.restype = ctypes.c_int
     L.mssm_force_variant.argtypes = [ctypes.c_int]
     L.mssm_force_variant.restype = ctypes.c_int
     L.mssm_last_variant.argtypes = []

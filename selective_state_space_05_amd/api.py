@@ -7,6 +7,7 @@ to the C ABI.  No arithmetic of the method happens here.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import torch
 
@@ -101,7 +102,6 @@ def last_variant() -> int:
 def device_status(clear: bool = False) -> int:
     """Status bits the library's kernels set on the current device
     (``_lib.DEVICE_LOOKBACK_TIMEOUT``); waits for the device first."""
-    import ctypes
     bits = ctypes.c_uint32(0)
     _check(_lib.lib().mssm_device_status(ctypes.byref(bits), 1 if clear else 0))
     return int(bits.value)
@@ -681,6 +681,272 @@ def linear_cross_entropy_bwd(hidden, weight, targets, lse, dloss, ignore_index=-
                                              dims, dt, _stream_handle(dev))
     _check(st)
     return g
+
+
+def _head_norm_args(q, k, positions, q_weight, k_weight, rotary_dim):
+    """Shared checks of the norm with rotation; returns (device, dims, dtypes)."""
+    dev = _on_gpu(q)
+    io = _io_dtype(q)
+    _need(q, "q")
+    if k is None:
+        raise ValueError("k is required")
+    _need(k, "k", q.dtype, dev)
+    if q.dim() < 2 or k.dim() != q.dim() or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+        raise ValueError("q and k must be (..., heads, dim) of the same tokens and dim")
+    dim = q.shape[-1]
+    rotary = dim // 2 * 2 if rotary_dim is None else int(rotary_dim)
+    if positions is None:
+        raise ValueError("positions is required")
+    _need(positions, "positions", torch.int64, dev)
+    _need_shape(positions, "positions", q.shape[:-2])
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _need(t, name, torch.float32, dev)
+        _need_shape(t, name, (dim,))
+    return (dev, _lib.HeadNormDims(positions.numel(), q.shape[-2], k.shape[-2], dim, rotary),
+            _lib.DTypes(io, _lib.MSSM_F32))
+
+
+def qk_norm_rotary_fwd(q, k, positions, q_weight=None, k_weight=None, base=10000.0, eps=1e-6,
+                       rotary_dim=None):
+    """Root-mean-square norm of queries and keys for each head, with their
+    rotation by position in the same pass, on the GPU.
+
+    q: (..., q_heads, dim), k: (..., k_heads, dim) float32 or bfloat16 (one
+    dtype), dim up to 256; positions: (...) int64; weights: (dim,) float32
+    (None: 1).  The first ``rotary_dim`` values of a head (None: all, an odd last
+    one left out) are rotated, value j with value j + rotary_dim / 2 by the angle
+    position * base^(-2 j / rotary_dim).  Returns ``(q, k)`` normed and rotated.
+    """
+    L = _lib.lib()
+    dev, dims, dt = _head_norm_args(q, k, positions, q_weight, k_weight, rotary_dim)
+    q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+    with _on_device(dev):
+        st = L.mssm_qk_norm_rotary_fwd(_ptr(q), _ptr(k), _ptr(positions), _ptr(q_weight), _ptr(k_weight),
+                                       float(base), float(eps), _ptr(q_out), _ptr(k_out), dims, dt,
+                                       _stream_handle(dev))
+    _check(st)
+    return q_out, k_out
+
+
+def qk_norm_rotary_bwd(dq, dk, q, k, positions, q_weight=None, k_weight=None, base=10000.0, eps=1e-6,
+                       rotary_dim=None):
+    """Gradients of the norm with rotation for the gradients ``dq`` and ``dk`` of
+    its outputs (like q and k).  Returns a dict: dq like q, dk like k, dq_weight
+    and dk_weight (dim,) float32."""
+    L = _lib.lib()
+    dev, dims, dt = _head_norm_args(q, k, positions, q_weight, k_weight, rotary_dim)
+    for name, t, like in (("dq", dq, q), ("dk", dk, k)):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        _need(t, name, like.dtype, dev)
+        _need_shape(t, name, like.shape)
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k),
+         "dq_weight": q.new_empty((q.shape[-1],), dtype=torch.float32),
+         "dk_weight": q.new_empty((q.shape[-1],), dtype=torch.float32)}
+    with _on_device(dev):
+        ws, at, nbytes = _workspace(L.mssm_qk_norm_rotary_bwd_workspace(dims, dt), dev)
+        st = L.mssm_qk_norm_rotary_bwd(_ptr(dq), _ptr(dk), _ptr(q), _ptr(k), _ptr(positions),
+                                       _ptr(q_weight), _ptr(k_weight), float(base), float(eps),
+                                       _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dq_weight"]),
+                                       _ptr(g["dk_weight"]), at, nbytes, dims, dt, _stream_handle(dev))
+    _check(st)
+    return g
+
+
+def _attention_args(q, k, v, log_decay, cu_seqlens, max_seqlen):
+    """Shared checks of the linear attention; returns (device, dims, dtypes)."""
+    dev = _on_gpu(q)
+    io = _io_dtype(q)
+    _need(q, "q")
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        _need(t, name, q.dtype, dev)
+    rank = 4 if cu_seqlens is None else 3
+    if q.dim() != rank or v.dim() != rank:
+        raise ValueError("q, k, v must be (batch, L, heads, width), or packed (total, heads, width) with cu_seqlens")
+    _need_shape(k, "k", q.shape)
+    _need_shape(v, "v", (*q.shape[:-1], v.shape[-1]))
+    heads = q.shape[-2]
+    if log_decay is None:
+        raise ValueError("log_decay is required")
+    _need(log_decay, "log_decay", torch.float32, dev)
+    _need_shape(log_decay, "log_decay", (heads,))
+    if cu_seqlens is None:
+        if max_seqlen is not None and int(max_seqlen) != q.shape[1]:
+            raise ValueError("max_seqlen goes with cu_seqlens")
+        seqs, seqlen = q.shape[:2]
+        total = seqs * seqlen
+    else:
+        _need(cu_seqlens, "cu_seqlens", torch.int64, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must be (sequences + 1,)")
+        seqs, total = cu_seqlens.shape[0] - 1, q.shape[0]
+        seqlen = -(-total // seqs) if max_seqlen is None and seqs else min(int(max_seqlen or 0), total)
+    return (dev, _lib.AttentionDims(seqs, seqlen, total, heads, q.shape[-1], v.shape[-1]),
+            _lib.DTypes(io, _lib.MSSM_F32))
+
+
+def _attention_states(dims, dev, **states):
+    for name, t in states.items():
+        _need(t, name, torch.float32, dev)
+        _need_shape(t, name, (dims.seqs, dims.heads, dims.key, dims.value))
+
+
+def linear_attention_fwd(q, k, v, log_decay, scale=1.0, h0=None, cu_seqlens=None, max_seqlen=None,
+                         return_last_state=True, out=None, h_out=None):
+    """Linear attention with a decay per head on the GPU:
+    S_t = exp(log_decay) S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t.
+
+    q, k: (batch, L, heads, key), v: (batch, L, heads, value) float32 or bfloat16
+    (one dtype), key and value up to 256; log_decay: (heads,) float32; h0:
+    (batch, heads, key, value) float32 initial states (None: zero; it may be
+    passed as ``h_out`` too, to advance states in place).  Sequences of different
+    lengths come packed, q, k: (total, heads, key), v: (total, heads, value), with
+    their first rows and the last one's end in ``cu_seqlens``: (batch + 1,) int64;
+    ``max_seqlen`` is the longest one's length (None: taken to be their mean; only
+    the time depends on it).  Returns ``(o, h_last)``: o like v (0 in rows of no
+    sequence), h_last like h0 (None if ``return_last_state`` is False).
+    """
+    L = _lib.lib()
+    dev, dims, dt = _attention_args(q, k, v, log_decay, cu_seqlens, max_seqlen)
+    _attention_states(dims, dev, h0=h0, h_out=h_out)
+    o = _output(out, v)
+    h_last = None
+    if return_last_state:
+        h_last = h_out if h_out is not None else torch.empty(
+            (dims.seqs, dims.heads, dims.key, dims.value), dtype=torch.float32, device=dev)
+    with _on_device(dev):
+        ws, at, nbytes = _workspace(L.mssm_linear_attention_workspace(dims, dt, 0), dev)
+        st = L.mssm_linear_attention_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), float(scale),
+                                         _ptr(h0), _ptr(cu_seqlens), _ptr(o), _ptr(h_last), at, nbytes,
+                                         dims, dt, _stream_handle(dev))
+    _check(st)
+    return o, h_last
+
+
+def linear_attention_bwd(q, k, v, log_decay, do, scale=1.0, h0=None, dh_last=None, cu_seqlens=None,
+                         max_seqlen=None):
+    """Gradients of the linear attention for output gradients ``do`` (like v) and
+    ``dh_last`` (like h0, None: zero).  Returns a dict: dq like q, dk like k, dv
+    like v, dh0 like h0.  The decays are constants and have no gradient."""
+    L = _lib.lib()
+    dev, dims, dt = _attention_args(q, k, v, log_decay, cu_seqlens, max_seqlen)
+    if do is None:
+        raise ValueError("do is required")
+    _need(do, "do", v.dtype, dev)
+    _need_shape(do, "do", v.shape)
+    _attention_states(dims, dev, h0=h0, dh_last=dh_last)
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+         "dh0": torch.empty((dims.seqs, dims.heads, dims.key, dims.value), dtype=torch.float32,
+                            device=dev)}
+    with _on_device(dev):
+        ws, at, nbytes = _workspace(L.mssm_linear_attention_workspace(dims, dt, 1), dev)
+        st = L.mssm_linear_attention_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), float(scale),
+                                         _ptr(h0), _ptr(cu_seqlens), _ptr(do), _ptr(dh_last),
+                                         _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dh0"]),
+                                         at, nbytes, dims, dt, _stream_handle(dev))
+    _check(st)
+    return g
+
+
+def linear_attention_update(state, q, k, v, log_decay, scale=1.0, out=None):
+    """One decode step of the linear attention, advancing ``state`` ((batch,
+    heads, key, value) float32) in place; q, k: (batch, heads, key), v: (batch,
+    heads, value).  Returns o like v."""
+    L = _lib.lib()
+    dev = _on_gpu(q)
+    io = _io_dtype(q)
+    _need(q, "q")
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        _need(t, name, q.dtype, dev)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k must be (batch, heads, key) and v (batch, heads, value)")
+    _need_shape(k, "k", q.shape)
+    _need_shape(v, "v", (*q.shape[:-1], v.shape[-1]))
+    for name, t, shape in (("log_decay", log_decay, q.shape[1:2]), ("state", state, (*q.shape, v.shape[-1]))):
+        if t is None:
+            raise ValueError("%s is required" % name)
+        _need(t, name, torch.float32, dev)
+        _need_shape(t, name, shape)
+    o = _output(out, v)
+    with _on_device(dev):
+        st = L.mssm_linear_attention_update(
+            _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), float(scale), _ptr(o),
+            _lib.AttentionDims(q.shape[0], 1, q.shape[0], q.shape[1], q.shape[2], v.shape[2]),
+            _lib.DTypes(io, _lib.MSSM_F32), _stream_handle(dev))
+    _check(st)
+    return o
+
+
+def beam_select(logits, scores, count=None):
+    """A beam search's selection over beams and vocabulary on the GPU: the
+    ``count`` (None: as many as beams; at most 64) largest of scores[b, j] +
+    log_softmax(logits[b, j])[v] over j and v, equal ones by the lowest
+    j * vocab + v.
+
+    logits: (batch, beams, vocab) float32 or bfloat16, up to 32 beams; scores:
+    (batch, beams) float32, -inf for a beam that is not to be continued.
+    Returns ``(scores, tokens, beams)``, (batch, count) float32, int64, int64.
+    """
+    L = _lib.lib()
+    dev = _on_gpu(logits)
+    io = _io_dtype(logits)
+    _need(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be (batch, beams, vocab)")
+    if scores is None:
+        raise ValueError("scores is required")
+    _need(scores, "scores", torch.float32, dev)
+    _need_shape(scores, "scores", logits.shape[:2])
+    batch, beams, vocab = logits.shape
+    n = beams if count is None else int(count)
+    dims, dt = _lib.BeamDims(batch, beams, vocab, n), _lib.DTypes(io, _lib.MSSM_F32)
+    best = torch.empty((batch, max(n, 0)), dtype=torch.float32, device=dev)
+    tokens = torch.empty(best.shape, dtype=torch.int64, device=dev)
+    origins = torch.empty_like(tokens)
+    with _on_device(dev):
+        ws, at, nbytes = _workspace(L.mssm_beam_select_workspace(dims, dt), dev)
+        st = L.mssm_beam_select(_ptr(logits), _ptr(scores), _ptr(best), _ptr(tokens), _ptr(origins),
+                                at, nbytes, dims, dt, _stream_handle(dev))
+    _check(st)
+    return best, tokens, origins
+
+
+def state_reorder(states, origins):
+    """Reorders the states of beams in place, all at once: row (b, j) of every
+    state becomes its row (b, origins[b, j]).  Beams that keep their row cost
+    nothing; an origin outside [0, beams) leaves its beam as it is.
+
+    states: a tensor (batch, beams, ...) of any dtype, or a list of them;
+    origins: (batch, beams) int64, up to 32 beams.  Returns ``states``.
+    """
+    L = _lib.lib()
+    each = [states] if isinstance(states, torch.Tensor) else list(states)
+    dev = _on_gpu(origins)
+    _need(origins, "origins", torch.int64, dev)
+    if origins.dim() != 2:
+        raise ValueError("origins must be (batch, beams)")
+    n, rows = len(each), origins.numel()
+    at, sizes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
+    for i, t in enumerate(each):
+        if t is None:
+            raise ValueError("states[%d] is required" % i)
+        _need(t, "states[%d]" % i, None, dev)
+        if t.shape[:2] != origins.shape:
+            raise ValueError("states[%d] must be (batch, beams, ...)" % i)
+        at[i] = t.data_ptr()
+        sizes[i] = t.numel() * t.element_size() // rows if rows else 0
+    if rows == 0:
+        return states
+    with _on_device(dev):
+        st = L.mssm_state_reorder(at, sizes, n, _ptr(origins),
+                                  _lib.BeamDims(origins.shape[0], origins.shape[1], 1, 1),
+                                  _stream_handle(dev))
+    _check(st)
+    return states
 
 
 def probe_copy(src, dst):

@@ -235,6 +235,78 @@ size_t linear_cross_entropy_workspace(const LossArgs &a, bool bwd, bool aligned)
 hipError_t launch_linear_cross_entropy_fwd(const LossArgs &a, void *workspace, hipStream_t stream);
 hipError_t launch_linear_cross_entropy_bwd(const LossArgs &a, void *workspace, hipStream_t stream);
 
+// One norm of queries and keys with their rotation, already validated: q, dq,
+// q_in, dq_in (tokens, q_heads, dim), the same of k; positions (tokens);
+// weights and their gradients (dim).
+struct HeadNormArgs {
+    const void *q;
+    const void *k;
+    const int64_t *positions;
+    const float *q_weight;    // may be null -> 1
+    const float *k_weight;    // may be null -> 1
+    double base;
+    float eps;
+    void *q_out;              // forward: normed; backward: gradients of q, k
+    void *k_out;
+    const void *dq;           // backward only, from here on: of the outputs
+    const void *dk;
+    float *dq_weight;         // may be null
+    float *dk_weight;         // may be null
+    int64_t tokens, q_heads, k_heads, dim, rotary;
+    IoType io;
+};
+hipError_t launch_qk_norm_rotary_fwd(const HeadNormArgs &a, hipStream_t stream);
+hipError_t launch_qk_norm_rotary_bwd(const HeadNormArgs &a, void *workspace, hipStream_t stream);
+size_t qk_norm_rotary_bwd_workspace(const HeadNormArgs &a);
+
+// One linear attention, already validated: q, k, dq, dk (rows, heads, key), v, o
+// and their gradients (rows, heads, value) with seqs * seqlen rows or, packed,
+// `total`; states (seqs, heads, key, value).  The step has its state in h_last.
+struct AttentionArgs {
+    const void *q;
+    const void *k;
+    const void *v;
+    const float *log_decay;
+    float scale;
+    const float *h0;              // may be null -> 0
+    const int64_t *cu_seqlens;    // (seqs + 1) of packed sequences, else null
+    void *o;
+    float *h_last;                // may be null
+    const void *dout;             // backward only, from here on
+    const float *dh_last;         // may be null -> 0
+    void *dq;
+    void *dk;
+    void *dv;
+    float *dh0;                   // may be null
+    int64_t seqs, seqlen, total, heads, key, value;
+    IoType io;
+};
+bool linear_attention_supported(const AttentionArgs &a);
+size_t linear_attention_workspace(const AttentionArgs &a, bool bwd);
+hipError_t launch_linear_attention_fwd(const AttentionArgs &a, void *workspace, hipStream_t stream);
+hipError_t launch_linear_attention_bwd(const AttentionArgs &a, void *workspace, hipStream_t stream);
+hipError_t launch_linear_attention_update(const AttentionArgs &a, hipStream_t stream);
+
+// One selection of beams, already validated: logits (batch, beams, vocab),
+// scores (batch, beams), the outputs (batch, count).
+struct BeamArgs {
+    const void *logits;
+    const float *scores;
+    float *out_scores;
+    int64_t *out_tokens;
+    int64_t *out_beams;
+    int64_t batch, beams, vocab, count;
+    IoType io;
+};
+int64_t beam_select_pieces(int64_t vocab);   // workgroups of a beam
+size_t beam_select_workspace(const BeamArgs &a);
+hipError_t launch_beam_select(const BeamArgs &a, void *workspace, hipStream_t stream);
+// Workgroups of one entry of a state; the reordering in place of `count` states of
+// (batch, beams, row_bytes[i]) bytes.
+int64_t state_reorder_blocks(const void *state, int64_t row_bytes);
+hipError_t launch_state_reorder(void *const *states, const int64_t *row_bytes, int64_t count, const int64_t *origins,
+                                int64_t batch, int64_t beams, hipStream_t stream);
+
 hipError_t launch_ssd_recurrent(const SSDArgs &a, hipStream_t stream);
 bool ssd_recurrent_supported(const SSDArgs &a);
 

@@ -1,0 +1,748 @@
+// linear_attention.hip -- linear attention with a decay per head: chunked over
+// sequences, its backward, and one decode step on a cached state.
+//
+//   S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   g = e^log_decay
+//
+// A walk goes over a sequence C steps at a time with the state X in front of the
+// chunk in matrix-core accumulators:
+//   o_i = scale (g^(i+e) X^T q_i + sum_{j <= i} g^(i-j) (q_i . k_j) v_j)
+//   X  <- g^n X + sum_j g^(n-e-j) k_j v_j^T               (n steps in the chunk)
+// with e = 1 forward, where a state decays before it is read.  The gradients are
+// walks of the same kind with other roles.  With R_t = scale q_t do_t^T + g R_{t+1}
+// (dh_last added at the last step):
+//   dq_t = scale S_t do_t    roles (do, v, k), state S^T, forward in time
+//   dk_t = R_t v_t           roles (v, do, q), state R^T, against time, e = 0
+//   dv_t = R_t^T k_t         roles (k, q, do), state R, against time, e = 0
+//   dh0  = g R_0             the state behind the last walk
+//
+// Few sequences and heads are cut into segments of whole chunks: a first launch
+// walks the segments for their states alone, a second folds them,
+//   X_{s+1} = g^T X_s + local_s,
+// and the third walks every segment from the state in front of it.  Everything is
+// summed in an order that depends on the sizes alone.
+#include <algorithm>
+
+#include "device_math.h"
+#include "internal.h"
+
+namespace mssm {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// ---- fragments: eight contraction values of one row of an operand per lane; the
+// ---- lane halves hold different ones, sixteen in all for a product of 32 x 32
+
+struct F8 {
+    float f[8];
+};
+template <typename T> struct FragOf;
+template <> struct FragOf<uint16_t> { typedef bf16x8 type; };
+template <> struct FragOf<float> { typedef F8 type; };
+
+__device__ __forceinline__ void mma(f32x16 &c, bf16x8 a, bf16x8 b) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x16 &c, const F8 &a, const F8 &b) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.f[j], b.f[j], c, 0, 0, 0);
+}
+
+__device__ __forceinline__ void set(bf16x8 &f, int j, float v) { f[j] = static_cast<__bf16>(v); }
+__device__ __forceinline__ void set(F8 &f, int j, float v) { f.f[j] = v; }
+__device__ __forceinline__ float get(const bf16x8 &f, int j) { return static_cast<float>(f[j]); }
+__device__ __forceinline__ float get(const F8 &f, int j) { return f.f[j]; }
+
+// Accumulator element e of a lane is row acc_row(e) + 4 (lane / 32) of its 32 x 32
+// block, column lane % 32.  As an operand of the next product elements 8 s .. + 7
+// are the contraction rows 16 s + 4 h + {0..3, 8..11} of half h.
+__device__ __forceinline__ int acc_row(int e) { return 8 * (e / 4) + e % 4; }
+
+template <typename F>
+__device__ __forceinline__ F from_acc(const f32x16 &c, int s) {
+    F f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) set(f, j, c[8 * s + j]);
+    return f;
+}
+
+// Eight elements side by side.
+__device__ __forceinline__ bf16x8 load_row(const uint16_t *p) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(p));
+}
+__device__ __forceinline__ F8 load_row(const float *p) {
+    F8 f;
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    f.f[0] = a.x; f.f[1] = a.y; f.f[2] = a.z; f.f[3] = a.w;
+    f.f[4] = b.x; f.f[5] = b.y; f.f[6] = b.z; f.f[7] = b.w;
+    return f;
+}
+
+// Column of a 32-wide block that row m of a transposed operand stands for: chosen so
+// that accumulator elements 8 s .. + 7 of half h, whose rows are those above, are the
+// columns 16 s + 8 h + {0..7}, side by side.
+__device__ __forceinline__ int column_of(int m) {
+    return (m & 16) + 8 * (m / 4 % 2) + 4 * (m / 8 % 2) + m % 4;
+}
+
+// Transposed operand: row m = lane % 32 is column column_of(m) of the block whose
+// first element (line 0 of 16, column 0) p points to; the lane's contraction values
+// are lines 4 h + {0..3, 8..11}.  In bfloat16 by the transposing LDS read: the 16
+// lanes of a group fetch four lines of four chunks of four columns, lane i line
+// i / 4 of chunk i % 4, and lane i receives column i % 4 of chunk i / 4.
+__device__ __forceinline__ bf16x8 load_col(const uint16_t *__restrict__ p, int pitch, int lane) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 LdsRow;
+    const int i = lane % 16;
+    const uint16_t *at = p + (4 * (lane / 32) + i / 4) * pitch + (lane & 16) + column_of(4 * (i % 4));
+    const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)at));
+    const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)(at + 8 * pitch)));
+    return __builtin_bit_cast(bf16x8, u32x4{lo.x, lo.y, hi.x, hi.y});
+}
+__device__ __forceinline__ F8 load_col(const float *__restrict__ p, int pitch, int lane) {
+    F8 f;
+    const float *at = p + 4 * (lane / 32) * pitch + column_of(lane % 32);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.f[j] = at[(j / 4 * 8 + j % 4) * pitch];
+    return f;
+}
+
+// ---- one walk ------------------------------------------------------------------
+
+// Roles and sizes of one walk.  Rows are tokens; a head's A (keys) or B (values)
+// numbers lie side by side.  Element (a, b) of a state given by the caller is at
+// a * sa + b * sb of its (sequence, head); states in the workspace are (A, B).
+struct Walk {
+    const void *q, *k, *v;
+    void *o;
+    const float *first;      // may be null -> 0
+    float *last;             // may be null
+    float *segments;         // states of this walk's segments in the workspace
+    int64_t first_sa, first_sb;
+    int64_t last_sa, last_sb;
+    int64_t seg_sa, seg_sb;  // strides of the workspace's states
+    int A, B;
+    int slices;              // of B, over workgroups
+    int early;               // e above
+    int reverse;             // against time
+    float inner, scale;      // factors of the inputs' products and of the outputs
+};
+
+struct Walks {
+    Walk w[3];
+    int count;               // of w
+    const int64_t *cu;       // first rows of packed sequences, may be null
+    const float *log_decay;
+    int64_t seqs, seqlen, total, heads, segment;   // segment: its steps
+    int segments;            // of a sequence
+};
+
+// Rows of sequence b: packed offsets are held to [0, total] and to rise, so that no
+// value in them leads out of the tensors.
+__device__ __forceinline__ void sequence(const Walks &W, int64_t b, int64_t *start, int64_t *len) {
+    if (!W.cu) {
+        *start = b * W.seqlen;
+        *len = W.seqlen;
+        return;
+    }
+    const int64_t lo = min(max(W.cu[b], int64_t(0)), W.total), hi = min(max(W.cu[b + 1], lo), W.total);
+    *start = lo;
+    *len = hi - lo;
+}
+
+// log2 of a head's decay; no decay faster than 2^-300 a step, which is 0 in float32
+// even after one step, so that g^0 stays 1.
+__device__ __forceinline__ float decay_log2(const float *log_decay, int64_t h) {
+    const float d = log_decay[h] * kLog2e;
+    return d < -300.0f ? -300.0f : d;
+}
+
+constexpr int kChunkBytes = 128;   // C elements: 64 steps in bfloat16, 32 in float32
+
+// KP: A rounded up to whole products.  WAVES: 32 columns of B each.
+template <typename T, int KP_, int WAVES_>
+struct Shape {
+    typedef T Type;
+    typedef typename FragOf<T>::type Frag;
+    static constexpr int KP = KP_, WAVES = WAVES_, threads = 64 * WAVES, VP = 32 * WAVES;
+    static constexpr int C = kChunkBytes / sizeof(T), E = 16 / sizeof(T);   // E: elements of a vector
+    static constexpr int kp = KP + E, vp = VP + E;                          // pitches in LDS
+    static constexpr int lds = (2 * C * kp + C * vp) * sizeof(T), lds_state = (C * kp + C * vp) * sizeof(T);
+    static constexpr int nk = C * KP / E / threads, nv = C * VP / E / threads;   // vectors of a tile a thread moves
+};
+
+// Whether any of a vector's elements is infinite or NaN.
+__device__ __forceinline__ bool not_finite(u32x4 v, uint16_t) {
+    bool r = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r |= (v[j] & 0x7f80u) == 0x7f80u || (v[j] & 0x7f800000u) == 0x7f800000u;
+    return r;
+}
+__device__ __forceinline__ bool not_finite(u32x4 v, float) {
+    bool r = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r |= (v[j] & 0x7f800000u) == 0x7f800000u;
+    return r;
+}
+
+// A walk's products leave out later inputs by a factor 0, which a v that is infinite
+// or NaN would carry to earlier outputs of its chunk: a chunk that holds such a value
+// is walked a step at a time.
+
+// A tile of C rows on its way from memory: P columns of `width` that exist, the
+// others and rows from n on are 0.  Rows begin at any element.
+template <typename S, int P, int N>
+struct Stage {
+    typedef typename S::Type T;
+    u32x4 r[N];
+
+    __device__ __forceinline__ void load(const T *base, int64_t row0, int64_t step, int64_t ld, int n, int width) {
+        typedef u32x4 Any __attribute__((aligned(2)));   // rows begin at any element
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int id = i * S::threads + threadIdx.x, row = id / (P / S::E), c = id % (P / S::E) * S::E;
+            r[i] = u32x4{0, 0, 0, 0};
+            if (row < n && c < width) {
+                const T *p = base + (row0 + row * step) * ld + c;
+                if (c + S::E <= width) {
+                    r[i] = *reinterpret_cast<const Any *>(p);
+                } else {
+                    T t[S::E] = {};
+#pragma unroll
+                    for (int x = 0; x < S::E; ++x)
+                        if (c + x < width) t[x] = p[x];
+                    r[i] = *reinterpret_cast<const u32x4 *>(t);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ bool odd() const {
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) any |= not_finite(r[i], T());
+        return any;
+    }
+    __device__ __forceinline__ void store(T *to, int pitch) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int id = i * S::threads + threadIdx.x, row = id / (P / S::E), c = id % (P / S::E) * S::E;
+            *reinterpret_cast<u32x4 *>(to + row * pitch + c) = r[i];
+        }
+    }
+};
+
+// The lane's contraction values outside steps lo .. hi - 1, the first of them being
+// step `at`, set to 0.
+template <typename F>
+__device__ __forceinline__ void keep_steps(F &f, int at, int lo, int hi) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int step = at + j / 4 * 8 + j % 4;
+        if (step < lo || step >= hi) set(f, j, 0.0f);
+    }
+}
+
+// Eight outputs side by side, those from `width` on left out.
+__device__ __forceinline__ void store8(uint16_t *p, const float *f, int left) {
+    typedef u32x4 Any __attribute__((aligned(2)));
+    bf16x8 b;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = static_cast<__bf16>(f[j]);
+    const u32x4 v = __builtin_bit_cast(u32x4, b);
+    if (left >= 8) {
+        *reinterpret_cast<Any *>(p) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = static_cast<uint16_t>(v[j / 2] >> 16 * (j % 2));
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float *f, int left) {
+    typedef f32x4 Any __attribute__((aligned(4)));
+    if (left >= 8) {
+        reinterpret_cast<Any *>(p)[0] = f32x4{f[0], f[1], f[2], f[3]};
+        reinterpret_cast<Any *>(p)[1] = f32x4{f[4], f[5], f[6], f[7]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = f[j];
+    }
+}
+
+// OUT: the walk with its outputs; else for the segments' states alone.
+template <typename S, bool OUT>
+__global__ __launch_bounds__(S::threads) void attention_walk_kernel(const Walks W) {
+    typedef typename S::Type T;
+    typedef typename S::Frag Frag;
+    constexpr int C = S::C, KB = S::KP / 32, KS = S::KP / 16, CS = C / 16, CB = C / 32;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    __shared__ int64_t odd_chunk;      // the last chunk with an infinite or NaN v
+    T *const Ks = reinterpret_cast<T *>(smem), *const Vs = Ks + C * S::kp, *const Qs = Vs + C * S::vp;
+
+    // workgroups go to the eight XCDs in turn: each gets a run of consecutive
+    // positions, so that the walks over one head's rows share its L2
+    const int n_ids = gridDim.x, x = blockIdx.x % 8;
+    int64_t at = static_cast<int64_t>(x) * (n_ids / 8) + min(x, n_ids % 8) + blockIdx.x / 8;
+    int role = 0;
+    if (W.count > 1) {
+        role = static_cast<int>(at % W.count);
+        at /= W.count;
+    }
+    const Walk &w = W.w[role];
+    const int most = max(max(W.w[0].slices, W.w[1].slices), W.w[2].slices);
+    const int slice = static_cast<int>(at % most);
+    at /= most;
+    const int64_t h = at % W.heads;
+    at /= W.heads;
+    const int seg = static_cast<int>(at % W.segments);
+    const int64_t b = at / W.segments;
+    if (slice >= w.slices) return;
+    int64_t start, len;
+    sequence(W, b, &start, &len);
+    const int64_t t0 = seg * W.segment;
+    const bool tail = seg == W.segments - 1;       // walks to the end, however far
+    const int64_t t1 = tail ? len : min(len, t0 + W.segment);
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, half = lane / 32, col = lane % 32;
+    const int v0 = slice * S::VP, width = min(S::VP, w.B - v0);
+
+    if (OUT && W.cu && ((b == 0 && seg == 0) || (b == W.seqs - 1 && tail))) {
+        // rows in front of the first sequence and behind the last one
+        for (int side = 0; side < 2; ++side) {
+            if (side == 0 ? !(b == 0 && seg == 0) : !(b == W.seqs - 1 && tail)) continue;
+            const int64_t lo = side == 0 ? 0 : start + len, hi = side == 0 ? start : W.total;
+            T *o = static_cast<T *>(w.o) + h * w.B + v0;
+            for (int64_t id = threadIdx.x; id < (hi - lo) * width; id += S::threads)
+                o[(lo + id / width) * W.heads * w.B + id % width] = T(0);
+        }
+    }
+    if (OUT ? (t0 >= len && seg > 0) : (tail || t0 + W.segment >= len)) return;   // nothing, or nothing behind it
+
+    const float ld = decay_log2(W.log_decay, h);
+    const int e = w.early;
+    auto power = [&](int n) { return fast_exp2(ld * static_cast<float>(n)); };
+    const int my_v = v0 + 32 * wave + column_of(col);    // column of this lane's state
+    const int64_t bh = b * W.heads + h;
+
+    // element j of block kb of the state: row 32 kb + 16 (j / 8) + 8 half + j % 8
+    f32x16 X[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) X[kb][j] = 0.0f;
+    if (OUT && (seg > 0 || w.first)) {
+        const int64_t sa = seg > 0 ? w.seg_sa : w.first_sa, sb = seg > 0 ? w.seg_sb : w.first_sb;
+        const int64_t states = static_cast<int64_t>(w.A) * w.B;
+        const float *from = seg > 0 ? w.segments + ((b * (W.segments - 1) + seg - 1) * W.heads + h) * states
+                                    : w.first + bh * states;
+        if (my_v < w.B) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int a = 32 * kb + 16 * (j / 8) + 8 * half + j % 8;
+                    if (a < w.A) X[kb][j] = from[a * sa + my_v * sb];
+                }
+        }
+    }
+
+    // decays inside a chunk: of outputs (this lane's is col of every block of 32) from
+    // the inputs of their own block and of the one before, and of the state
+    float inside[16], across[16], weight[8];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const int gap = col - acc_row(j) - 4 * half;
+        inside[j] = w.inner * power(max(gap, 0));
+        across[j] = CB > 1 ? w.inner * power(32 + gap) : 0.0f;
+    }
+    const float front = power(col + e), whole = power(C), block = power(32), line = power(16);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) weight[j] = w.inner * power(16 - e - 4 * half - (j / 4 * 8 + j % 4));   // of the last 16 steps
+
+    const T *q = static_cast<const T *>(w.q) + h * w.A, *k = static_cast<const T *>(w.k) + h * w.A,
+            *v = static_cast<const T *>(w.v) + h * w.B + v0;
+    const int64_t lda = W.heads * w.A, ldb = W.heads * w.B, step = w.reverse ? -1 : 1;
+    const int64_t row_first = w.reverse ? start + len - 1 : start;
+    Stage<S, S::KP, S::nk> kin, qin;
+    Stage<S, S::VP, S::nv> vin;
+    auto fetch = [&](int64_t t) {
+        const int n = static_cast<int>(min(int64_t(C), t1 - t));
+        const int64_t row = row_first + t * step;
+        kin.load(k, row, step, lda, n, w.A);
+        vin.load(v, row, step, ldb, n, width);
+        if (OUT) qin.load(q, row, step, lda, n, w.A);
+    };
+    if (threadIdx.x == 0) odd_chunk = -1;
+    if (t0 < t1) fetch(t0);
+    for (int64_t t = t0; t < t1; t += C) {
+        const int n = static_cast<int>(min(int64_t(C), t1 - t));
+        __syncthreads();
+        kin.store(Ks, S::kp);
+        vin.store(Vs, S::vp);
+        if (OUT) qin.store(Qs, S::kp);
+        if (OUT && vin.odd()) odd_chunk = t;      // written by any thread that finds one, alike
+        __syncthreads();
+        if (t + C < t1) fetch(t + C);
+
+        // all n steps at once, or each by itself
+        const bool single = OUT && odd_chunk == t;
+        for (int lo = 0, hi = single ? 1 : n; lo < n; lo = hi, ++hi) {
+            const bool part = hi - lo < C;
+            Frag vf[CS];
+#pragma unroll
+            for (int s = 0; s < CS; ++s) {
+                vf[s] = load_col(Vs + 16 * s * S::vp + 32 * wave, S::vp, lane);
+                if (single) keep_steps(vf[s], 16 * s + 4 * half, lo, hi);
+            }
+            if (OUT) {
+#pragma unroll
+                for (int ib = 0; ib < CB; ++ib) {
+                    Frag qf[KS];
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) qf[s] = load_row(Qs + (32 * ib + col) * S::kp + 16 * s + 8 * half);
+                    f32x16 O;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) O[j] = 0.0f;
+                    // The state enters as an operand of the I/O dtype: in bfloat16 half a
+                    // step, 2^-8 of each of its values, like the rounding of the output.
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) mma(O, from_acc<Frag>(X[s / 2], s % 2), qf[s]);
+                    const float f = single ? power(max(32 * ib + col + e - lo, 0)) : ib == 0 ? front : front * block;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) O[j] *= f;
+#pragma unroll
+                    for (int jb = 0; jb <= ib; ++jb) {
+                        f32x16 G;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) G[j] = 0.0f;
+#pragma unroll
+                        for (int s = 0; s < KS; ++s)
+                            mma(G, load_row(Ks + (32 * jb + col) * S::kp + 16 * s + 8 * half), qf[s]);
+                        // later inputs leave nothing, whatever their products hold
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            G[j] = jb < ib ? G[j] * across[j] : acc_row(j) + 4 * half <= col ? G[j] * inside[j] : 0.0f;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) mma(O, vf[2 * jb + s], from_acc<Frag>(G, s));
+                    }
+                    const int row = 32 * ib + col;
+                    if (row >= lo && row < hi) {
+                        T *o = static_cast<T *>(w.o) + (row_first + (t + row) * step) * ldb + h * w.B + v0;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            float out[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) out[j] = O[8 * s + j] * w.scale;
+                            const int c = 32 * wave + 16 * s + 8 * half;
+                            store8(o + c, out, width - c);
+                        }
+                    }
+                }
+            }
+            // The state: k_j exact, its partner g^(n-e-j) v_j in bfloat16 as the sum of two
+            // roundings, which hold it to 2^-16.
+            const float f = part ? power(hi - lo) : whole;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) X[kb][j] *= f;
+            float g = 1.0f;
+#pragma unroll
+            for (int s = CS - 1; s >= 0; --s) {
+                Frag up, rest;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float u = weight[j] * g;
+                    if (part) u = w.inner * power(max(hi - e - (16 * s + 4 * half + j / 4 * 8 + j % 4), 0));
+                    u *= get(vf[s], j);
+                    set(up, j, u);
+                    set(rest, j, u - get(up, j));
+                }
+                g *= line;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    Frag a = load_col(Ks + 16 * s * S::kp + 32 * kb, S::kp, lane);
+                    if (single) keep_steps(a, 16 * s + 4 * half, lo, hi);
+                    mma(X[kb], a, up);
+                    if (sizeof(T) == 2) mma(X[kb], a, rest);
+                }
+            }
+        }
+    }
+
+    if (OUT && !w.last) return;
+    if (OUT && !(t1 == len && (t1 > t0 || seg == 0))) return;
+    const int64_t states = static_cast<int64_t>(w.A) * w.B;
+    float *to = OUT ? w.last + bh * states : w.segments + ((b * (W.segments - 1) + seg) * W.heads + h) * states;
+    const int64_t sa = OUT ? w.last_sa : w.seg_sa, sb = OUT ? w.last_sb : w.seg_sb;
+    if (my_v < w.B) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int a = 32 * kb + 16 * (j / 8) + 8 * half + j % 8;
+                if (a < w.A) to[a * sa + my_v * sb] = X[kb][j];
+            }
+    }
+}
+
+// X_{s+1} = g^T X_s + local_s in place: slot s receives the state in front of segment
+// s + 1.
+__global__ __launch_bounds__(256) void attention_fold_kernel(const Walks W) {
+    const Walk &w = W.w[blockIdx.z];
+    const int64_t bh = blockIdx.y, b = bh / W.heads, h = bh % W.heads;
+    const int64_t states = static_cast<int64_t>(w.A) * w.B;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (id >= states) return;
+    int64_t start, len;
+    sequence(W, b, &start, &len);
+    // segments that end before the sequence does
+    const int64_t full = len <= 0 ? 0 : min(int64_t(W.segments - 1), (len - 1) / W.segment);
+    const float g = fast_exp2(decay_log2(W.log_decay, h) * static_cast<float>(W.segment));
+    const int64_t a = id / w.B, c = id % w.B;
+    float x = w.first ? w.first[bh * states + a * w.first_sa + c * w.first_sb] : 0.0f;
+    float *p = w.segments + (b * (W.segments - 1) * W.heads + h) * states + a * w.seg_sa + c * w.seg_sb;
+    for (int64_t s = 0; s < full; ++s, p += W.heads * states) {
+        x = fmaf(g, x, *p);
+        *p = x;
+    }
+}
+
+// ---- launches ------------------------------------------------------------------
+
+constexpr int kTarget = 512;   // workgroups to aim at
+
+int waves_of(int64_t B) { return B <= 64 ? 2 : 4; }
+int slices_of(int64_t B) { return static_cast<int>((B + 32 * waves_of(B) - 1) / (32 * waves_of(B))); }
+
+// Segments of a sequence and their steps.
+void cut(const AttentionArgs &a, bool bwd, int *segments, int64_t *steps) {
+    const int64_t chunk = a.io == IO_F32 ? 32 : 64, least = 4 * chunk;
+    const int64_t walks = a.seqs * a.heads * slices_of(a.value);
+    const int64_t want = std::max<int64_t>(1, (kTarget + walks - 1) / std::max<int64_t>(1, walks));
+    const int64_t n = std::max<int64_t>(1, std::min(want, a.seqlen / least));
+    *steps = ((a.seqlen + n - 1) / n + chunk - 1) / chunk * chunk;
+    *segments = *steps > 0 ? static_cast<int>((a.seqlen + *steps - 1) / *steps) : 1;
+    if (*segments < 1) *segments = 1;
+    if (*steps < chunk) *steps = chunk;
+}
+
+template <typename S, bool OUT>
+hipError_t launch_walks(const Walks &W, hipStream_t stream) {
+    int most = 0;
+    for (int i = 0; i < W.count; ++i) most = std::max(most, W.w[i].slices);
+    const int64_t n = W.seqs * W.segments * W.heads * most * W.count;
+    constexpr int lds = OUT ? S::lds : S::lds_state;
+    if (lds > 65536)
+        if (const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attention_walk_kernel<S, OUT>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds))
+            return e;
+    hipLaunchKernelGGL((attention_walk_kernel<S, OUT>), dim3(static_cast<uint32_t>(n)), dim3(S::threads), lds, stream, W);
+    return hipGetLastError();
+}
+
+template <typename T, bool OUT>
+hipError_t launch_group(const Walks &W, int64_t A, int waves, hipStream_t stream) {
+    if (waves == 2) {
+        if (A <= 64) return launch_walks<Shape<T, 64, 2>, OUT>(W, stream);
+        if (A <= 128) return launch_walks<Shape<T, 128, 2>, OUT>(W, stream);
+        return launch_walks<Shape<T, 256, 2>, OUT>(W, stream);
+    }
+    if (A <= 64) return launch_walks<Shape<T, 64, 4>, OUT>(W, stream);
+    if (A <= 128) return launch_walks<Shape<T, 128, 4>, OUT>(W, stream);
+    return launch_walks<Shape<T, 256, 4>, OUT>(W, stream);
+}
+
+// Walks of one shape share a launch.
+template <bool OUT>
+hipError_t launch_all(const Walks &W, bool f32, hipStream_t stream) {
+    auto shape = [](const Walk &w) { return (w.A <= 64 ? 0 : w.A <= 128 ? 1 : 2) * 2 + (waves_of(w.B) == 4); };
+    bool done[3] = {false, false, false};
+    for (int i = 0; i < W.count; ++i) {
+        if (done[i]) continue;
+        Walks G = W;
+        G.count = 0;
+        for (int j = i; j < W.count; ++j)
+            if (!done[j] && shape(W.w[j]) == shape(W.w[i])) {
+                G.w[G.count++] = W.w[j];
+                done[j] = true;
+            }
+        for (int j = G.count; j < 3; ++j) G.w[j] = G.w[0];
+        const int waves = waves_of(G.w[0].B);
+        const hipError_t e = f32 ? launch_group<float, OUT>(G, G.w[0].A, waves, stream)
+                                 : launch_group<uint16_t, OUT>(G, G.w[0].A, waves, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+Walks common(const AttentionArgs &a, bool bwd) {
+    Walks W{};
+    W.cu = a.cu_seqlens;
+    W.log_decay = a.log_decay;
+    W.seqs = a.seqs; W.seqlen = a.seqlen; W.total = a.total; W.heads = a.heads;
+    cut(a, bwd, &W.segments, &W.segment);
+    return W;
+}
+
+hipError_t fold(const Walks &W, hipStream_t stream) {
+    int64_t states = 0;
+    for (int i = 0; i < W.count; ++i) states = std::max(states, static_cast<int64_t>(W.w[i].A) * W.w[i].B);
+    hipLaunchKernelGGL(attention_fold_kernel,
+                       dim3(static_cast<uint32_t>((states + 255) / 256), static_cast<uint32_t>(W.seqs * W.heads), W.count),
+                       dim3(256), 0, stream, W);
+    return hipGetLastError();
+}
+
+// ---- one step ------------------------------------------------------------------
+
+// A workgroup holds LANES x VEC columns of one state; groups of LANES lanes take the
+// rows in turn.
+template <typename T, int VEC, int LANES>
+__global__ __launch_bounds__(256) void attention_step_kernel(float *__restrict__ state, const T *__restrict__ q,
+                                                             const T *__restrict__ k, const T *__restrict__ v,
+                                                             const float *__restrict__ log_decay, float scale,
+                                                             T *__restrict__ o, int heads, int K, int V, int slices) {
+    constexpr int GROUPS = 256 / LANES, COLS = LANES * VEC;
+    __shared__ float sum[GROUPS][COLS];
+    const int64_t bh = blockIdx.x / slices;
+    const int slice = blockIdx.x % slices, h = static_cast<int>(bh % heads);
+    const int group = threadIdx.x / LANES, c = slice * COLS + threadIdx.x % LANES * VEC;
+    const float g = fast_exp2(decay_log2(log_decay, h));
+    state += bh * K * V;
+    q += bh * K;
+    k += bh * K;
+    v += bh * V;
+    o += bh * V;
+    float acc[VEC] = {};
+    if (c < V) {
+        float vv[VEC];
+#pragma unroll
+        for (int x = 0; x < VEC; ++x) vv[x] = Io<T>::load(v, c + x);
+#pragma unroll 8
+        for (int a = group; a < K; a += GROUPS) {
+            float *p = state + static_cast<int64_t>(a) * V + c;
+            const float kk = Io<T>::load(k, a), qq = Io<T>::load(q, a);
+            if constexpr (VEC == 4) {
+                float4 s = *reinterpret_cast<const float4 *>(p);
+                s.x = fmaf(g, s.x, kk * vv[0]);
+                s.y = fmaf(g, s.y, kk * vv[1]);
+                s.z = fmaf(g, s.z, kk * vv[2]);
+                s.w = fmaf(g, s.w, kk * vv[3]);
+                *reinterpret_cast<float4 *>(p) = s;
+                acc[0] = fmaf(qq, s.x, acc[0]);
+                acc[1] = fmaf(qq, s.y, acc[1]);
+                acc[2] = fmaf(qq, s.z, acc[2]);
+                acc[3] = fmaf(qq, s.w, acc[3]);
+            } else {
+                const float s = fmaf(g, *p, kk * vv[0]);
+                *p = s;
+                acc[0] = fmaf(qq, s, acc[0]);
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < VEC; ++x) sum[group][threadIdx.x % LANES * VEC + x] = acc[x];
+    __syncthreads();
+    for (int x = threadIdx.x; x < COLS; x += 256) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) s += sum[i][x];
+        if (slice * COLS + x < V) Io<T>::store(o, slice * COLS + x, s * scale);
+    }
+}
+
+template <typename T>
+hipError_t step(const AttentionArgs &a, hipStream_t stream) {
+    const int64_t bh = a.seqs * a.heads;
+    auto go = [&](auto kernel, int cols) {
+        const int64_t slices = (a.value + cols - 1) / cols;
+        hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(bh * slices)), dim3(256), 0, stream, a.h_last,
+                           static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
+                           a.log_decay, a.scale, static_cast<T *>(a.o), static_cast<int>(a.heads),
+                           static_cast<int>(a.key), static_cast<int>(a.value), static_cast<int>(slices));
+    };
+    const bool vec = a.value % 4 == 0 && reinterpret_cast<uintptr_t>(a.h_last) % 16 == 0;
+    if (!vec) go(attention_step_kernel<T, 1, 32>, 32);
+    else if (bh * ((a.value + 127) / 128) >= 256) go(attention_step_kernel<T, 4, 32>, 128);
+    else go(attention_step_kernel<T, 4, 8>, 32);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+bool linear_attention_supported(const AttentionArgs &a) {
+    if (a.key > MSSM_MAX_HEAD_DIM || a.value > MSSM_MAX_HEAD_DIM) return false;
+    // grids stay below 2^31 workgroups of up to three walks, rows below 2^31
+    if (a.seqs * a.heads >= (int64_t(1) << 16) * 16 || a.total >= (int64_t(1) << 31)) return false;
+    return true;
+}
+
+size_t linear_attention_workspace(const AttentionArgs &a, bool bwd) {
+    const Walks W = common(a, bwd);
+    return static_cast<size_t>(W.segments - 1) * a.seqs * a.heads * a.key * a.value * sizeof(float) * (bwd ? 2 : 1);
+}
+
+hipError_t launch_linear_attention_fwd(const AttentionArgs &a, void *workspace, hipStream_t stream) {
+    Walks W = common(a, false);
+    const size_t bytes = linear_attention_workspace(a, false);
+    void *ws = workspace;
+    if (bytes && !ws)
+        if (const hipError_t e = scratch_alloc(&ws, bytes, stream)) return e;
+    const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
+    W.count = 1;
+    W.w[0] = Walk{a.q, a.k, a.v, a.o, a.h0, a.h_last, static_cast<float *>(ws), V, 1, V, 1, V, 1, K, V,
+                  slices_of(V), 1, 0, 1.0f, a.scale};
+    hipError_t e = hipSuccess;
+    if (W.segments > 1) {
+        e = launch_all<false>(W, a.io == IO_F32, stream);
+        if (e == hipSuccess) e = fold(W, stream);
+    }
+    if (e == hipSuccess) e = launch_all<true>(W, a.io == IO_F32, stream);
+    if (bytes && !workspace) {
+        const hipError_t f = scratch_free(ws, stream);
+        if (e == hipSuccess) e = f;
+    }
+    return e;
+}
+
+hipError_t launch_linear_attention_bwd(const AttentionArgs &a, void *workspace, hipStream_t stream) {
+    Walks W = common(a, true);
+    const size_t bytes = linear_attention_workspace(a, true);
+    void *ws = workspace;
+    if (bytes && !ws)
+        if (const hipError_t e = scratch_alloc(&ws, bytes, stream)) return e;
+    const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
+    float *S = static_cast<float *>(ws), *R = S + bytes / 2 / sizeof(float);
+    // S^T in (V, K) as the first walk forms it; R in (K, V) as the third does
+    const Walk dq{a.dout, a.v, a.k, a.dq, a.h0, nullptr, S, 1, V, 0, 0, K, 1, V, K, slices_of(K), 1, 0, 1.0f, a.scale};
+    const Walk dk{a.v, a.dout, a.q, a.dk, a.dh_last, nullptr, R, 1, V, 0, 0, 1, V, V, K, slices_of(K), 0, 1, a.scale, 1.0f};
+    const Walk dv{a.k, a.q, a.dout, a.dv, a.dh_last, a.dh0, R, V, 1, V, 1, V, 1, K, V, slices_of(V), 0, 1, a.scale, 1.0f};
+    hipError_t e = hipSuccess;
+    if (W.segments > 1) {
+        W.count = 2;
+        W.w[0] = dq;
+        W.w[1] = dv;
+        W.w[2] = dq;
+        e = launch_all<false>(W, a.io == IO_F32, stream);
+        if (e == hipSuccess) e = fold(W, stream);
+    }
+    W.count = 3;
+    W.w[0] = dq;
+    W.w[1] = dk;
+    W.w[2] = dv;
+    if (e == hipSuccess) e = launch_all<true>(W, a.io == IO_F32, stream);
+    if (bytes && !workspace) {
+        const hipError_t f = scratch_free(ws, stream);
+        if (e == hipSuccess) e = f;
+    }
+    return e;
+}
+
+hipError_t launch_linear_attention_update(const AttentionArgs &a, hipStream_t stream) {
+    return a.io == IO_F32 ? step<float>(a, stream) : step<uint16_t>(a, stream);
+}
+
+}  // namespace mssm

@@ -449,6 +449,102 @@ mssm_status check_loss(mssm_loss_dims d, mssm_dtypes dtypes, LossSizes *z) {
     return MSSM_OK;
 }
 
+// Sizes in bytes of a norm with rotation, after the checks both passes share.
+struct HeadNormSizes {
+    int64_t q_bytes, k_bytes;
+};
+
+mssm_status check_head_norm(mssm_head_norm_dims d, double base, float eps, mssm_dtypes dtypes, HeadNormSizes *z) {
+    if (mssm_status s = check_dtypes(dtypes)) return s;
+    if (d.tokens < 0 || d.q_heads < 0 || d.k_heads < 0)
+        return fail(MSSM_ERR_INVALID_ARG, "negative size (tokens %lld, heads %lld and %lld)", (long long)d.tokens,
+                    (long long)d.q_heads, (long long)d.k_heads);
+    if (d.dim < 1) return fail(MSSM_ERR_INVALID_ARG, "dim must be >= 1, got %lld", (long long)d.dim);
+    if (d.dim > MSSM_MAX_HEAD_DIM)
+        return fail(MSSM_ERR_UNSUPPORTED, "dim %lld exceeds MSSM_MAX_HEAD_DIM (%d)", (long long)d.dim, MSSM_MAX_HEAD_DIM);
+    if (d.rotary < 0 || d.rotary > d.dim || d.rotary % 2)
+        return fail(MSSM_ERR_INVALID_ARG, "rotary must be even and in [0, dim], got %lld", (long long)d.rotary);
+    if (!(base > 0.0) || !std::isfinite(base))
+        return fail(MSSM_ERR_INVALID_ARG, "base must be finite and > 0, got %g", base);
+    if (!(eps >= 0.0f) || !std::isfinite(eps))
+        return fail(MSSM_ERR_INVALID_ARG, "eps must be finite and >= 0, got %g", (double)eps);
+    int64_t q, k;
+    const int64_t lim = int64_t(1) << 31;
+    if (!mul_ok(d.tokens, d.q_heads, &q) || !mul_ok(d.tokens, d.k_heads, &k) || q >= lim || k >= lim || d.tokens >= lim ||
+        d.q_heads >= (lim >> 8) || d.k_heads >= (lim >> 8))
+        return fail(MSSM_ERR_UNSUPPORTED, "tokens %lld times heads %lld or %lld is 2^31 or more, or heads 2^23",
+                    (long long)d.tokens, (long long)d.q_heads, (long long)d.k_heads);
+    const int64_t esz = dtypes.io == MSSM_F32 ? 4 : 2;
+    *z = HeadNormSizes{q * d.dim * esz, k * d.dim * esz};
+    return MSSM_OK;
+}
+
+// Sizes of a linear attention: bytes but for `states`, the states' elements.
+struct AttentionSizes {
+    int64_t key_bytes, value_bytes, states, state_bytes;
+};
+
+mssm_status check_attention(mssm_attention_dims d, float scale, bool packed, mssm_dtypes dtypes, AttentionSizes *z) {
+    if (mssm_status s = check_dtypes(dtypes)) return s;
+    if (d.seqs < 0 || d.seqlen < 0 || d.total < 0 || d.heads < 0)
+        return fail(MSSM_ERR_INVALID_ARG, "negative size (seqs %lld, seqlen %lld, total %lld, heads %lld)",
+                    (long long)d.seqs, (long long)d.seqlen, (long long)d.total, (long long)d.heads);
+    if (d.key < 1 || d.value < 1)
+        return fail(MSSM_ERR_INVALID_ARG, "key and value must be >= 1, got %lld and %lld", (long long)d.key,
+                    (long long)d.value);
+    if (!std::isfinite(scale)) return fail(MSSM_ERR_INVALID_ARG, "scale must be finite, got %g", (double)scale);
+    if (d.key > MSSM_MAX_HEAD_DIM || d.value > MSSM_MAX_HEAD_DIM)
+        return fail(MSSM_ERR_UNSUPPORTED, "key %lld or value %lld exceeds MSSM_MAX_HEAD_DIM (%d)", (long long)d.key,
+                    (long long)d.value, MSSM_MAX_HEAD_DIM);
+    int64_t rows, bh, n;
+    const int64_t lim = int64_t(1) << 31;
+    if (!mul_ok(d.seqs, d.seqlen, &rows) || !mul_ok(d.seqs, d.heads, &bh) || !mul_ok(d.total, d.heads, &n) ||
+        n >= (int64_t(1) << 48))
+        return fail(MSSM_ERR_INVALID_ARG, "sizes overflow");
+    if (!packed && rows != d.total)
+        return fail(MSSM_ERR_INVALID_ARG, "total %lld is not seqs * seqlen (%lld)", (long long)d.total, (long long)rows);
+    if (d.seqs >= (lim >> 11) || bh >= (lim >> 11) || d.total >= lim || d.seqlen >= lim)
+        return fail(MSSM_ERR_UNSUPPORTED, "seqs * heads %lld reaches 2^20, or total %lld or seqlen %lld 2^31",
+                    (long long)bh, (long long)d.total, (long long)d.seqlen);
+    const int64_t esz = dtypes.io == MSSM_F32 ? 4 : 2, states = bh * d.key * d.value;
+    *z = AttentionSizes{n * d.key * esz, n * d.value * esz, states, states * 4};
+    return MSSM_OK;
+}
+
+mssm::AttentionArgs attention_args(mssm_attention_dims d, mssm_dtypes dtypes) {
+    mssm::AttentionArgs a{};
+    a.seqs = d.seqs; a.seqlen = d.seqlen; a.total = d.total; a.heads = d.heads; a.key = d.key; a.value = d.value;
+    a.io = io_type(dtypes);
+    return a;
+}
+
+mssm_status check_beams(mssm_beam_dims d) {
+    if (d.batch < 0) return fail(MSSM_ERR_INVALID_ARG, "negative size (batch %lld)", (long long)d.batch);
+    if (d.beams < 1) return fail(MSSM_ERR_INVALID_ARG, "beams must be >= 1, got %lld", (long long)d.beams);
+    if (d.beams > MSSM_MAX_BEAMS)
+        return fail(MSSM_ERR_UNSUPPORTED, "beams %lld exceed MSSM_MAX_BEAMS (%d)", (long long)d.beams, MSSM_MAX_BEAMS);
+    if (d.batch >= (int64_t(1) << 24))
+        return fail(MSSM_ERR_UNSUPPORTED, "batch %lld reaches 2^24", (long long)d.batch);
+    return MSSM_OK;
+}
+
+mssm_status check_selection(mssm_beam_dims d, mssm_dtypes dtypes) {
+    if (mssm_status s = check_dtypes(dtypes)) return s;
+    if (mssm_status s = check_beams(d)) return s;
+    if (d.vocab < 1 || d.count < 1)
+        return fail(MSSM_ERR_INVALID_ARG, "vocab and count must be >= 1, got %lld and %lld", (long long)d.vocab,
+                    (long long)d.count);
+    if (d.vocab >= (int64_t(1) << 30) || d.count > MSSM_MAX_BEAM_COUNT)
+        return fail(MSSM_ERR_UNSUPPORTED, "vocab %lld reaches 2^30, or count %lld exceeds MSSM_MAX_BEAM_COUNT (%d)",
+                    (long long)d.vocab, (long long)d.count, MSSM_MAX_BEAM_COUNT);
+    if (d.count > d.beams * d.vocab)
+        return fail(MSSM_ERR_INVALID_ARG, "count %lld exceeds beams * vocab", (long long)d.count);
+    if (d.batch * d.beams * mssm::beam_select_pieces(d.vocab) >= (int64_t(1) << 24))
+        return fail(MSSM_ERR_UNSUPPORTED, "batch %lld times beams %lld of %lld words is too large", (long long)d.batch,
+                    (long long)d.beams, (long long)d.vocab);
+    return MSSM_OK;
+}
+
 }  // namespace
 
 namespace mssm {
@@ -987,6 +1083,278 @@ int64_t mssm_linear_cross_entropy_workspace(mssm_loss_dims dims, mssm_dtypes dty
     mssm::LossArgs a{};
     a.tokens = dims.tokens; a.dim = dims.dim; a.vocab = dims.vocab; a.io = io_type(dtypes);
     return static_cast<int64_t>(mssm::linear_cross_entropy_workspace(a, backward != 0, aligned != 0));
+}
+
+mssm_status mssm_qk_norm_rotary_fwd(const void *q, const void *k, const int64_t *positions,
+                                    const float *q_weight, const float *k_weight, double base,
+                                    float eps, void *q_out, void *k_out, mssm_head_norm_dims dims,
+                                    mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    HeadNormSizes z;
+    if (mssm_status s = check_head_norm(dims, base, eps, dtypes, &z)) return s;
+    g_last_variant = MSSM_VARIANT_AUTO;
+    if (z.q_bytes == 0 && z.k_bytes == 0) return MSSM_OK;
+    if (z.q_bytes && !q) return fail(MSSM_ERR_INVALID_ARG, "q is null");
+    if (z.k_bytes && !k) return fail(MSSM_ERR_INVALID_ARG, "k is null");
+    if (dims.rotary && !positions) return fail(MSSM_ERR_INVALID_ARG, "positions is null");
+    if (z.q_bytes && !q_out) return fail(MSSM_ERR_INVALID_ARG, "q_out is null");
+    if (z.k_bytes && !k_out) return fail(MSSM_ERR_INVALID_ARG, "k_out is null");
+    const Range ins[] = {range("q", q, z.q_bytes), range("k", k, z.k_bytes),
+                         range("positions", positions, dims.tokens * 8),
+                         range("q_weight", q_weight, dims.dim * 4), range("k_weight", k_weight, dims.dim * 4)};
+    const Range outs[] = {range("q_out", q_out, z.q_bytes), range("k_out", k_out, z.k_bytes)};
+    if (mssm_status c = check_overlaps(ins, 5, outs, 2, nullptr, nullptr)) return c;
+    const mssm::HeadNormArgs a{q, k, positions, q_weight, k_weight, base, eps, q_out, k_out, nullptr, nullptr,
+                               nullptr, nullptr, dims.tokens, dims.q_heads, dims.k_heads, dims.dim, dims.rotary,
+                               io_type(dtypes)};
+    const hipError_t e = mssm::launch_qk_norm_rotary_fwd(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "norm-and-rotation launch");
+    return MSSM_OK;
+}
+
+mssm_status mssm_qk_norm_rotary_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                                    const int64_t *positions, const float *q_weight,
+                                    const float *k_weight, double base, float eps, void *dq, void *dk,
+                                    float *dq_weight, float *dk_weight, void *workspace,
+                                    int64_t workspace_bytes, mssm_head_norm_dims dims,
+                                    mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    HeadNormSizes z;
+    if (mssm_status s = check_head_norm(dims, base, eps, dtypes, &z)) return s;
+    g_last_variant = MSSM_VARIANT_AUTO;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const mssm::HeadNormArgs a{q, k, positions, q_weight, k_weight, base, eps, dq, dk, dq_out, dk_out,
+                               dq_weight, dk_weight, dims.tokens, dims.q_heads, dims.k_heads, dims.dim, dims.rotary,
+                               io_type(dtypes)};
+    Range ws;
+    if (mssm_status s = check_workspace(workspace, workspace_bytes, mssm::qk_norm_rotary_bwd_workspace(a), &ws)) return s;
+    const Range outs[] = {range("dq", dq, z.q_bytes), range("dk", dk, z.k_bytes),
+                          range("dq_weight", dq_weight, dims.dim * 4), range("dk_weight", dk_weight, dims.dim * 4), ws};
+    if (z.q_bytes == 0 && z.k_bytes == 0) {
+        if (overlaps(outs[2], outs[3])) return fail(MSSM_ERR_INVALID_ARG, "dq_weight overlaps dk_weight");
+        hipError_t e = hipSuccess;
+        if (dq_weight) e = zero_fill(dq_weight, dims.dim, st);
+        if (e == hipSuccess && dk_weight) e = zero_fill(dk_weight, dims.dim, st);
+        if (e != hipSuccess) return hip_fail(e, "zero-fill of the gradients");
+        return MSSM_OK;
+    }
+    if (z.q_bytes && !dq_out) return fail(MSSM_ERR_INVALID_ARG, "dq_out is null");
+    if (z.k_bytes && !dk_out) return fail(MSSM_ERR_INVALID_ARG, "dk_out is null");
+    if (z.q_bytes && !q) return fail(MSSM_ERR_INVALID_ARG, "q is null");
+    if (z.k_bytes && !k) return fail(MSSM_ERR_INVALID_ARG, "k is null");
+    if (dims.rotary && !positions) return fail(MSSM_ERR_INVALID_ARG, "positions is null");
+    if (z.q_bytes && !dq) return fail(MSSM_ERR_INVALID_ARG, "dq is null");
+    if (z.k_bytes && !dk) return fail(MSSM_ERR_INVALID_ARG, "dk is null");
+    const Range ins[] = {range("dq_out", dq_out, z.q_bytes), range("dk_out", dk_out, z.k_bytes),
+                         range("q", q, z.q_bytes), range("k", k, z.k_bytes),
+                         range("positions", positions, dims.tokens * 8),
+                         range("q_weight", q_weight, dims.dim * 4), range("k_weight", k_weight, dims.dim * 4)};
+    if (mssm_status c = check_overlaps(ins, 7, outs, 5, nullptr, nullptr)) return c;
+    const hipError_t e = mssm::launch_qk_norm_rotary_bwd(a, workspace, st);
+    if (e != hipSuccess) return hip_fail(e, "norm-and-rotation backward launch");
+    return MSSM_OK;
+}
+
+int64_t mssm_qk_norm_rotary_bwd_workspace(mssm_head_norm_dims dims, mssm_dtypes dtypes) {
+    g_last_error.clear();
+    HeadNormSizes z;
+    if (check_head_norm(dims, 1.0, 0.0f, dtypes, &z)) return -1;
+    mssm::HeadNormArgs a{};
+    a.tokens = dims.tokens; a.q_heads = dims.q_heads; a.k_heads = dims.k_heads;
+    a.dim = dims.dim; a.rotary = dims.rotary; a.io = io_type(dtypes);
+    return static_cast<int64_t>(mssm::qk_norm_rotary_bwd_workspace(a));
+}
+
+mssm_status mssm_linear_attention_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                                      float scale, const float *h0, const int64_t *cu_seqlens, void *o,
+                                      float *h_last, void *workspace, int64_t workspace_bytes,
+                                      mssm_attention_dims dims, mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    AttentionSizes z;
+    if (mssm_status s = check_attention(dims, scale, cu_seqlens != nullptr, dtypes, &z)) return s;
+    g_last_variant = MSSM_VARIANT_AUTO;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (z.states == 0) {
+        // no sequence covers any row
+        if (z.value_bytes && !o) return fail(MSSM_ERR_INVALID_ARG, "o is null");
+        const hipError_t e = zero_fill_bytes(o, z.value_bytes, st);
+        if (e != hipSuccess) return hip_fail(e, "zero-fill of o");
+        return MSSM_OK;
+    }
+    if (dims.total == 0) return copy_or_zero_state("h_last", h_last, "h0", h0, z.states, st);
+    if (!q) return fail(MSSM_ERR_INVALID_ARG, "q is null");
+    if (!k) return fail(MSSM_ERR_INVALID_ARG, "k is null");
+    if (!v) return fail(MSSM_ERR_INVALID_ARG, "v is null");
+    if (!log_decay) return fail(MSSM_ERR_INVALID_ARG, "log_decay is null");
+    if (!o) return fail(MSSM_ERR_INVALID_ARG, "o is null");
+    mssm::AttentionArgs a = attention_args(dims, dtypes);
+    a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.scale = scale; a.h0 = h0; a.cu_seqlens = cu_seqlens;
+    a.o = o; a.h_last = h_last;
+    Range ws;
+    if (mssm_status s = check_workspace(workspace, workspace_bytes, mssm::linear_attention_workspace(a, false), &ws))
+        return s;
+    const Range ins[] = {range("q", q, z.key_bytes), range("k", k, z.key_bytes), range("v", v, z.value_bytes),
+                         range("log_decay", log_decay, dims.heads * 4), range("h0", h0, z.state_bytes),
+                         range("cu_seqlens", cu_seqlens, (dims.seqs + 1) * 8)};
+    const Range outs[] = {range("o", o, z.value_bytes), range("h_last", h_last, z.state_bytes), ws};
+    if (mssm_status c = check_overlaps(ins, 6, outs, 3, h0, h_last)) return c;
+    const hipError_t e = mssm::launch_linear_attention_fwd(a, workspace, st);
+    if (e != hipSuccess) return hip_fail(e, "linear-attention launch");
+    return MSSM_OK;
+}
+
+mssm_status mssm_linear_attention_bwd(const void *q, const void *k, const void *v, const float *log_decay,
+                                      float scale, const float *h0, const int64_t *cu_seqlens, const void *d_o,
+                                      const float *dh_last, void *dq, void *dk, void *dv, float *dh0,
+                                      void *workspace, int64_t workspace_bytes, mssm_attention_dims dims,
+                                      mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    AttentionSizes z;
+    if (mssm_status s = check_attention(dims, scale, cu_seqlens != nullptr, dtypes, &z)) return s;
+    g_last_variant = MSSM_VARIANT_AUTO;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    Range outs[] = {range("dq", dq, z.key_bytes), range("dk", dk, z.key_bytes), range("dv", dv, z.value_bytes),
+                    range("dh0", dh0, z.state_bytes), Range{}};
+    if (z.states == 0) {
+        if (z.key_bytes && !dq) return fail(MSSM_ERR_INVALID_ARG, "dq is null");
+        if (z.key_bytes && !dk) return fail(MSSM_ERR_INVALID_ARG, "dk is null");
+        if (z.value_bytes && !dv) return fail(MSSM_ERR_INVALID_ARG, "dv is null");
+        if (mssm_status c = check_overlaps(nullptr, 0, outs, 3, nullptr, nullptr)) return c;
+        hipError_t e = zero_fill_bytes(dq, z.key_bytes, st);
+        if (e == hipSuccess) e = zero_fill_bytes(dk, z.key_bytes, st);
+        if (e == hipSuccess) e = zero_fill_bytes(dv, z.value_bytes, st);
+        if (e != hipSuccess) return hip_fail(e, "zero-fill of the gradients");
+        return MSSM_OK;
+    }
+    if (dims.total == 0) {
+        if (dh0 && dh0 == dh_last) return fail(MSSM_ERR_INVALID_ARG, "output dh0 overlaps input dh_last");
+        return copy_or_zero_state("dh0", dh0, "dh_last", dh_last, z.states, st);
+    }
+    if (!q) return fail(MSSM_ERR_INVALID_ARG, "q is null");
+    if (!k) return fail(MSSM_ERR_INVALID_ARG, "k is null");
+    if (!v) return fail(MSSM_ERR_INVALID_ARG, "v is null");
+    if (!log_decay) return fail(MSSM_ERR_INVALID_ARG, "log_decay is null");
+    if (!d_o) return fail(MSSM_ERR_INVALID_ARG, "d_o is null");
+    if (!dq) return fail(MSSM_ERR_INVALID_ARG, "dq is null");
+    if (!dk) return fail(MSSM_ERR_INVALID_ARG, "dk is null");
+    if (!dv) return fail(MSSM_ERR_INVALID_ARG, "dv is null");
+    mssm::AttentionArgs a = attention_args(dims, dtypes);
+    a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.scale = scale; a.h0 = h0; a.cu_seqlens = cu_seqlens;
+    a.dout = d_o; a.dh_last = dh_last; a.dq = dq; a.dk = dk; a.dv = dv; a.dh0 = dh0;
+    if (mssm_status s = check_workspace(workspace, workspace_bytes, mssm::linear_attention_workspace(a, true), &outs[4]))
+        return s;
+    const Range ins[] = {range("q", q, z.key_bytes), range("k", k, z.key_bytes), range("v", v, z.value_bytes),
+                         range("log_decay", log_decay, dims.heads * 4), range("h0", h0, z.state_bytes),
+                         range("cu_seqlens", cu_seqlens, (dims.seqs + 1) * 8), range("d_o", d_o, z.value_bytes),
+                         range("dh_last", dh_last, z.state_bytes)};
+    if (mssm_status c = check_overlaps(ins, 8, outs, 5, nullptr, nullptr)) return c;
+    const hipError_t e = mssm::launch_linear_attention_bwd(a, workspace, st);
+    if (e != hipSuccess) return hip_fail(e, "linear-attention backward launch");
+    return MSSM_OK;
+}
+
+mssm_status mssm_linear_attention_update(float *state, const void *q, const void *k, const void *v,
+                                         const float *log_decay, float scale, void *o,
+                                         mssm_attention_dims dims, mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    dims.seqlen = 1;
+    dims.total = dims.seqs;
+    AttentionSizes z;
+    if (mssm_status s = check_attention(dims, scale, false, dtypes, &z)) return s;
+    g_last_variant = MSSM_VARIANT_AUTO;
+    if (z.states == 0) return MSSM_OK;
+    if (!state) return fail(MSSM_ERR_INVALID_ARG, "state is null");
+    if (!q) return fail(MSSM_ERR_INVALID_ARG, "q is null");
+    if (!k) return fail(MSSM_ERR_INVALID_ARG, "k is null");
+    if (!v) return fail(MSSM_ERR_INVALID_ARG, "v is null");
+    if (!log_decay) return fail(MSSM_ERR_INVALID_ARG, "log_decay is null");
+    if (!o) return fail(MSSM_ERR_INVALID_ARG, "o is null");
+    mssm::AttentionArgs a = attention_args(dims, dtypes);
+    a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.scale = scale; a.o = o; a.h_last = state;
+    const Range ins[] = {range("q", q, z.key_bytes), range("k", k, z.key_bytes), range("v", v, z.value_bytes),
+                         range("log_decay", log_decay, dims.heads * 4)};
+    const Range outs[] = {range("o", o, z.value_bytes), range("state", state, z.state_bytes)};
+    if (mssm_status c = check_overlaps(ins, 4, outs, 2, nullptr, nullptr)) return c;
+    const hipError_t e = mssm::launch_linear_attention_update(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "linear-attention step launch");
+    return MSSM_OK;
+}
+
+int64_t mssm_linear_attention_workspace(mssm_attention_dims dims, mssm_dtypes dtypes, int backward) {
+    g_last_error.clear();
+    AttentionSizes z;
+    if (check_attention(dims, 0.0f, true, dtypes, &z)) return -1;
+    if (z.states == 0 || dims.total == 0) return 0;
+    return static_cast<int64_t>(mssm::linear_attention_workspace(attention_args(dims, dtypes), backward != 0));
+}
+
+mssm_status mssm_beam_select(const void *logits, const float *scores, float *out_scores, int64_t *out_tokens,
+                             int64_t *out_beams, void *workspace, int64_t workspace_bytes,
+                             mssm_beam_dims dims, mssm_dtypes dtypes, void *stream) {
+    g_last_error.clear();
+    if (mssm_status s = check_selection(dims, dtypes)) return s;
+    g_last_variant = MSSM_VARIANT_AUTO;
+    if (dims.batch == 0) return MSSM_OK;
+    if (!logits) return fail(MSSM_ERR_INVALID_ARG, "logits is null");
+    if (!scores) return fail(MSSM_ERR_INVALID_ARG, "scores is null");
+    if (!out_scores) return fail(MSSM_ERR_INVALID_ARG, "out_scores is null");
+    if (!out_tokens) return fail(MSSM_ERR_INVALID_ARG, "out_tokens is null");
+    if (!out_beams) return fail(MSSM_ERR_INVALID_ARG, "out_beams is null");
+    const mssm::BeamArgs a{logits, scores, out_scores, out_tokens, out_beams, dims.batch, dims.beams, dims.vocab,
+                           dims.count, io_type(dtypes)};
+    Range ws;
+    if (mssm_status s = check_workspace(workspace, workspace_bytes, mssm::beam_select_workspace(a), &ws)) return s;
+    const int64_t rows = dims.batch * dims.beams, n = dims.batch * dims.count;
+    const Range ins[] = {range("logits", logits, rows * dims.vocab * (dtypes.io == MSSM_F32 ? 4 : 2)),
+                         range("scores", scores, rows * 4)};
+    const Range outs[] = {range("out_scores", out_scores, n * 4), range("out_tokens", out_tokens, n * 8),
+                          range("out_beams", out_beams, n * 8), ws};
+    if (mssm_status c = check_overlaps(ins, 2, outs, 4, nullptr, nullptr)) return c;
+    const hipError_t e = mssm::launch_beam_select(a, workspace, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "beam-selection launch");
+    return MSSM_OK;
+}
+
+int64_t mssm_beam_select_workspace(mssm_beam_dims dims, mssm_dtypes dtypes) {
+    g_last_error.clear();
+    if (check_selection(dims, dtypes)) return -1;
+    mssm::BeamArgs a{};
+    a.batch = dims.batch; a.beams = dims.beams; a.vocab = dims.vocab; a.count = dims.count;
+    return static_cast<int64_t>(mssm::beam_select_workspace(a));
+}
+
+mssm_status mssm_state_reorder(void *const *states, const int64_t *row_bytes, int64_t count, const int64_t *origins,
+                               mssm_beam_dims dims, void *stream) {
+    g_last_error.clear();
+    if (mssm_status s = check_beams(dims)) return s;
+    if (count < 0) return fail(MSSM_ERR_INVALID_ARG, "negative size (count %lld)", (long long)count);
+    g_last_variant = MSSM_VARIANT_AUTO;
+    if (dims.batch == 0 || count == 0) return MSSM_OK;
+    if (!states) return fail(MSSM_ERR_INVALID_ARG, "states is null");
+    if (!row_bytes) return fail(MSSM_ERR_INVALID_ARG, "row_bytes is null");
+    if (!origins) return fail(MSSM_ERR_INVALID_ARG, "origins is null");
+    const int64_t rows = dims.batch * dims.beams;
+    const Range from = range("origins", origins, rows * 8);
+    for (int64_t i = 0; i < count; ++i) {
+        int64_t bytes;
+        if (row_bytes[i] < 0) return fail(MSSM_ERR_INVALID_ARG, "negative size (row_bytes[%lld])", (long long)i);
+        if (row_bytes[i] == 0) continue;
+        if (!states[i]) return fail(MSSM_ERR_INVALID_ARG, "states[%lld] is null", (long long)i);
+        if (!mul_ok(rows, row_bytes[i], &bytes)) return fail(MSSM_ERR_INVALID_ARG, "sizes overflow int64");
+        if (row_bytes[i] >= (int64_t(1) << 40) ||
+            mssm::state_reorder_blocks(states[i], row_bytes[i]) * dims.batch >= (int64_t(1) << 24))
+            return fail(MSSM_ERR_UNSUPPORTED, "states[%lld]: %lld entries of %lld bytes a beam are too large", (long long)i,
+                        (long long)dims.batch, (long long)row_bytes[i]);
+        const Range mine = range("states", states[i], bytes);
+        if (overlaps(mine, from)) return fail(MSSM_ERR_INVALID_ARG, "states[%lld] overlaps origins", (long long)i);
+        for (int64_t j = 0; j < i; ++j)
+            if (row_bytes[j] && overlaps(mine, range("states", states[j], rows * row_bytes[j])))
+                return fail(MSSM_ERR_INVALID_ARG, "states[%lld] overlaps states[%lld]", (long long)i, (long long)j);
+    }
+    const hipError_t e = mssm::launch_state_reorder(states, row_bytes, count, origins, dims.batch, dims.beams,
+                                                    static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "state-reorder launch");
+    return MSSM_OK;
 }
 
 mssm_variant mssm_force_variant(mssm_variant v) {
