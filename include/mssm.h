@@ -719,11 +719,13 @@ typedef struct {
  * products run on the matrix cores: float32 sums of exact products of bfloat16
  * values; inside a chunk the decayed products q.k, and the state as it meets q,
  * enter as bfloat16 where `io` is bfloat16 (float32 otherwise), while the state
- * itself is carried in float32.  Results are repeatable bit for bit.
+ * itself is carried in float32.  Results are repeatable bit for bit.  A v that is
+ * infinite or NaN makes its own column NaN from its step on, in o and in the state;
+ * a q or k that is not finite reaches what the formula says it does.
  * Errors as for mssm_selective_scan_fwd; also MSSM_ERR_INVALID_ARG for a scale
  * that is not finite, key or value < 1, or total != seqs * seqlen without
  * cu_seqlens; MSSM_ERR_UNSUPPORTED for key or value > MSSM_MAX_HEAD_DIM,
- * seqs * heads >= 2^20 or total >= 2^31.  seqs == 0 or heads == 0: o is zeroed.
+ * heads >= 2^15, seqs * heads >= 2^20 or total >= 2^31.  seqs == 0 or heads == 0: o is zeroed.
  */
 MSSM_API mssm_status mssm_linear_attention_fwd(const void *q, const void *k,
                                 const void *v, const float *log_decay,

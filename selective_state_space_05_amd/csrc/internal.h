@@ -281,7 +281,6 @@ struct AttentionArgs {
     int64_t seqs, seqlen, total, heads, key, value;
     IoType io;
 };
-bool linear_attention_supported(const AttentionArgs &a);
 size_t linear_attention_workspace(const AttentionArgs &a, bool bwd);
 hipError_t launch_linear_attention_fwd(const AttentionArgs &a, void *workspace, hipStream_t stream);
 hipError_t launch_linear_attention_bwd(const AttentionArgs &a, void *workspace, hipStream_t stream);

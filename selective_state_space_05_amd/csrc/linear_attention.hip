@@ -3,7 +3,7 @@
 //
 //   S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   g = e^log_decay
 //
-// A walk goes over a sequence C steps at a time with the state X in front of the
+// A walk goes over a sequence C = 32 steps at a time with the state X in front of the
 // chunk in matrix-core accumulators:
 //   o_i = scale (g^(i+e) X^T q_i + sum_{j <= i} g^(i-j) (q_i . k_j) v_j)
 //   X  <- g^n X + sum_j g^(n-e-j) k_j v_j^T               (n steps in the chunk)
@@ -128,6 +128,7 @@ struct Walk {
     int slices;              // of B, over workgroups
     int early;               // e above
     int reverse;             // against time
+    int vectors;             // bits 0, 1, 2: rows of q, k, v are whole 16-byte vectors
     float inner, scale;      // factors of the inputs' products and of the outputs
 };
 
@@ -160,7 +161,7 @@ __device__ __forceinline__ float decay_log2(const float *log_decay, int64_t h) {
     return d < -300.0f ? -300.0f : d;
 }
 
-constexpr int kChunkBytes = 128;   // C elements: 64 steps in bfloat16, 32 in float32
+constexpr int C = 32;   // steps of a chunk: one block of products
 
 // KP: A rounded up to whole products.  WAVES: 32 columns of B each.
 template <typename T, int KP_, int WAVES_>
@@ -168,82 +169,96 @@ struct Shape {
     typedef T Type;
     typedef typename FragOf<T>::type Frag;
     static constexpr int KP = KP_, WAVES = WAVES_, threads = 64 * WAVES, VP = 32 * WAVES;
-    static constexpr int C = kChunkBytes / sizeof(T), E = 16 / sizeof(T);   // E: elements of a vector
+    static constexpr int E = 16 / sizeof(T);                                // elements of a vector
     static constexpr int kp = KP + E, vp = VP + E;                          // pitches in LDS
-    static constexpr int lds = (2 * C * kp + C * vp) * sizeof(T), lds_state = (C * kp + C * vp) * sizeof(T);
+    // bytes of a chunk's tiles in LDS, and how many chunks: two, where two fit
+    static constexpr int tiles(bool out) { return ((out ? 2 : 1) * C * kp + C * vp) * static_cast<int>(sizeof(T)); }
+    static constexpr int stages(bool out) { return 2 * tiles(out) <= 156 * 1024 ? 2 : 1; }
     static constexpr int nk = C * KP / E / threads, nv = C * VP / E / threads;   // vectors of a tile a thread moves
 };
 
-// Whether any of a vector's elements is infinite or NaN.
-__device__ __forceinline__ bool not_finite(u32x4 v, uint16_t) {
-    bool r = false;
+// Bits of the elements of a vector that are infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite(u32x4 v, uint16_t) {
+    uint32_t r = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r |= (v[j] & 0x7f80u) == 0x7f80u || (v[j] & 0x7f800000u) == 0x7f800000u;
+    for (int j = 0; j < 4; ++j)
+        r |= ((v[j] & 0x7f80u) == 0x7f80u ? 1u : 0u) << 2 * j | ((v[j] & 0x7f800000u) == 0x7f800000u ? 2u : 0u) << 2 * j;
     return r;
 }
-__device__ __forceinline__ bool not_finite(u32x4 v, float) {
-    bool r = false;
+__device__ __forceinline__ uint32_t not_finite(u32x4 v, float) {
+    uint32_t r = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r |= (v[j] & 0x7f800000u) == 0x7f800000u;
+    for (int j = 0; j < 4; ++j) r |= ((v[j] & 0x7f800000u) == 0x7f800000u ? 1u : 0u) << j;
     return r;
 }
 
-// A walk's products leave out later inputs by a factor 0, which a v that is infinite
-// or NaN would carry to earlier outputs of its chunk: a chunk that holds such a value
-// is walked a step at a time.
+// The rows of one head of a tensor, in the order that a walk goes over them.
+template <typename T>
+struct Rows {
+    const T *p;          // the head's values in the sequence's first row of the walk
+    int64_t ld;          // values between rows, negative against time
+    int width;
+    bool vectors;        // rows are whole vectors on 16-byte boundaries
+};
 
-// A tile of C rows on its way from memory: P columns of `width` that exist, the
-// others and rows from n on are 0.  Rows begin at any element.
+// A tile of C rows on its way from memory into P columns, those from `width` on and rows
+// from n on being 0.
 template <typename S, int P, int N>
 struct Stage {
     typedef typename S::Type T;
+    static constexpr int kLine = P / S::E;                  // vectors of a row
+    static constexpr int kStep = S::threads / kLine;        // rows between a thread's vectors
     u32x4 r[N];
 
-    __device__ __forceinline__ void load(const T *base, int64_t row0, int64_t step, int64_t ld, int n, int width) {
-        typedef u32x4 Any __attribute__((aligned(2)));   // rows begin at any element
+    __device__ __forceinline__ void load(const Rows<T> &R, int64_t t, int n) {
+        const int row = threadIdx.x / kLine, c = threadIdx.x % kLine * S::E;
+        if (R.vectors) {
+            // rows past the end lie outside the buffer and read as zero: behind it, or, against
+            // time, in front of it (their offsets are negative, far behind as unsigned ones)
+            const int ld = static_cast<int>(R.ld) * static_cast<int>(sizeof(T)), low = R.ld < 0 ? n - 1 : 0;
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<T *>(R.p + (t + low) * R.ld), 0,
+                (n - 1) * (R.ld < 0 ? -ld : ld) + R.width * static_cast<int>(sizeof(T)), 0x00020000);
+            const int first = c < R.width ? (row - low) * ld + c * static_cast<int>(sizeof(T)) : INT32_MIN;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     rsrc, c < R.width ? first + i * kStep * ld : INT32_MIN, 0, 0));
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int id = i * S::threads + threadIdx.x, row = id / (P / S::E), c = id % (P / S::E) * S::E;
-            r[i] = u32x4{0, 0, 0, 0};
-            if (row < n && c < width) {
-                const T *p = base + (row0 + row * step) * ld + c;
-                if (c + S::E <= width) {
-                    r[i] = *reinterpret_cast<const Any *>(p);
-                } else {
-                    T t[S::E] = {};
+            T v[S::E] = {};
+            if (row + i * kStep < n) {
+                const T *p = R.p + (t + row + i * kStep) * R.ld + c;
 #pragma unroll
-                    for (int x = 0; x < S::E; ++x)
-                        if (c + x < width) t[x] = p[x];
-                    r[i] = *reinterpret_cast<const u32x4 *>(t);
-                }
+                for (int x = 0; x < S::E; ++x)
+                    if (c + x < R.width) v[x] = p[x];
             }
+            r[i] = *reinterpret_cast<const u32x4 *>(v);
         }
     }
-    __device__ __forceinline__ bool odd() const {
-        bool any = false;
+    // Takes the infinite and NaN values out; f(row, column) for each.
+    template <typename F>
+    __device__ __forceinline__ void clean(F f) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) any |= not_finite(r[i], T());
-        return any;
+        for (int i = 0; i < N; ++i) {
+            uint32_t odd = not_finite(r[i], T());
+            if (odd == 0) continue;
+#pragma unroll
+            for (int x = 0; x < S::E; ++x)
+                if (odd >> x & 1) {
+                    r[i][x * sizeof(T) / 4] &= sizeof(T) == 4 ? 0u : x % 2 ? 0x0000ffffu : 0xffff0000u;
+                    f(threadIdx.x / kLine + i * kStep, threadIdx.x % kLine * S::E + x);
+                }
+        }
     }
     __device__ __forceinline__ void store(T *to, int pitch) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int id = i * S::threads + threadIdx.x, row = id / (P / S::E), c = id % (P / S::E) * S::E;
-            *reinterpret_cast<u32x4 *>(to + row * pitch + c) = r[i];
-        }
+        for (int i = 0; i < N; ++i)
+            *reinterpret_cast<u32x4 *>(to + (threadIdx.x / kLine + i * kStep) * pitch + threadIdx.x % kLine * S::E) = r[i];
     }
 };
-
-// The lane's contraction values outside steps lo .. hi - 1, the first of them being
-// step `at`, set to 0.
-template <typename F>
-__device__ __forceinline__ void keep_steps(F &f, int at, int lo, int hi) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int step = at + j / 4 * 8 + j % 4;
-        if (step < lo || step >= hi) set(f, j, 0.0f);
-    }
-}
 
 // Eight outputs side by side, those from `width` on left out.
 __device__ __forceinline__ void store8(uint16_t *p, const float *f, int left) {
@@ -274,13 +289,18 @@ __device__ __forceinline__ void store8(float *p, const float *f, int left) {
 
 // OUT: the walk with its outputs; else for the segments' states alone.
 template <typename S, bool OUT>
-__global__ __launch_bounds__(S::threads) void attention_walk_kernel(const Walks W) {
+__global__ __launch_bounds__(S::threads, S::KP <= 64 || (S::KP <= 128 && sizeof(typename S::Type) == 2) ? 2 : 1) void attention_walk_kernel(const Walks W) {
     typedef typename S::Type T;
     typedef typename S::Frag Frag;
-    constexpr int C = S::C, KB = S::KP / 32, KS = S::KP / 16, CS = C / 16, CB = C / 32;
+    constexpr int KB = S::KP / 32, KS = S::KP / 16, CS = C / 16;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    __shared__ int64_t odd_chunk;      // the last chunk with an infinite or NaN v
-    T *const Ks = reinterpret_cast<T *>(smem), *const Vs = Ks + C * S::kp, *const Qs = Vs + C * S::vp;
+    // A product leaves out later inputs by a factor 0, which an infinite or NaN v would
+    // carry to earlier outputs of its chunk.  Such values are taken out, and what they reach
+    // is set to NaN: their column from their step on.  Here: the first such step of every
+    // column, with the chunk's number above it, so that older entries are told apart.
+    __shared__ uint32_t reached[OUT ? 2 : 1][OUT ? S::VP : 1], odd_chunk[2];
+    constexpr int kTiles = S::tiles(OUT) / static_cast<int>(sizeof(T)), kStages = S::stages(OUT);
+    T *const tiles = reinterpret_cast<T *>(smem);
 
     // workgroups go to the eight XCDs in turn: each gets a run of consecutive
     // positions, so that the walks over one head's rows share its L2
@@ -348,126 +368,123 @@ __global__ __launch_bounds__(S::threads) void attention_walk_kernel(const Walks 
         }
     }
 
-    // decays inside a chunk: of outputs (this lane's is col of every block of 32) from
-    // the inputs of their own block and of the one before, and of the state
-    float inside[16], across[16], weight[8];
+    // decays inside a chunk: of outputs (this lane's is col) from its inputs and from the
+    // state in front, and of the inputs to the state behind
+    float inside[16], weight[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-        const int gap = col - acc_row(j) - 4 * half;
-        inside[j] = w.inner * power(max(gap, 0));
-        across[j] = CB > 1 ? w.inner * power(32 + gap) : 0.0f;
+        const int row = acc_row(j) + 4 * half;
+        inside[j] = w.inner * power(max(col - row, 0));
+        weight[j] = w.inner * power(C - e - row);
     }
-    const float front = power(col + e), whole = power(C), block = power(32), line = power(16);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) weight[j] = w.inner * power(16 - e - 4 * half - (j / 4 * 8 + j % 4));   // of the last 16 steps
+    const float front = power(col + e);
+    float whole = power(C);
 
-    const T *q = static_cast<const T *>(w.q) + h * w.A, *k = static_cast<const T *>(w.k) + h * w.A,
-            *v = static_cast<const T *>(w.v) + h * w.B + v0;
-    const int64_t lda = W.heads * w.A, ldb = W.heads * w.B, step = w.reverse ? -1 : 1;
-    const int64_t row_first = w.reverse ? start + len - 1 : start;
+    const int64_t row_first = w.reverse ? start + len - 1 : start, sign = w.reverse ? -1 : 1;
+    const int64_t lda = W.heads * w.A, ldb = W.heads * w.B;
+    const Rows<T> q{static_cast<const T *>(w.q) + row_first * lda + h * w.A, sign * lda, w.A, (w.vectors & 1) != 0},
+        k{static_cast<const T *>(w.k) + row_first * lda + h * w.A, sign * lda, w.A, (w.vectors & 2) != 0},
+        v{static_cast<const T *>(w.v) + row_first * ldb + h * w.B + v0, sign * ldb, width, (w.vectors & 4) != 0};
+    T *o = OUT ? static_cast<T *>(w.o) + (row_first + sign * (t0 + col)) * ldb + h * w.B + v0 + 32 * wave + 8 * half : nullptr;
     Stage<S, S::KP, S::nk> kin, qin;
     Stage<S, S::VP, S::nv> vin;
     auto fetch = [&](int64_t t) {
         const int n = static_cast<int>(min(int64_t(C), t1 - t));
-        const int64_t row = row_first + t * step;
-        kin.load(k, row, step, lda, n, w.A);
-        vin.load(v, row, step, ldb, n, width);
-        if (OUT) qin.load(q, row, step, lda, n, w.A);
+        kin.load(k, t, n);
+        vin.load(v, t, n);
+        if (OUT) qin.load(q, t, n);
     };
-    if (threadIdx.x == 0) odd_chunk = -1;
+    if (OUT) {
+        for (int i = threadIdx.x; i < 2 * S::VP; i += S::threads) reached[i / S::VP][i % S::VP] = 0;
+        if (threadIdx.x < 2) odd_chunk[threadIdx.x] = 0;
+    }
     if (t0 < t1) fetch(t0);
-    for (int64_t t = t0; t < t1; t += C) {
-        const int n = static_cast<int>(min(int64_t(C), t1 - t));
-        __syncthreads();
+    __syncthreads();
+    uint32_t chunk = 1;
+    for (int64_t t = t0; t < t1; t += C, ++chunk) {
+        const int n = static_cast<int>(min(int64_t(C), t1 - t)), turn = chunk % 2;
+        T *const Ks = tiles + (kStages == 2 ? turn : 0) * kTiles, *const Vs = Ks + C * S::kp, *const Qs = Vs + C * S::vp;
+        if (OUT)
+            vin.clean([&](int row, int c) {
+                atomicMax(&reached[turn][c], chunk * (C + 1) + (C - row));
+                odd_chunk[turn] = chunk;          // alike from every thread that finds one
+            });
+        if (kStages == 1) __syncthreads();
         kin.store(Ks, S::kp);
         vin.store(Vs, S::vp);
         if (OUT) qin.store(Qs, S::kp);
-        if (OUT && vin.odd()) odd_chunk = t;      // written by any thread that finds one, alike
-        __syncthreads();
+        __syncthreads();                          // who reads the other half has read it
         if (t + C < t1) fetch(t + C);
+        const bool odd = OUT && odd_chunk[turn] == chunk;
+        if (n < C) {                              // the last chunk
+            whole = power(n);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) weight[j] = w.inner * power(max(n - e - acc_row(j) - 4 * half, 0));
+        }
 
-        // all n steps at once, or each by itself
-        const bool single = OUT && odd_chunk == t;
-        for (int lo = 0, hi = single ? 1 : n; lo < n; lo = hi, ++hi) {
-            const bool part = hi - lo < C;
-            Frag vf[CS];
+        Frag vf[CS];
 #pragma unroll
-            for (int s = 0; s < CS; ++s) {
-                vf[s] = load_col(Vs + 16 * s * S::vp + 32 * wave, S::vp, lane);
-                if (single) keep_steps(vf[s], 16 * s + 4 * half, lo, hi);
+        for (int s = 0; s < CS; ++s) vf[s] = load_col(Vs + 16 * s * S::vp + 32 * wave, S::vp, lane);
+        if (OUT) {
+            f32x16 G, O;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) G[j] = O[j] = 0.0f;
+            // The state enters as an operand of the I/O dtype: in bfloat16 half a step, 2^-8
+            // of each of its values, like the rounding of the output.
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const Frag qf = load_row(Qs + col * S::kp + 16 * s + 8 * half);
+                mma(G, load_row(Ks + col * S::kp + 16 * s + 8 * half), qf);
+                mma(O, from_acc<Frag>(X[s / 2], s % 2), qf);
             }
-            if (OUT) {
 #pragma unroll
-                for (int ib = 0; ib < CB; ++ib) {
-                    Frag qf[KS];
+            for (int j = 0; j < 16; ++j) O[j] *= front;
+            // later inputs leave nothing, whatever their products hold
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) qf[s] = load_row(Qs + (32 * ib + col) * S::kp + 16 * s + 8 * half);
-                    f32x16 O;
+            for (int j = 0; j < 16; ++j) G[j] = acc_row(j) + 4 * half <= col ? G[j] * inside[j] : 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) O[j] = 0.0f;
-                    // The state enters as an operand of the I/O dtype: in bfloat16 half a
-                    // step, 2^-8 of each of its values, like the rounding of the output.
+            for (int s = 0; s < CS; ++s) mma(O, vf[s], from_acc<Frag>(G, s));
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) mma(O, from_acc<Frag>(X[s / 2], s % 2), qf[s]);
-                    const float f = single ? power(max(32 * ib + col + e - lo, 0)) : ib == 0 ? front : front * block;
+            for (int j = 0; j < 16; ++j) O[j] *= w.scale;
+            if (odd) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) O[j] *= f;
-#pragma unroll
-                    for (int jb = 0; jb <= ib; ++jb) {
-                        f32x16 G;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) G[j] = 0.0f;
-#pragma unroll
-                        for (int s = 0; s < KS; ++s)
-                            mma(G, load_row(Ks + (32 * jb + col) * S::kp + 16 * s + 8 * half), qf[s]);
-                        // later inputs leave nothing, whatever their products hold
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            G[j] = jb < ib ? G[j] * across[j] : acc_row(j) + 4 * half <= col ? G[j] * inside[j] : 0.0f;
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) mma(O, vf[2 * jb + s], from_acc<Frag>(G, s));
-                    }
-                    const int row = 32 * ib + col;
-                    if (row >= lo && row < hi) {
-                        T *o = static_cast<T *>(w.o) + (row_first + (t + row) * step) * ldb + h * w.B + v0;
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            float out[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) out[j] = O[8 * s + j] * w.scale;
-                            const int c = 32 * wave + 16 * s + 8 * half;
-                            store8(o + c, out, width - c);
-                        }
-                    }
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t r = reached[turn][32 * wave + 16 * (j / 8) + 8 * half + j % 8];
+                    if (r / (C + 1) == chunk && col >= static_cast<int>(C - r % (C + 1))) O[j] = __builtin_nanf("");
                 }
             }
-            // The state: k_j exact, its partner g^(n-e-j) v_j in bfloat16 as the sum of two
-            // roundings, which hold it to 2^-16.
-            const float f = part ? power(hi - lo) : whole;
+            if (col < n) {
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+                for (int s = 0; s < CS; ++s) {
+                    float out[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) X[kb][j] *= f;
-            float g = 1.0f;
-#pragma unroll
-            for (int s = CS - 1; s >= 0; --s) {
-                Frag up, rest;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float u = weight[j] * g;
-                    if (part) u = w.inner * power(max(hi - e - (16 * s + 4 * half + j / 4 * 8 + j % 4), 0));
-                    u *= get(vf[s], j);
-                    set(up, j, u);
-                    set(rest, j, u - get(up, j));
+                    for (int j = 0; j < 8; ++j) out[j] = O[8 * s + j];
+                    store8(o + 16 * s, out, width - (32 * wave + 16 * s + 8 * half));
                 }
-                g *= line;
+            }
+            o += sign * C * ldb;
+        }
+        // The state: k_j exact, its partner g^(n-e-j) v_j in bfloat16 as the sum of two
+        // roundings, which hold it to 2^-16.
+        if (odd && reached[turn][32 * wave + column_of(col)] / (C + 1) == chunk) whole = __builtin_nanf("");
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    Frag a = load_col(Ks + 16 * s * S::kp + 32 * kb, S::kp, lane);
-                    if (single) keep_steps(a, 16 * s + 4 * half, lo, hi);
-                    mma(X[kb], a, up);
-                    if (sizeof(T) == 2) mma(X[kb], a, rest);
-                }
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) X[kb][j] *= whole;
+#pragma unroll
+        for (int s = 0; s < CS; ++s) {
+            Frag up, rest;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float u = weight[8 * s + j] * get(vf[s], j);
+                set(up, j, u);
+                set(rest, j, u - get(up, j));
+            }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const Frag a = load_col(Ks + 16 * s * S::kp + 32 * kb, S::kp, lane);
+                mma(X[kb], a, up);
+                if (sizeof(T) == 2) mma(X[kb], a, rest);
             }
         }
     }
@@ -519,22 +536,28 @@ int slices_of(int64_t B) { return static_cast<int>((B + 32 * waves_of(B) - 1) / 
 
 // Segments of a sequence and their steps.
 void cut(const AttentionArgs &a, bool bwd, int *segments, int64_t *steps) {
-    const int64_t chunk = a.io == IO_F32 ? 32 : 64, least = 4 * chunk;
+    const int64_t least = 8 * C;
     const int64_t walks = a.seqs * a.heads * slices_of(a.value);
     const int64_t want = std::max<int64_t>(1, (kTarget + walks - 1) / std::max<int64_t>(1, walks));
     const int64_t n = std::max<int64_t>(1, std::min(want, a.seqlen / least));
-    *steps = ((a.seqlen + n - 1) / n + chunk - 1) / chunk * chunk;
+    *steps = ((a.seqlen + n - 1) / n + C - 1) / C * C;
     *segments = *steps > 0 ? static_cast<int>((a.seqlen + *steps - 1) / *steps) : 1;
     if (*segments < 1) *segments = 1;
-    if (*steps < chunk) *steps = chunk;
+    if (*steps < C) *steps = C;
 }
 
 template <typename S, bool OUT>
-hipError_t launch_walks(const Walks &W, hipStream_t stream) {
+hipError_t launch_walks(Walks W, hipStream_t stream) {
+    for (Walk &w : W.w) {
+        const auto whole = [](const void *p, int width) {
+            return reinterpret_cast<uintptr_t>(p) % 16 == 0 && width % S::E == 0;
+        };
+        w.vectors = whole(w.q, w.A) | whole(w.k, w.A) << 1 | whole(w.v, w.B) << 2;
+    }
     int most = 0;
     for (int i = 0; i < W.count; ++i) most = std::max(most, W.w[i].slices);
     const int64_t n = W.seqs * W.segments * W.heads * most * W.count;
-    constexpr int lds = OUT ? S::lds : S::lds_state;
+    constexpr int lds = S::stages(OUT) * S::tiles(OUT);
     if (lds > 65536)
         if (const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attention_walk_kernel<S, OUT>),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds))
@@ -673,13 +696,6 @@ hipError_t step(const AttentionArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-bool linear_attention_supported(const AttentionArgs &a) {
-    if (a.key > MSSM_MAX_HEAD_DIM || a.value > MSSM_MAX_HEAD_DIM) return false;
-    // grids stay below 2^31 workgroups of up to three walks, rows below 2^31
-    if (a.seqs * a.heads >= (int64_t(1) << 16) * 16 || a.total >= (int64_t(1) << 31)) return false;
-    return true;
-}
-
 size_t linear_attention_workspace(const AttentionArgs &a, bool bwd) {
     const Walks W = common(a, bwd);
     return static_cast<size_t>(W.segments - 1) * a.seqs * a.heads * a.key * a.value * sizeof(float) * (bwd ? 2 : 1);
@@ -694,7 +710,7 @@ hipError_t launch_linear_attention_fwd(const AttentionArgs &a, void *workspace, 
     const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
     W.count = 1;
     W.w[0] = Walk{a.q, a.k, a.v, a.o, a.h0, a.h_last, static_cast<float *>(ws), V, 1, V, 1, V, 1, K, V,
-                  slices_of(V), 1, 0, 1.0f, a.scale};
+                  slices_of(V), 1, 0, 0, 1.0f, a.scale};
     hipError_t e = hipSuccess;
     if (W.segments > 1) {
         e = launch_all<false>(W, a.io == IO_F32, stream);
@@ -717,9 +733,9 @@ hipError_t launch_linear_attention_bwd(const AttentionArgs &a, void *workspace, 
     const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
     float *S = static_cast<float *>(ws), *R = S + bytes / 2 / sizeof(float);
     // S^T in (V, K) as the first walk forms it; R in (K, V) as the third does
-    const Walk dq{a.dout, a.v, a.k, a.dq, a.h0, nullptr, S, 1, V, 0, 0, K, 1, V, K, slices_of(K), 1, 0, 1.0f, a.scale};
-    const Walk dk{a.v, a.dout, a.q, a.dk, a.dh_last, nullptr, R, 1, V, 0, 0, 1, V, V, K, slices_of(K), 0, 1, a.scale, 1.0f};
-    const Walk dv{a.k, a.q, a.dout, a.dv, a.dh_last, a.dh0, R, V, 1, V, 1, V, 1, K, V, slices_of(V), 0, 1, a.scale, 1.0f};
+    const Walk dq{a.dout, a.v, a.k, a.dq, a.h0, nullptr, S, 1, V, 0, 0, K, 1, V, K, slices_of(K), 1, 0, 0, 1.0f, a.scale};
+    const Walk dk{a.v, a.dout, a.q, a.dk, a.dh_last, nullptr, R, 1, V, 0, 0, 1, V, V, K, slices_of(K), 0, 1, 0, a.scale, 1.0f};
+    const Walk dv{a.k, a.q, a.dout, a.dv, a.dh_last, a.dh0, R, V, 1, V, 1, V, 1, K, V, slices_of(V), 0, 1, 0, a.scale, 1.0f};
     hipError_t e = hipSuccess;
     if (W.segments > 1) {
         W.count = 2;

@@ -503,9 +503,9 @@ mssm_status check_attention(mssm_attention_dims d, float scale, bool packed, mss
         return fail(MSSM_ERR_INVALID_ARG, "sizes overflow");
     if (!packed && rows != d.total)
         return fail(MSSM_ERR_INVALID_ARG, "total %lld is not seqs * seqlen (%lld)", (long long)d.total, (long long)rows);
-    if (d.seqs >= (lim >> 11) || bh >= (lim >> 11) || d.total >= lim || d.seqlen >= lim)
-        return fail(MSSM_ERR_UNSUPPORTED, "seqs * heads %lld reaches 2^20, or total %lld or seqlen %lld 2^31",
-                    (long long)bh, (long long)d.total, (long long)d.seqlen);
+    if (d.seqs >= (lim >> 11) || d.heads >= (lim >> 16) || bh >= (lim >> 11) || d.total >= lim || d.seqlen >= lim)
+        return fail(MSSM_ERR_UNSUPPORTED, "heads %lld reach 2^15, seqs * heads %lld 2^20, or total %lld or seqlen %lld 2^31",
+                    (long long)d.heads, (long long)bh, (long long)d.total, (long long)d.seqlen);
     const int64_t esz = dtypes.io == MSSM_F32 ? 4 : 2, states = bh * d.key * d.value;
     *z = AttentionSizes{n * d.key * esz, n * d.value * esz, states, states * 4};
     return MSSM_OK;
