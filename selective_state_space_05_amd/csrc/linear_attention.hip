@@ -21,6 +21,7 @@
 // and the third walks every segment from the state in front of it.  Everything is
 // summed in an order that depends on the sizes alone.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_math.h"
 #include "internal.h"
@@ -32,6 +33,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int C = 32;   // steps of a chunk: one block of products
 
 // ---- fragments: eight contraction values of one row of an operand per lane; the
 // ---- lane halves hold different ones, sixteen in all for a product of 32 x 32
@@ -69,15 +72,38 @@ __device__ __forceinline__ F from_acc(const f32x16 &c, int s) {
     return f;
 }
 
-// Eight elements side by side.
-__device__ __forceinline__ bf16x8 load_row(const uint16_t *p) {
-    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(p));
+// A tile of C rows of P values in LDS.  Its 16-byte chunks are permuted inside their
+// rows so that 16 rows' reads of one chunk, and a transposed read's four chunks of four
+// rows, cover the 64 banks.
+template <typename T, int P>
+struct Tile {
+    static constexpr int E = 16 / sizeof(T), kChunks = P / E, kBytes = C * P * static_cast<int>(sizeof(T));
+    static_assert(kChunks >= 8, "a row is 128 bytes or more");
+    static __device__ __forceinline__ int swizzle(int row) {
+        return kChunks == 8 ? row / 2 % 2 * 4 + row / 4 % 4 : row % 4 * 4 + row / 4 % 4;
+    }
+    static __device__ __forceinline__ int at(int row, int chunk) {
+        return row * kChunks * 16 + (chunk ^ swizzle(row)) * 16;
+    }
+};
+
+// Eight values side by side, chunk `chunk` on, of a row.  __restrict__ here and in the
+// loads: a chunk is read only after its loads were waited for, and without the promise
+// the compiler waits for all that are under way.
+template <typename L>
+__device__ __forceinline__ bf16x8 load_row(const unsigned char *__restrict__ tile, int row, int value, uint16_t) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(tile + L::at(row, value / 8)));
 }
-__device__ __forceinline__ F8 load_row(const float *p) {
+template <typename L>
+__device__ __forceinline__ F8 load_row(const unsigned char *__restrict__ tile, int row, int value, float) {
     F8 f;
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    f.f[0] = a.x; f.f[1] = a.y; f.f[2] = a.z; f.f[3] = a.w;
-    f.f[4] = b.x; f.f[5] = b.y; f.f[6] = b.z; f.f[7] = b.w;
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + L::at(row, value / 4));
+    const f32x4 b = *reinterpret_cast<const f32x4 *>(tile + L::at(row, value / 4 + 1));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f.f[j] = a[j];
+        f.f[4 + j] = b[j];
+    }
     return f;
 }
 
@@ -88,26 +114,56 @@ __device__ __forceinline__ int column_of(int m) {
     return (m & 16) + 8 * (m / 4 % 2) + 4 * (m / 8 % 2) + m % 4;
 }
 
-// Transposed operand: row m = lane % 32 is column column_of(m) of the block whose
-// first element (line 0 of 16, column 0) p points to; the lane's contraction values
-// are lines 4 h + {0..3, 8..11}.  In bfloat16 by the transposing LDS read: the 16
-// lanes of a group fetch four lines of four chunks of four columns, lane i line
-// i / 4 of chunk i % 4, and lane i receives column i % 4 of chunk i / 4.
-__device__ __forceinline__ bf16x8 load_col(const uint16_t *__restrict__ p, int pitch, int lane) {
+// Transposed operand: row m = lane % 32 is column `value` + column_of(m) of the tile; the
+// lane's contraction values are rows `row` + 4 h + {0..3, 8..11}.  In bfloat16 by the
+// transposing LDS read: the 16 lanes of a group fetch four rows of four chunks of four
+// columns, lane i row i / 4 of chunk i % 4, and lane i receives column i % 4 of chunk
+// i / 4.
+template <typename L>
+__device__ __forceinline__ bf16x8 load_col(const unsigned char *__restrict__ tile, int row, int value, int lane, uint16_t) {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s16x4 LdsRow;
-    const int i = lane % 16;
-    const uint16_t *at = p + (4 * (lane / 32) + i / 4) * pitch + (lane & 16) + column_of(4 * (i % 4));
-    const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)at));
-    const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)(at + 8 * pitch)));
+    const int i = lane % 16, r = row + 4 * (lane / 32) + i / 4, c = (lane & 16) + column_of(4 * (i % 4));
+    const unsigned char *a = tile + L::at(r, value / 8 + c / 8) + c % 8 * 2;
+    const unsigned char *b = tile + L::at(r + 8, value / 8 + c / 8) + c % 8 * 2;
+    const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)a));
+    const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsRow *)b));
     return __builtin_bit_cast(bf16x8, u32x4{lo.x, lo.y, hi.x, hi.y});
 }
-__device__ __forceinline__ F8 load_col(const float *__restrict__ p, int pitch, int lane) {
+template <typename L>
+__device__ __forceinline__ F8 load_col(const unsigned char *__restrict__ tile, int row, int value, int lane, float) {
     F8 f;
-    const float *at = p + 4 * (lane / 32) * pitch + column_of(lane % 32);
+    const int c = value + column_of(lane % 32);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f.f[j] = at[(j / 4 * 8 + j % 4) * pitch];
+    for (int j = 0; j < 8; ++j)
+        f.f[j] = *reinterpret_cast<const float *>(tile + L::at(row + 4 * (lane / 32) + j / 4 * 8 + j % 4, c / 4) + c % 4 * 4);
     return f;
+}
+
+// The infinite and NaN values of a fragment set to 0; the number of the first step that
+// held one, its own steps being `first` + {0..3, 8..11}, or `none`.
+__device__ __forceinline__ bool any_odd(const bf16x8 &f) {
+    const u32x4 v = __builtin_bit_cast(u32x4, f);
+    uint32_t r = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r |= (v[j] & 0x7fff7fffu) + 0x00800080u;   // an exponent of all ones carries
+    return r & 0x80008000u;
+}
+__device__ __forceinline__ bool any_odd(const F8 &f) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r |= (__float_as_uint(f.f[j]) & 0x7fffffffu) + 0x00800000u;
+    return r & 0x80000000u;
+}
+template <typename F>
+__device__ __forceinline__ int clean(F &f, int first, int none) {
+#pragma unroll
+    for (int j = 7; j >= 0; --j)
+        if (!(fabsf(get(f, j)) < __builtin_inff())) {
+            set(f, j, 0.0f);
+            none = first + j / 4 * 8 + j % 4;
+        }
+    return none;
 }
 
 // ---- one walk ------------------------------------------------------------------
@@ -128,7 +184,6 @@ struct Walk {
     int slices;              // of B, over workgroups
     int early;               // e above
     int reverse;             // against time
-    int vectors;             // bits 0, 1, 2: rows of q, k, v are whole 16-byte vectors
     float inner, scale;      // factors of the inputs' products and of the outputs
 };
 
@@ -161,146 +216,139 @@ __device__ __forceinline__ float decay_log2(const float *log_decay, int64_t h) {
     return d < -300.0f ? -300.0f : d;
 }
 
-constexpr int C = 32;   // steps of a chunk: one block of products
 
-// KP: A rounded up to whole products.  WAVES: 32 columns of B each.
-template <typename T, int KP_, int WAVES_>
+// KP: A rounded up to whole products.  WAVES: 32 columns of B each.  VEC: all rows are
+// whole 16-byte vectors on 16-byte boundaries.
+template <typename T, int KP_, int WAVES_, bool VEC_>
 struct Shape {
     typedef T Type;
     typedef typename FragOf<T>::type Frag;
+    static constexpr bool VEC = VEC_;
     static constexpr int KP = KP_, WAVES = WAVES_, threads = 64 * WAVES, VP = 32 * WAVES;
-    static constexpr int E = 16 / sizeof(T);                                // elements of a vector
-    static constexpr int kp = KP + E, vp = VP + E;                          // pitches in LDS
-    // bytes of a chunk's tiles in LDS, and how many chunks: two, where two fit
-    static constexpr int tiles(bool out) { return ((out ? 2 : 1) * C * kp + C * vp) * static_cast<int>(sizeof(T)); }
-    static constexpr int stages(bool out) { return 2 * tiles(out) <= 156 * 1024 ? 2 : 1; }
-    static constexpr int nk = C * KP / E / threads, nv = C * VP / E / threads;   // vectors of a tile a thread moves
+    typedef Tile<T, KP> Keys;
+    typedef Tile<T, VP> Values;
+    // bytes of a chunk's tiles in LDS, and how many chunks: loads of whole vectors go
+    // straight to LDS, two chunks ahead where there is room
+    static constexpr int tiles(bool out) { return (out ? 2 : 1) * Keys::kBytes + Values::kBytes; }
+    static constexpr int stages(bool out) {
+        const int fit = 160 * 1024 / tiles(out), most = VEC ? 3 : 2;
+        return fit < most ? fit : most;
+    }
+    // registers for two waves a SIMD, but for the largest states
+    static constexpr int waves_a_simd(bool) { return KP <= 64 || (KP <= 128 && sizeof(T) == 2) ? 2 : 1; }
+    static constexpr int loads(bool out) { return tiles(out) / 1024 / WAVES; }   // of a wave and chunk
+    static constexpr int stores = C * 32 * sizeof(T) / 1024;                     // the same
 };
-
-// Bits of the elements of a vector that are infinite or NaN.
-__device__ __forceinline__ uint32_t not_finite(u32x4 v, uint16_t) {
-    uint32_t r = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        r |= ((v[j] & 0x7f80u) == 0x7f80u ? 1u : 0u) << 2 * j | ((v[j] & 0x7f800000u) == 0x7f800000u ? 2u : 0u) << 2 * j;
-    return r;
-}
-__device__ __forceinline__ uint32_t not_finite(u32x4 v, float) {
-    uint32_t r = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r |= ((v[j] & 0x7f800000u) == 0x7f800000u ? 1u : 0u) << j;
-    return r;
-}
 
 // The rows of one head of a tensor, in the order that a walk goes over them.
 template <typename T>
 struct Rows {
-    const T *p;          // the head's values in the sequence's first row of the walk
+    T *p;                // the head's values in the sequence's first row of the walk
     int64_t ld;          // values between rows, negative against time
     int width;
-    bool vectors;        // rows are whole vectors on 16-byte boundaries
+
+    // A buffer of the n rows of a chunk from row t on: those past the end lie outside it,
+    // behind it or, against time, in front (their offsets are negative, far behind as
+    // unsigned ones), read as zero and are not written.  Offsets are those of offset() plus shift().
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(int64_t t, int n) const {
+        const int bytes = static_cast<int>(ld < 0 ? -ld : ld) * static_cast<int>(sizeof(T));
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<std::remove_const_t<T> *>(p + (t + (ld < 0 ? n - 1 : 0)) * ld), 0,
+                                                 (n - 1) * bytes + width * static_cast<int>(sizeof(T)), 0x00020000);
+    }
+    __device__ __forceinline__ int shift(int n) const {
+        return ld < 0 ? -(n - 1) * static_cast<int>(ld) * static_cast<int>(sizeof(T)) : 0;
+    }
+    __device__ __forceinline__ int offset(int row, int value) const {
+        return value < width ? (row * static_cast<int>(ld) + value) * static_cast<int>(sizeof(T)) : INT32_MIN;
+    }
 };
 
-// A tile of C rows on its way from memory into P columns, those from `width` on and rows
-// from n on being 0.
-template <typename S, int P, int N>
-struct Stage {
+// A tile's way from memory: columns from `width` on and rows from n on are 0.
+template <typename S, typename L>
+struct Feed {
     typedef typename S::Type T;
-    static constexpr int kLine = P / S::E;                  // vectors of a row
-    static constexpr int kStep = S::threads / kLine;        // rows between a thread's vectors
-    u32x4 r[N];
+    typedef __attribute__((address_space(3))) void Lds;
+    static constexpr int N = L::kBytes / 1024 / S::WAVES;    // instructions of 1024 bytes a wave
+    u32x4 r[S::VEC ? 1 : N];
 
-    __device__ __forceinline__ void load(const Rows<T> &R, int64_t t, int n) {
-        const int row = threadIdx.x / kLine, c = threadIdx.x % kLine * S::E;
-        if (R.vectors) {
-            // rows past the end lie outside the buffer and read as zero: behind it, or, against
-            // time, in front of it (their offsets are negative, far behind as unsigned ones)
-            const int ld = static_cast<int>(R.ld) * static_cast<int>(sizeof(T)), low = R.ld < 0 ? n - 1 : 0;
-            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<T *>(R.p + (t + low) * R.ld), 0,
-                (n - 1) * (R.ld < 0 ? -ld : ld) + R.width * static_cast<int>(sizeof(T)), 0x00020000);
-            const int first = c < R.width ? (row - low) * ld + c * static_cast<int>(sizeof(T)) : INT32_MIN;
+    // Row and chunk of this lane's 16 bytes of instruction i.
+    static __device__ __forceinline__ int row(int i) {
+        return (i * S::threads + static_cast<int>(threadIdx.x)) / L::kChunks;
+    }
+    static __device__ __forceinline__ int chunk(int i) {
+        return static_cast<int>(threadIdx.x) % L::kChunks ^ L::swizzle(row(i));
+    }
+    // Straight into LDS.
+    static __device__ __forceinline__ void send(const Rows<const T> &R, int64_t t, int n, int wave,
+                                                unsigned char *__restrict__ tile) {
+#if defined(__HIP_DEVICE_COMPILE__)   // with the builtin in it, the host pass leaves out the kernel's handle
+        const auto rsrc = R.buffer(t, n);
+        const int shift = R.shift(n);
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                     rsrc, c < R.width ? first + i * kStep * ld : INT32_MIN, 0, 0));
-            return;
-        }
+        for (int i = 0; i < N; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds *)(tile + (i * S::WAVES + wave) * 1024), 16,
+                                                     R.offset(row(i), chunk(i) * S::Keys::E) + shift, 0, 0, 0);
+#endif
+    }
+    // Through registers, element by element.
+    __device__ __forceinline__ void fetch(const Rows<const T> &R, int64_t t, int n) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            T v[S::E] = {};
-            if (row + i * kStep < n) {
-                const T *p = R.p + (t + row + i * kStep) * R.ld + c;
+            T v[L::E] = {};
+            if (row(i) < n) {
+                const T *p = R.p + (t + row(i)) * R.ld;
 #pragma unroll
-                for (int x = 0; x < S::E; ++x)
-                    if (c + x < R.width) v[x] = p[x];
+                for (int x = 0; x < L::E; ++x)
+                    if (chunk(i) * L::E + x < R.width) v[x] = p[chunk(i) * L::E + x];
             }
             r[i] = *reinterpret_cast<const u32x4 *>(v);
         }
     }
-    // Takes the infinite and NaN values out; f(row, column) for each.
-    template <typename F>
-    __device__ __forceinline__ void clean(F f) {
+    __device__ __forceinline__ void store(unsigned char *tile) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            uint32_t odd = not_finite(r[i], T());
-            if (odd == 0) continue;
-#pragma unroll
-            for (int x = 0; x < S::E; ++x)
-                if (odd >> x & 1) {
-                    r[i][x * sizeof(T) / 4] &= sizeof(T) == 4 ? 0u : x % 2 ? 0x0000ffffu : 0xffff0000u;
-                    f(threadIdx.x / kLine + i * kStep, threadIdx.x % kLine * S::E + x);
-                }
-        }
-    }
-    __device__ __forceinline__ void store(T *to, int pitch) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            *reinterpret_cast<u32x4 *>(to + (threadIdx.x / kLine + i * kStep) * pitch + threadIdx.x % kLine * S::E) = r[i];
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(tile + (i * S::threads + threadIdx.x) * 16) = r[i];
     }
 };
 
-// Eight outputs side by side, those from `width` on left out.
-__device__ __forceinline__ void store8(uint16_t *p, const float *f, int left) {
-    typedef u32x4 Any __attribute__((aligned(2)));
+// Waits until at most N of this wave's loads and stores are under way, then for the
+// other waves.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+}
+
+// Eight outputs side by side: as whole vectors, or one by one up to `left`.
+__device__ __forceinline__ void store_vectors(const Rows<uint16_t> &o, int64_t t, int n, int row, int value, const float *f) {
     bf16x8 b;
 #pragma unroll
     for (int j = 0; j < 8; ++j) b[j] = static_cast<__bf16>(f[j]);
-    const u32x4 v = __builtin_bit_cast(u32x4, b);
-    if (left >= 8) {
-        *reinterpret_cast<Any *>(p) = v;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < left) p[j] = static_cast<uint16_t>(v[j / 2] >> 16 * (j % 2));
-    }
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, b), o.buffer(t, n), o.offset(row, value) + o.shift(n), 0, 0);
 }
-__device__ __forceinline__ void store8(float *p, const float *f, int left) {
-    typedef f32x4 Any __attribute__((aligned(4)));
-    if (left >= 8) {
-        reinterpret_cast<Any *>(p)[0] = f32x4{f[0], f[1], f[2], f[3]};
-        reinterpret_cast<Any *>(p)[1] = f32x4{f[4], f[5], f[6], f[7]};
-    } else {
+__device__ __forceinline__ void store_vectors(const Rows<float> &o, int64_t t, int n, int row, int value, const float *f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < left) p[j] = f[j];
-    }
+    for (int i = 0; i < 2; ++i)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            u32x4{__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3])},
+            o.buffer(t, n), o.offset(row, value + 4 * i) + o.shift(n), 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float *f, int left) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < left) Io<T>::store(p, j, f[j]);
 }
 
 // OUT: the walk with its outputs; else for the segments' states alone.
 template <typename S, bool OUT>
-__global__ __launch_bounds__(S::threads, S::KP <= 64 || (S::KP <= 128 && sizeof(typename S::Type) == 2) ? 2 : 1) void attention_walk_kernel(const Walks W) {
+__global__ __launch_bounds__(S::threads, S::waves_a_simd(OUT)) void attention_walk_kernel(const Walks W) {
     typedef typename S::Type T;
     typedef typename S::Frag Frag;
     constexpr int KB = S::KP / 32, KS = S::KP / 16, CS = C / 16;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    // A product leaves out later inputs by a factor 0, which an infinite or NaN v would
-    // carry to earlier outputs of its chunk.  Such values are taken out, and what they reach
-    // is set to NaN: their column from their step on.  Here: the first such step of every
-    // column, with the chunk's number above it, so that older entries are told apart.
-    __shared__ uint32_t reached[OUT ? 2 : 1][OUT ? S::VP : 1], odd_chunk[2];
-    constexpr int kTiles = S::tiles(OUT) / static_cast<int>(sizeof(T)), kStages = S::stages(OUT);
-    T *const tiles = reinterpret_cast<T *>(smem);
+    constexpr int kStages = S::stages(OUT), kTiles = S::tiles(OUT), kLoads = S::loads(OUT);
+    constexpr int kStores = OUT ? S::stores : 0;
 
     // workgroups go to the eight XCDs in turn: each gets a run of consecutive
     // positions, so that the walks over one head's rows share its L2
@@ -325,7 +373,7 @@ __global__ __launch_bounds__(S::threads, S::KP <= 64 || (S::KP <= 128 && sizeof(
     const int64_t t0 = seg * W.segment;
     const bool tail = seg == W.segments - 1;       // walks to the end, however far
     const int64_t t1 = tail ? len : min(len, t0 + W.segment);
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, half = lane / 32, col = lane % 32;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, half = lane / 32, col = lane % 32;
     const int v0 = slice * S::VP, width = min(S::VP, w.B - v0);
 
     if (OUT && W.cu && ((b == 0 && seg == 0) || (b == W.seqs - 1 && tail))) {
@@ -382,49 +430,84 @@ __global__ __launch_bounds__(S::threads, S::KP <= 64 || (S::KP <= 128 && sizeof(
 
     const int64_t row_first = w.reverse ? start + len - 1 : start, sign = w.reverse ? -1 : 1;
     const int64_t lda = W.heads * w.A, ldb = W.heads * w.B;
-    const Rows<T> q{static_cast<const T *>(w.q) + row_first * lda + h * w.A, sign * lda, w.A, (w.vectors & 1) != 0},
-        k{static_cast<const T *>(w.k) + row_first * lda + h * w.A, sign * lda, w.A, (w.vectors & 2) != 0},
-        v{static_cast<const T *>(w.v) + row_first * ldb + h * w.B + v0, sign * ldb, width, (w.vectors & 4) != 0};
-    T *o = OUT ? static_cast<T *>(w.o) + (row_first + sign * (t0 + col)) * ldb + h * w.B + v0 + 32 * wave + 8 * half : nullptr;
-    Stage<S, S::KP, S::nk> kin, qin;
-    Stage<S, S::VP, S::nv> vin;
-    auto fetch = [&](int64_t t) {
-        const int n = static_cast<int>(min(int64_t(C), t1 - t));
-        kin.load(k, t, n);
-        vin.load(v, t, n);
-        if (OUT) qin.load(q, t, n);
+    const Rows<const T> q{static_cast<const T *>(w.q) + row_first * lda + h * w.A, sign * lda, w.A},
+        k{static_cast<const T *>(w.k) + row_first * lda + h * w.A, sign * lda, w.A},
+        v{static_cast<const T *>(w.v) + row_first * ldb + h * w.B + v0, sign * ldb, width};
+    const Rows<T> o{OUT ? static_cast<T *>(w.o) + row_first * ldb + h * w.B + v0 : nullptr, sign * ldb, width};
+    const int my_out = 32 * wave + 8 * half;      // first of the outputs of row col
+    Feed<S, typename S::Keys> kin, qin;
+    Feed<S, typename S::Values> vin;
+    auto steps = [&](int64_t t) { return static_cast<int>(min(int64_t(C), t1 - t)); };
+    auto send = [&](int64_t t, int stage) {
+        unsigned char *const to = smem + stage * kTiles;
+        kin.send(k, t, steps(t), wave, to);
+        vin.send(v, t, steps(t), wave, to + S::Keys::kBytes);
+        if (OUT) qin.send(q, t, steps(t), wave, to + S::Keys::kBytes + S::Values::kBytes);
     };
-    if (OUT) {
-        for (int i = threadIdx.x; i < 2 * S::VP; i += S::threads) reached[i / S::VP][i % S::VP] = 0;
-        if (threadIdx.x < 2) odd_chunk[threadIdx.x] = 0;
+    auto fetch = [&](int64_t t) {
+        kin.fetch(k, t, steps(t));
+        vin.fetch(v, t, steps(t));
+        if (OUT) qin.fetch(q, t, steps(t));
+    };
+    if (t0 < t1) {
+        if (S::VEC) {
+            for (int ahead = 0; ahead < kStages - 1; ++ahead)
+                if (t0 + ahead * C < t1) send(t0 + ahead * C, ahead);
+        } else {
+            fetch(t0);
+        }
     }
-    if (t0 < t1) fetch(t0);
-    __syncthreads();
-    uint32_t chunk = 1;
-    for (int64_t t = t0; t < t1; t += C, ++chunk) {
-        const int n = static_cast<int>(min(int64_t(C), t1 - t)), turn = chunk % 2;
-        T *const Ks = tiles + (kStages == 2 ? turn : 0) * kTiles, *const Vs = Ks + C * S::kp, *const Qs = Vs + C * S::vp;
-        if (OUT)
-            vin.clean([&](int row, int c) {
-                atomicMax(&reached[turn][c], chunk * (C + 1) + (C - row));
-                odd_chunk[turn] = chunk;          // alike from every thread that finds one
-            });
-        if (kStages == 1) __syncthreads();
-        kin.store(Ks, S::kp);
-        vin.store(Vs, S::vp);
-        if (OUT) qin.store(Qs, S::kp);
-        __syncthreads();                          // who reads the other half has read it
-        if (t + C < t1) fetch(t + C);
-        const bool odd = OUT && odd_chunk[turn] == chunk;
+    int stage = 0, last_stage = kStages - 1;
+    for (int64_t t = t0; t < t1; t += C) {
+        const int n = steps(t);
+        const unsigned char *const Ks = smem + stage * kTiles, *const Vs = Ks + S::Keys::kBytes, *const Qs = Vs + S::Values::kBytes;
+        if constexpr (S::VEC) {
+            // What is under way behind this chunk's loads may stay so: those of the next
+            // chunk and the outputs of the one before, which were sent after them.  Then
+            // every wave has read the stage that the next loads go to.
+            if constexpr (kStages == 1) {
+                wait_and_meet<0>();
+                send(t, 0);
+                wait_and_meet<0>();
+            } else {
+                if (kStages == 2 || t + C >= t1) wait_and_meet<0>();
+                else if (t == t0) wait_and_meet<kLoads>();
+                else wait_and_meet<kLoads + kStores>();
+                if (t + (kStages - 1) * C < t1) send(t + (kStages - 1) * C, last_stage);
+            }
+        } else {
+            unsigned char *const to = smem + stage * kTiles;
+            if (kStages == 1) __syncthreads();
+            kin.store(to);
+            vin.store(to + S::Keys::kBytes);
+            if (OUT) qin.store(to + S::Keys::kBytes + S::Values::kBytes);
+            __syncthreads();                      // who reads the other stage has read it
+            if (t + C < t1) fetch(t + C);
+        }
+        last_stage = stage;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
         if (n < C) {                              // the last chunk
             whole = power(n);
 #pragma unroll
             for (int j = 0; j < 16; ++j) weight[j] = w.inner * power(max(n - e - acc_row(j) - 4 * half, 0));
         }
 
+        // The products leave out later inputs by a factor 0, which an infinite or NaN v
+        // would carry to earlier outputs of its chunk.  Such values are taken out, and what
+        // they reach is set to NaN: their column from their step on.
         Frag vf[CS];
+        bool odd = false;
+        int reached = C;                          // first such step of this lane's column
 #pragma unroll
-        for (int s = 0; s < CS; ++s) vf[s] = load_col(Vs + 16 * s * S::vp + 32 * wave, S::vp, lane);
+        for (int s = 0; s < CS; ++s) {
+            vf[s] = load_col<typename S::Values>(Vs, 16 * s, 32 * wave, lane, T());
+            odd |= any_odd(vf[s]);
+        }
+        if (__any(odd)) {
+#pragma unroll
+            for (int s = CS - 1; s >= 0; --s) reached = clean(vf[s], 16 * s + 4 * half, reached);
+            reached = min(reached, __shfl_xor(reached, 32));
+        }
         if (OUT) {
             f32x16 G, O;
 #pragma unroll
@@ -433,8 +516,8 @@ __global__ __launch_bounds__(S::threads, S::KP <= 64 || (S::KP <= 128 && sizeof(
             // of each of its values, like the rounding of the output.
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const Frag qf = load_row(Qs + col * S::kp + 16 * s + 8 * half);
-                mma(G, load_row(Ks + col * S::kp + 16 * s + 8 * half), qf);
+                const Frag qf = load_row<typename S::Keys>(Qs, col, 16 * s + 8 * half, T());
+                mma(G, load_row<typename S::Keys>(Ks, col, 16 * s + 8 * half, T()), qf);
                 mma(O, from_acc<Frag>(X[s / 2], s % 2), qf);
             }
 #pragma unroll
@@ -444,33 +527,30 @@ __global__ __launch_bounds__(S::threads, S::KP <= 64 || (S::KP <= 128 && sizeof(
             for (int j = 0; j < 16; ++j) G[j] = acc_row(j) + 4 * half <= col ? G[j] * inside[j] : 0.0f;
 #pragma unroll
             for (int s = 0; s < CS; ++s) mma(O, vf[s], from_acc<Frag>(G, s));
+            if (__any(odd)) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) O[j] *= w.scale;
-            if (odd) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint32_t r = reached[turn][32 * wave + 16 * (j / 8) + 8 * half + j % 8];
-                    if (r / (C + 1) == chunk && col >= static_cast<int>(C - r % (C + 1))) O[j] = __builtin_nanf("");
-                }
+                for (int j = 0; j < 16; ++j)
+                    if (col >= __shfl(reached, acc_row(j) + 4 * half)) O[j] = __builtin_nanf("");
             }
-            if (col < n) {
+            float out[16];
 #pragma unroll
-                for (int s = 0; s < CS; ++s) {
-                    float out[8];
+            for (int j = 0; j < 16; ++j) out[j] = O[j] * w.scale;
+            if constexpr (S::VEC) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) out[j] = O[8 * s + j];
-                    store8(o + 16 * s, out, width - (32 * wave + 16 * s + 8 * half));
-                }
+                for (int s = 0; s < CS; ++s) store_vectors(o, t, n, col, my_out + 16 * s, out + 8 * s);
+            } else if (col < n) {
+                T *const to = o.p + (t + col) * o.ld + my_out;
+#pragma unroll
+                for (int s = 0; s < CS; ++s) store8(to + 16 * s, out + 8 * s, width - my_out - 16 * s);
             }
-            o += sign * C * ldb;
         }
         // The state: k_j exact, its partner g^(n-e-j) v_j in bfloat16 as the sum of two
         // roundings, which hold it to 2^-16.
-        if (odd && reached[turn][32 * wave + column_of(col)] / (C + 1) == chunk) whole = __builtin_nanf("");
+        const float f = reached < C ? __builtin_nanf("") : whole;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) X[kb][j] *= whole;
+            for (int j = 0; j < 16; ++j) X[kb][j] *= f;
 #pragma unroll
         for (int s = 0; s < CS; ++s) {
             Frag up, rest;
@@ -482,7 +562,7 @@ __global__ __launch_bounds__(S::threads, S::KP <= 64 || (S::KP <= 128 && sizeof(
             }
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                const Frag a = load_col(Ks + 16 * s * S::kp + 32 * kb, S::kp, lane);
+                const Frag a = load_col<typename S::Keys>(Ks, 16 * s, 32 * kb, lane, T());
                 mma(X[kb], a, up);
                 if (sizeof(T) == 2) mma(X[kb], a, rest);
             }
@@ -521,39 +601,37 @@ __global__ __launch_bounds__(256) void attention_fold_kernel(const Walks W) {
     const int64_t a = id / w.B, c = id % w.B;
     float x = w.first ? w.first[bh * states + a * w.first_sa + c * w.first_sb] : 0.0f;
     float *p = w.segments + (b * (W.segments - 1) * W.heads + h) * states + a * w.seg_sa + c * w.seg_sb;
-    for (int64_t s = 0; s < full; ++s, p += W.heads * states) {
-        x = fmaf(g, x, *p);
-        *p = x;
+    const int64_t next = W.heads * states;
+    for (int64_t s = 0; s < full; s += 8, p += 8 * next) {
+        float local[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) local[i] = s + i < full ? p[i * next] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x = fmaf(g, x, local[i]);
+            if (s + i < full) p[i * next] = x;
+        }
     }
 }
 
 // ---- launches ------------------------------------------------------------------
 
-constexpr int kTarget = 512;   // workgroups to aim at
-
 int waves_of(int64_t B) { return B <= 64 ? 2 : 4; }
 int slices_of(int64_t B) { return static_cast<int>((B + 32 * waves_of(B) - 1) / (32 * waves_of(B))); }
 
-// Segments of a sequence and their steps.
+constexpr int64_t kSlots = 512;   // workgroups that the device holds at once
+
+// Segments of a sequence and their steps: as many as give every compute unit two
+// workgroups of the forward, all at once.
 void cut(const AttentionArgs &a, bool bwd, int *segments, int64_t *steps) {
-    const int64_t least = 8 * C;
-    const int64_t walks = a.seqs * a.heads * slices_of(a.value);
-    const int64_t want = std::max<int64_t>(1, (kTarget + walks - 1) / std::max<int64_t>(1, walks));
-    const int64_t n = std::max<int64_t>(1, std::min(want, a.seqlen / least));
-    *steps = ((a.seqlen + n - 1) / n + C - 1) / C * C;
-    *segments = *steps > 0 ? static_cast<int>((a.seqlen + *steps - 1) / *steps) : 1;
-    if (*segments < 1) *segments = 1;
-    if (*steps < C) *steps = C;
+    const int64_t walks = std::max<int64_t>(1, a.seqs * a.heads * slices_of(a.value));
+    const int64_t n = std::max<int64_t>(1, std::min((bwd ? kSlots / 2 : kSlots) / walks, a.seqlen / (4 * C)));
+    *steps = std::max<int64_t>(C, ((a.seqlen + n - 1) / n + C - 1) / C * C);
+    *segments = static_cast<int>(std::max<int64_t>(1, (a.seqlen + *steps - 1) / *steps));
 }
 
 template <typename S, bool OUT>
-hipError_t launch_walks(Walks W, hipStream_t stream) {
-    for (Walk &w : W.w) {
-        const auto whole = [](const void *p, int width) {
-            return reinterpret_cast<uintptr_t>(p) % 16 == 0 && width % S::E == 0;
-        };
-        w.vectors = whole(w.q, w.A) | whole(w.k, w.A) << 1 | whole(w.v, w.B) << 2;
-    }
+hipError_t launch_walks(const Walks &W, hipStream_t stream) {
     int most = 0;
     for (int i = 0; i < W.count; ++i) most = std::max(most, W.w[i].slices);
     const int64_t n = W.seqs * W.segments * W.heads * most * W.count;
@@ -566,39 +644,56 @@ hipError_t launch_walks(Walks W, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename T, bool OUT>
-hipError_t launch_group(const Walks &W, int64_t A, int waves, hipStream_t stream) {
-    if (waves == 2) {
-        if (A <= 64) return launch_walks<Shape<T, 64, 2>, OUT>(W, stream);
-        if (A <= 128) return launch_walks<Shape<T, 128, 2>, OUT>(W, stream);
-        return launch_walks<Shape<T, 256, 2>, OUT>(W, stream);
-    }
-    if (A <= 64) return launch_walks<Shape<T, 64, 4>, OUT>(W, stream);
-    if (A <= 128) return launch_walks<Shape<T, 128, 4>, OUT>(W, stream);
-    return launch_walks<Shape<T, 256, 4>, OUT>(W, stream);
+// What instantiates the kernel for a walk: A rounded up, waves, whole vectors.
+struct Kind {
+    int keys, waves;
+    bool vec;
+    bool operator==(const Kind &k) const { return keys == k.keys && waves == k.waves && vec == k.vec; }
+};
+
+template <bool OUT>
+Kind kind_of(const Walk &w, int size) {
+    const auto p = [](const void *a) { return reinterpret_cast<uintptr_t>(a); };
+    const uintptr_t at = p(w.k) | p(w.v) | (OUT ? p(w.q) | p(w.o) : 0);
+    return Kind{w.A <= 64 ? 64 : w.A <= 128 ? 128 : 256, waves_of(w.B), (at | (w.A | w.B) * size) % 16 == 0};
 }
 
-// Walks of one shape share a launch.
-template <bool OUT>
-hipError_t launch_all(const Walks &W, bool f32, hipStream_t stream) {
-    auto shape = [](const Walk &w) { return (w.A <= 64 ? 0 : w.A <= 128 ? 1 : 2) * 2 + (waves_of(w.B) == 4); };
+template <typename T, bool OUT, bool VEC>
+hipError_t launch_group(const Walks &W, const Kind &k, hipStream_t stream) {
+    if (k.waves == 2) {
+        if (k.keys == 64) return launch_walks<Shape<T, 64, 2, VEC>, OUT>(W, stream);
+        if (k.keys == 128) return launch_walks<Shape<T, 128, 2, VEC>, OUT>(W, stream);
+        return launch_walks<Shape<T, 256, 2, VEC>, OUT>(W, stream);
+    }
+    if (k.keys == 64) return launch_walks<Shape<T, 64, 4, VEC>, OUT>(W, stream);
+    if (k.keys == 128) return launch_walks<Shape<T, 128, 4, VEC>, OUT>(W, stream);
+    return launch_walks<Shape<T, 256, 4, VEC>, OUT>(W, stream);
+}
+
+// Walks of one kind share a launch.
+template <typename T, bool OUT>
+hipError_t launch_all(const Walks &W, hipStream_t stream) {
     bool done[3] = {false, false, false};
     for (int i = 0; i < W.count; ++i) {
         if (done[i]) continue;
+        const Kind kind = kind_of<OUT>(W.w[i], sizeof(T));
         Walks G = W;
         G.count = 0;
         for (int j = i; j < W.count; ++j)
-            if (!done[j] && shape(W.w[j]) == shape(W.w[i])) {
+            if (!done[j] && kind_of<OUT>(W.w[j], sizeof(T)) == kind) {
                 G.w[G.count++] = W.w[j];
                 done[j] = true;
             }
         for (int j = G.count; j < 3; ++j) G.w[j] = G.w[0];
-        const int waves = waves_of(G.w[0].B);
-        const hipError_t e = f32 ? launch_group<float, OUT>(G, G.w[0].A, waves, stream)
-                                 : launch_group<uint16_t, OUT>(G, G.w[0].A, waves, stream);
-        if (e != hipSuccess) return e;
+        if (const hipError_t e = kind.vec ? launch_group<T, OUT, true>(G, kind, stream) : launch_group<T, OUT, false>(G, kind, stream))
+            return e;
     }
     return hipSuccess;
+}
+
+template <bool OUT>
+hipError_t launch_all(const Walks &W, bool f32, hipStream_t stream) {
+    return f32 ? launch_all<float, OUT>(W, stream) : launch_all<uint16_t, OUT>(W, stream);
 }
 
 Walks common(const AttentionArgs &a, bool bwd) {
@@ -710,7 +805,7 @@ hipError_t launch_linear_attention_fwd(const AttentionArgs &a, void *workspace, 
     const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
     W.count = 1;
     W.w[0] = Walk{a.q, a.k, a.v, a.o, a.h0, a.h_last, static_cast<float *>(ws), V, 1, V, 1, V, 1, K, V,
-                  slices_of(V), 1, 0, 0, 1.0f, a.scale};
+                  slices_of(V), 1, 0, 1.0f, a.scale};
     hipError_t e = hipSuccess;
     if (W.segments > 1) {
         e = launch_all<false>(W, a.io == IO_F32, stream);
@@ -733,9 +828,9 @@ hipError_t launch_linear_attention_bwd(const AttentionArgs &a, void *workspace, 
     const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
     float *S = static_cast<float *>(ws), *R = S + bytes / 2 / sizeof(float);
     // S^T in (V, K) as the first walk forms it; R in (K, V) as the third does
-    const Walk dq{a.dout, a.v, a.k, a.dq, a.h0, nullptr, S, 1, V, 0, 0, K, 1, V, K, slices_of(K), 1, 0, 0, 1.0f, a.scale};
-    const Walk dk{a.v, a.dout, a.q, a.dk, a.dh_last, nullptr, R, 1, V, 0, 0, 1, V, V, K, slices_of(K), 0, 1, 0, a.scale, 1.0f};
-    const Walk dv{a.k, a.q, a.dout, a.dv, a.dh_last, a.dh0, R, V, 1, V, 1, V, 1, K, V, slices_of(V), 0, 1, 0, a.scale, 1.0f};
+    const Walk dq{a.dout, a.v, a.k, a.dq, a.h0, nullptr, S, 1, V, 0, 0, K, 1, V, K, slices_of(K), 1, 0, 1.0f, a.scale};
+    const Walk dk{a.v, a.dout, a.q, a.dk, a.dh_last, nullptr, R, 1, V, 0, 0, 1, V, V, K, slices_of(K), 0, 1, a.scale, 1.0f};
+    const Walk dv{a.k, a.q, a.dout, a.dv, a.dh_last, a.dh0, R, V, 1, V, 1, V, 1, K, V, slices_of(V), 0, 1, a.scale, 1.0f};
     hipError_t e = hipSuccess;
     if (W.segments > 1) {
         W.count = 2;
