@@ -11,9 +11,9 @@
 //
 // What can be left out is found by bisection: t is the largest number that `count` of
 // the lanes' maxima reach, and a wave counts them with one comparison and one scalar
-// population count a bit.  Few words beyond `count` reach t; where more than 64 do
-// (equal logits), the bisection goes over all of them, with the word as the last
-// digits, so that it ends with exactly `count`.
+// population count a bit; the sixteen high bits do, and few words beyond `count` reach t.
+// Where too many do (equal logits), the bisection goes over all of them, with the word
+// as the last digits, so that it ends with exactly `count`.
 //
 // A beam without values (its score or its lse not finite) counts as -infinity for
 // every word, which its lowest words then stand for.
@@ -22,6 +22,7 @@
 // moved beams come from before it writes any, so rows change places inside the
 // buffer, and beams that stay cost nothing.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_math.h"
 #include "internal.h"
@@ -38,13 +39,13 @@ constexpr int kWaves = 4;                       // of a workgroup of the first l
 constexpr int kThreads = 64 * kWaves;
 constexpr int kPiece = kThreads * kItems;       // words of a workgroup
 constexpr int kKeep = 64;                       // words that a piece leaves at most
+constexpr int kList = 256;                      // keys of a wave's list in LDS
 static_assert(MSSM_MAX_BEAM_COUNT <= kKeep, "a piece keeps all that are asked for");
 
 // What a piece leaves.
 struct Piece {
-    float top, sum;     // maximum, sum of exp(logit - maximum)
-    int count, unused;
-    uint64_t key[kKeep];
+    float top, sum;            // maximum, sum of exp(logit - maximum)
+    uint64_t key[kKeep];       // 0: none
 };
 
 // Order of floats as unsigned numbers (-0 and 0 are one), and a key that falls with the
@@ -59,16 +60,27 @@ __device__ __forceinline__ uint64_t key_of(uint32_t order, int word) {
 }
 __device__ __forceinline__ int word_of(uint64_t key) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)); }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+// A value of all lanes joined by f, the same in all of them.
+template <typename F>
+__device__ __forceinline__ float wave_join(float x, F f) {
+    const auto dpp = [](float v, auto ctrl) {
+        return __builtin_bit_cast(
+            float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    x = f(x, dpp(x, std::integral_constant<int, 0xb1>()));    // quad_perm 1 0 3 2
+    x = f(x, dpp(x, std::integral_constant<int, 0x4e>()));    // quad_perm 2 3 0 1
+    x = f(x, dpp(x, std::integral_constant<int, 0x141>()));   // halves of 8 mirrored
+    x = f(x, dpp(x, std::integral_constant<int, 0x140>()));   // rows of 16 mirrored
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return f(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
-template <typename V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-    return v;
+__device__ __forceinline__ float wave_max(float v) {
+    return wave_join(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    return wave_join(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ int lanes_before(uint64_t mask) {
     return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
@@ -82,46 +94,62 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The largest t that at least `count` lanes' values reach; 0 if fewer hold any.
-template <typename U>
+// The largest t of multiples of 2^LOW that at least `count` lanes' values reach; 0 if
+// fewer hold any.
+template <int LOW, typename U>
 __device__ __forceinline__ U reached_by(U mine, int count) {
     U t = 0;
-    for (int bit = 8 * sizeof(U) - 1; bit >= 0; --bit) {
+#pragma unroll 4
+    for (int bit = 8 * sizeof(U) - 1; bit >= LOW; --bit) {
         const U with = t | U(1) << bit;
         if (__popcll(__ballot(mine >= with)) >= count) t = with;
     }
     return t;
 }
 
-// Keeps of the n keys at `list` (LDS, one wave's own, in any order) those among which
-// the `count` largest are, at most kKeep; returns how many.
-__device__ int reduce(uint64_t *list, int n, int count) {
-    const int lane = threadIdx.x % 64;
-    if (n <= kKeep) return n;
+// Appends those of the lanes' keys to the n that `list` (a wave's own, in LDS) holds
+// among which the `count` largest are, in any order; returns how many it holds then: at
+// most `room` more, which is `count` or more.
+template <int R>
+__device__ __forceinline__ int append(const uint64_t (&key)[R], uint64_t *list, int n, int count, int room) {
     uint64_t top = 0;
-    for (int i = lane; i < n; i += 64) top = max(top, list[i]);
-    uint64_t t = static_cast<uint64_t>(reached_by(static_cast<uint32_t>(top >> 32), count)) << 32;
+#pragma unroll
+    for (int r = 0; r < R; ++r) top = max(top, key[r]);
+    uint64_t t = static_cast<uint64_t>(reached_by<16>(static_cast<uint32_t>(top >> 32), count)) << 32;
+    t = max(t, uint64_t(1));
     int reach = 0;
-    for (int i = 0; i < n; i += 64) reach += __popcll(__ballot(i + lane < n && list[min(i + lane, n - 1)] >= t));
-    if (reach > kKeep) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) reach += __popcll(__ballot(key[r] >= t));
+    if (reach > room) {
         t = 0;
         for (int bit = 63; bit >= 0; --bit) {
             const uint64_t with = t | uint64_t(1) << bit;
             int found = 0;
-            for (int i = 0; i < n; i += 64) found += __popcll(__ballot(i + lane < n && list[min(i + lane, n - 1)] >= with));
+#pragma unroll
+            for (int r = 0; r < R; ++r) found += __popcll(__ballot(key[r] >= with));
             if (found >= count) t = with;
         }
+        t = max(t, uint64_t(1));
     }
-    int kept = 0;
-    for (int i = 0; i < n; i += 64) {   // never ahead of what is still to be read
-        const uint64_t key = i + lane < n ? list[i + lane] : 0;
-        const bool keep = i + lane < n && key >= t;
-        const uint64_t mask = __ballot(keep);
-        if (keep) list[kept + lanes_before(mask)] = key;
-        kept += __popcll(mask);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint64_t mask = __ballot(key[r] >= t);
+        if (key[r] >= t) list[n + lanes_before(mask)] = key[r];
+        n += __popcll(mask);
     }
     wave_sync();
-    return kept;
+    return n;
+}
+
+// The same of the n <= kList keys that the list holds, to at most kKeep.
+__device__ __forceinline__ int reduce(uint64_t *list, int n, int count) {
+    if (n <= kKeep) return n;
+    const int lane = threadIdx.x % 64;
+    uint64_t key[kList / 64];
+#pragma unroll
+    for (int r = 0; r < kList / 64; ++r) key[r] = 64 * r + lane < n ? list[64 * r + lane] : 0;
+    wave_sync();
+    return append(key, list, 0, count, kKeep);
 }
 
 // Four consecutive logits, at any element's address.
@@ -140,7 +168,7 @@ __device__ __forceinline__ void load4(const uint16_t *p, float *v) {
 template <typename T>
 __global__ __launch_bounds__(kThreads) void beam_pieces_kernel(const T *__restrict__ logits, Piece *__restrict__ out,
                                                                int vocab, int count, int pieces) {
-    __shared__ uint64_t list[kWaves * 64 * kItems];
+    __shared__ uint64_t lists[kWaves * kList];
     __shared__ float tops[kWaves], sums[kWaves];
     __shared__ int counts[kWaves];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -159,12 +187,9 @@ __global__ __launch_bounds__(kThreads) void beam_pieces_kernel(const T *__restri
             for (int i = 0; i < 4; ++i) v[j + i] = word(j + i) < vocab ? Io<T>::load(logits, word(j + i)) : kLow;
         }
     }
-    uint32_t mine = 0;
 #pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-        top = fmaxf(top, v[j]);
-        if (word(j) < vocab) mine = max(mine, ordered(v[j] != v[j] ? kLow : v[j]));
-    }
+    for (int j = 0; j < kItems; ++j) top = fmaxf(top, v[j]);   // passes over NaN
+    const float mine = top;
     top = wave_max(top);
     float sum = 0.0f;                       // 0 without finite logits, NaN with +infinity or NaN
     const float base = top == kLow ? 0.0f : top;
@@ -172,18 +197,31 @@ __global__ __launch_bounds__(kThreads) void beam_pieces_kernel(const T *__restri
     for (int j = 0; j < kItems; ++j) sum += fast_exp2((v[j] - base) * kLog2e);
     sum = wave_sum(sum);
 
-    uint64_t *const own = list + wave * 64 * kItems;
-    const uint32_t t = reached_by(mine, count);
+    uint64_t *const own = lists + wave * kList;
+    // A lane that holds nothing above -infinity counts as less than all that do.
+    const uint32_t t = reached_by<16>(ordered(mine), count);
+    const float limit = unordered(t);
     int n = 0;
+    if (limit > kLow) {
 #pragma unroll
-    for (int j = 0; j < kItems; ++j) {
-        const uint32_t order = ordered(v[j] != v[j] ? kLow : v[j]);
-        const bool keep = word(j) < vocab && order >= t;
-        const uint64_t mask = __ballot(keep);
-        if (keep) own[n + lanes_before(mask)] = key_of(order, word(j));
-        n += __popcll(mask);
+        for (int j = 0; j < kItems; ++j) n += __popcll(__ballot(v[j] >= limit));
     }
-    wave_sync();
+    if (n > 0 && n <= kList) {
+        n = 0;
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            const uint64_t mask = __ballot(v[j] >= limit);
+            if (v[j] >= limit) own[n + lanes_before(mask)] = key_of(ordered(v[j]), word(j));
+            n += __popcll(mask);
+        }
+        wave_sync();
+    } else {                                // words at -infinity are asked for, or very many are equal
+        uint64_t key[kItems];
+#pragma unroll
+        for (int j = 0; j < kItems; ++j)
+            key[j] = word(j) < vocab ? key_of(ordered(v[j] != v[j] ? kLow : v[j]), word(j)) : 0;
+        n = append(key, own, 0, count, kList);
+    }
     n = reduce(own, n, count);
     if (lane == 0) {
         tops[wave] = top;
@@ -192,17 +230,14 @@ __global__ __launch_bounds__(kThreads) void beam_pieces_kernel(const T *__restri
     }
     __syncthreads();
     if (wave > 0) return;
-    // the waves' lists side by side, then the same once more
-    int total = counts[0];
-    for (int w = 1; w < kWaves; ++w) {
-        const uint64_t key = lane < counts[w] ? list[w * 64 * kItems + lane] : 0;
-        if (lane < counts[w]) list[total + lane] = key;
-        total += counts[w];
-    }
+    // the same of what the waves left
+    uint64_t left[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) left[w] = lane < counts[w] ? lists[w * kList + lane] : 0;
     wave_sync();
-    total = reduce(list, total, count);
+    const int total = append(left, lists, 0, count, kKeep);
     Piece &p = out[blockIdx.x];
-    if (lane < total) p.key[lane] = list[lane];
+    p.key[lane] = lane < total ? lists[lane] : 0;
     const float my_top = lane < kWaves ? tops[lane] : kLow, all = wave_max(my_top);
     float part = 0.0f;
     if (lane < kWaves && sums[lane] != 0.0f) part = sums[lane] * fast_exp2((my_top - all) * kLog2e);
@@ -210,66 +245,108 @@ __global__ __launch_bounds__(kThreads) void beam_pieces_kernel(const T *__restri
     if (lane == 0) {
         p.top = all;
         p.sum = part;
-        p.count = total;
     }
 }
 
-// A workgroup per batch entry, a wave at a time per beam.  LDS: for every beam kKeep
-// values and words; for every wave a list.
-constexpr int kMergeWaves = 4, kMergeList = 9 * kKeep;
+// A workgroup per batch entry, a wave at a time per beam.
+constexpr int kMergeWaves = 8, kMergeThreads = 64 * kMergeWaves;
+constexpr int kTogether = 16;    // pieces that a lane loads at once
 
-__global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(
+// A float64 as an unsigned number of the same order, for values without NaN; -0 does not occur.
+__device__ __forceinline__ uint64_t ordered(double v) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+    return b >> 63 ? ~b : b | uint64_t(1) << 63;
+}
+
+struct __attribute__((aligned(16))) Candidate {
+    double value;
+    uint64_t place;     // beam and word
+};
+
+__global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     const Piece *__restrict__ in, const float *__restrict__ scores, float *__restrict__ out_scores,
     int64_t *__restrict__ out_tokens, int64_t *__restrict__ out_beams, int beams, int vocab, int count, int pieces) {
-    __shared__ uint64_t lists[kMergeWaves * kMergeList];
-    __shared__ double value[MSSM_MAX_BEAMS * kKeep];
-    __shared__ int64_t flat[MSSM_MAX_BEAMS * kKeep];
+    __shared__ uint64_t lists[kMergeWaves * kList];
+    __shared__ Candidate all[MSSM_MAX_BEAMS * kKeep];
     __shared__ int total;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int64_t entry = blockIdx.x;
     const double kLow = -__builtin_inf();
-    uint64_t *const list = lists + wave * kMergeList;
+    uint64_t *const list = lists + wave * kList;
     if (threadIdx.x == 0) total = 0;
     __syncthreads();
     for (int j = wave; j < beams; j += kMergeWaves) {
         const int64_t row = entry * beams + j;
         const Piece *const mine = in + row * pieces;
-        float top = -__builtin_inff();
-        for (int s = lane; s < pieces; s += 64) top = fmaxf(top, mine[s].top);
-        top = wave_max(top);
-        double sum = 0.0;
-        for (int s = lane; s < pieces; s += 64)
-            if (mine[s].sum != 0.0f) sum += mine[s].sum * exp(static_cast<double>(mine[s].top) - top);
-        const double lse = top + log(wave_sum(sum)), score = scores[row];
-        const bool live = fabs(lse) < __builtin_inf() && fabs(score) < __builtin_inf();
-        int n = live ? 0 : min(count, vocab);
-        for (int s = 0; live && s < pieces; ++s) {
-            const int more = mine[s].count;
-            if (lane < more) list[n + lane] = mine[s].key[lane];
-            n += more;
-            wave_sync();
-            if (n > kMergeList - kKeep || s == pieces - 1) n = reduce(list, n, count);
+        const float score32 = scores[row];
+        const bool few = pieces <= 64;
+        const float2 first = lane < pieces ? *reinterpret_cast<const float2 *>(&mine[lane].top) : float2{-__builtin_inff(), 0.0f};
+        int n = 0;
+        for (int s = 0; s < pieces; s += kTogether) {
+            // a piece's keys lie in its first places: turned, so that all lanes receive some
+            uint64_t key[kTogether];
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i)
+                key[i] = s + i < pieces ? mine[s + i].key[(lane + i * (64 / kTogether)) % 64] : 0;
+            n = reduce(list, append(key, list, n, count, kList - n), count);
         }
+        float top = first.x;
+        for (int s = 64 + lane; !few && s < pieces; s += 64) top = fmaxf(top, mine[s].top);
+        top = wave_max(top);
+        double sum = first.y != 0.0f ? static_cast<double>(first.y) * expf(first.x - top) : 0.0;
+        for (int s = 64 + lane; !few && s < pieces; s += 64)
+            if (mine[s].sum != 0.0f) sum += static_cast<double>(mine[s].sum) * expf(mine[s].top - top);
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+        const double lse = top + log(sum), score = score32;
+        const bool live = fabs(lse) < __builtin_inf() && fabs(score) < __builtin_inf();
+        if (!live) n = min(count, vocab);
         int at = 0;
         if (lane == 0) at = atomicAdd(&total, n);      // where, not in which order they rank
         at = __shfl(at, 0);
         if (lane < n) {
             const uint64_t key = live ? list[lane] : 0;
             const int word = live ? word_of(key) : lane;
-            value[at + lane] = live ? score + (unordered(static_cast<uint32_t>(key >> 32)) - lse) : kLow;
-            flat[at + lane] = static_cast<int64_t>(j) * vocab + word;
+            all[at + lane] = Candidate{live ? score + (unordered(static_cast<uint32_t>(key >> 32)) - lse) : kLow,
+                                       static_cast<uint64_t>(j) << 32 | static_cast<uint32_t>(word)};
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < total; i += 64 * kMergeWaves) {
-        const double mine = value[i];
-        const int64_t place = flat[i];
+    // Every value's rank is how many come before it; of many, those below what `count` of a
+    // wave's lanes reach are left out first.
+    const int n = total;
+    uint64_t t = 0;
+    if (n > kMergeThreads / 2) {
+        uint64_t best = 0;
+        for (int i = lane; i < n; i += 64) best = max(best, ordered(all[i].value));
+        t = reached_by<0>(best, count);
+        __syncthreads();
+        if (threadIdx.x == 0) total = 0;
+        __syncthreads();
+        constexpr int kEach = MSSM_MAX_BEAMS * kKeep / kMergeThreads;
+        Candidate c[kEach];
+#pragma unroll
+        for (int r = 0; r < kEach; ++r)
+            if (r * kMergeThreads + static_cast<int>(threadIdx.x) < n) c[r] = all[r * kMergeThreads + threadIdx.x];
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kEach; ++r)
+            if (r * kMergeThreads + static_cast<int>(threadIdx.x) < n && ordered(c[r].value) >= t) all[atomicAdd(&total, 1)] = c[r];
+        __syncthreads();
+    }
+    const int left = total;
+    for (int i = threadIdx.x; i < left; i += kMergeThreads) {
+        const Candidate mine = all[i];
         int rank = 0;
-        for (int k = 0; k < total; ++k) rank += value[k] > mine || (value[k] == mine && flat[k] < place);
+#pragma unroll 8
+        for (int k = 0; k < left; ++k) {
+            const Candidate c = all[k];
+            rank += (c.value > mine.value) | ((c.value == mine.value) & (c.place < mine.place));
+        }
         if (rank < count) {
-            out_scores[entry * count + rank] = static_cast<float>(mine);
-            out_tokens[entry * count + rank] = place % vocab;
-            out_beams[entry * count + rank] = place / vocab;
+            out_scores[entry * count + rank] = static_cast<float>(mine.value);
+            out_tokens[entry * count + rank] = static_cast<uint32_t>(mine.place);
+            out_beams[entry * count + rank] = static_cast<int64_t>(mine.place >> 32);
         }
     }
 }
@@ -353,7 +430,7 @@ hipError_t launch_beam_select(const BeamArgs &a, void *workspace, hipStream_t st
         hipLaunchKernelGGL(beam_pieces_kernel<uint16_t>, grid, dim3(kThreads), 0, stream,
                            static_cast<const uint16_t *>(a.logits), static_cast<Piece *>(ws), vocab, count,
                            static_cast<int>(pieces));
-    hipLaunchKernelGGL(beam_merge_kernel, dim3(static_cast<uint32_t>(a.batch)), dim3(64 * kMergeWaves), 0, stream,
+    hipLaunchKernelGGL(beam_merge_kernel, dim3(static_cast<uint32_t>(a.batch)), dim3(kMergeThreads), 0, stream,
                        static_cast<const Piece *>(ws), a.scores, a.out_scores, a.out_tokens, a.out_beams,
                        static_cast<int>(a.beams), vocab, count, static_cast<int>(pieces));
     hipError_t e = hipGetLastError();
