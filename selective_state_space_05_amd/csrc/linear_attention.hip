@@ -15,11 +15,11 @@
 //   dv_t = R_t^T k_t         roles (k, q, do), state R, against time, e = 0
 //   dh0  = g R_0             the state behind the last walk
 //
-// Few sequences and heads are cut into segments of whole chunks: a first launch
-// walks the segments for their states alone, a second folds them,
-//   X_{s+1} = g^T X_s + local_s,
-// and the third walks every segment from the state in front of it.  Everything is
-// summed in an order that depends on the sizes alone.
+// Few sequences and heads are cut into segments of whole chunks, which are walked side
+// by side: a first launch walks them for their states alone, a second folds these,
+//   X_{s+1} = g^n X_s + sum_s  (n steps a segment),
+// and the third walks every segment from the state in front of it.  Everything is summed
+// in an order that depends on the sizes alone.
 #include <algorithm>
 #include <type_traits>
 
@@ -64,12 +64,49 @@ __device__ __forceinline__ float get(const F8 &f, int j) { return f.f[j]; }
 // are the contraction rows 16 s + 4 h + {0..3, 8..11} of half h.
 __device__ __forceinline__ int acc_row(int e) { return 8 * (e / 4) + e % 4; }
 
+__device__ __forceinline__ void pack(bf16x8 &f, const float *v) {
+    typedef float f32x8 __attribute__((ext_vector_type(8)));
+    f = __builtin_convertvector((f32x8{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}), bf16x8);
+}
+__device__ __forceinline__ void pack(F8 &f, const float *v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.f[j] = v[j];
+}
 template <typename F>
 __device__ __forceinline__ F from_acc(const f32x16 &c, int s) {
-    F f;
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) set(f, j, c[8 * s + j]);
+    for (int j = 0; j < 8; ++j) v[j] = c[8 * s + j];
+    F f;
+    pack(f, v);
     return f;
+}
+
+// Which of a fragment's contraction values {0..3, 8..11} are `last` or less, and what
+// leaves the others 0, NaN included.
+template <typename F> struct Mask;
+template <> struct Mask<bf16x8> {
+    u32x4 bits;
+};
+template <> struct Mask<F8> {
+    int last;
+};
+__device__ __forceinline__ Mask<bf16x8> mask_of(const bf16x8 &, int last) {
+    Mask<bf16x8> m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int v = j / 2 * 8 + j % 2 * 2;
+        m.bits[j] = (v <= last ? 0xffffu : 0u) | (v + 1 <= last ? 0xffff0000u : 0u);
+    }
+    return m;
+}
+__device__ __forceinline__ Mask<F8> mask_of(const F8 &, int last) { return Mask<F8>{last}; }
+__device__ __forceinline__ void keep(bf16x8 &f, const Mask<bf16x8> &m) {
+    f = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, f) & m.bits);
+}
+__device__ __forceinline__ void keep(F8 &f, const Mask<F8> &m) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.f[j] = j / 4 * 8 + j % 4 <= m.last ? f.f[j] : 0.0f;
 }
 
 // A tile of C rows of P values in LDS.  Its 16-byte chunks are permuted inside their
@@ -142,18 +179,22 @@ __device__ __forceinline__ F8 load_col(const unsigned char *__restrict__ tile, i
 
 // The infinite and NaN values of a fragment set to 0; the number of the first step that
 // held one, its own steps being `first` + {0..3, 8..11}, or `none`.
-__device__ __forceinline__ bool any_odd(const bf16x8 &f) {
-    const u32x4 v = __builtin_bit_cast(u32x4, f);
-    uint32_t r = 0;
+__device__ __forceinline__ bool any_odd(const bf16x8 &a, const bf16x8 &b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    float r = 0.0f;                          // products with 0: NaN if one is not finite
+    const bf16x2 zero = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r |= (v[j] & 0x7fff7fffu) + 0x00800080u;   // an exponent of all ones carries
-    return r & 0x80008000u;
+    for (int j = 0; j < 8; j += 2) {
+        r = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{a[j], a[j + 1]}, zero, r, false);
+        r = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{b[j], b[j + 1]}, zero, r, false);
+    }
+    return r != 0.0f;
 }
-__device__ __forceinline__ bool any_odd(const F8 &f) {
-    uint32_t r = 0;
+__device__ __forceinline__ bool any_odd(const F8 &a, const F8 &b) {
+    float r = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r |= (__float_as_uint(f.f[j]) & 0x7fffffffu) + 0x00800000u;
-    return r & 0x80000000u;
+    for (int j = 0; j < 8; ++j) r = fmaf(b.f[j], 0.0f, fmaf(a.f[j], 0.0f, r));
+    return r != 0.0f;
 }
 template <typename F>
 __device__ __forceinline__ int clean(F &f, int first, int none) {
@@ -176,7 +217,7 @@ struct Walk {
     void *o;
     const float *first;      // may be null -> 0
     float *last;             // may be null
-    float *segments;         // states of this walk's segments in the workspace
+    float *segments;         // in the workspace: in front of every segment but the first, the state
     int64_t first_sa, first_sb;
     int64_t last_sa, last_sb;
     int64_t seg_sa, seg_sb;  // strides of the workspace's states
@@ -217,58 +258,67 @@ __device__ __forceinline__ float decay_log2(const float *log_decay, int64_t h) {
 }
 
 
-// KP: A rounded up to whole products.  WAVES: 32 columns of B each.  VEC: all rows are
-// whole 16-byte vectors on 16-byte boundaries.
-template <typename T, int KP_, int WAVES_, bool VEC_>
+// KB: blocks of 32 of A.  WAVES: 32 columns of B each.  VEC: all rows are whole 16-byte
+// vectors on 16-byte boundaries.
+template <typename T, int KB_, int WAVES_, bool VEC_>
 struct Shape {
     typedef T Type;
     typedef typename FragOf<T>::type Frag;
     static constexpr bool VEC = VEC_;
-    static constexpr int KP = KP_, WAVES = WAVES_, threads = 64 * WAVES, VP = 32 * WAVES;
-    typedef Tile<T, KP> Keys;
+    static constexpr int KB = KB_, WAVES = WAVES_, threads = 64 * WAVES, VP = 32 * WAVES;
+    typedef Tile<T, KB <= 2 ? 64 : KB <= 4 ? 128 : 256> Keys;
     typedef Tile<T, VP> Values;
-    // bytes of a chunk's tiles in LDS, and how many chunks: loads of whole vectors go
-    // straight to LDS, two chunks ahead where there is room
+    // registers for two waves a SIMD, but for the largest states
+    static constexpr int kWavesASimd = KB <= 2 || (KB <= 4 && sizeof(T) == 2) ? 2 : 1;
+    // Bytes of a chunk's tiles in LDS, and how many chunks: loads of whole vectors go
+    // straight to LDS, up to three chunks ahead where there is room for two workgroups.
     static constexpr int tiles(bool out) { return (out ? 2 : 1) * Keys::kBytes + Values::kBytes; }
     static constexpr int stages(bool out) {
-        const int fit = 160 * 1024 / tiles(out), most = VEC ? 3 : 2;
-        return fit < most ? fit : most;
+        const int fit = 160 * 1024 / kWavesASimd / tiles(out), most = VEC ? 4 : 2;
+        return fit < 1 ? 1 : fit < most ? fit : most;
     }
-    // registers for two waves a SIMD, but for the largest states
-    static constexpr int waves_a_simd(bool) { return KP <= 64 || (KP <= 128 && sizeof(T) == 2) ? 2 : 1; }
     static constexpr int loads(bool out) { return tiles(out) / 1024 / WAVES; }   // of a wave and chunk
-    static constexpr int stores = C * 32 * sizeof(T) / 1024;                     // the same
+    static constexpr int stores = C * 32 * sizeof(T) / 1024;
 };
 
-// The rows of one head of a tensor, in the order that a walk goes over them.
+// The rows of one head of a tensor in the order that a walk goes over them, a chunk at a
+// time: a buffer of its n rows.  Rows past the end lie outside it, behind it or, against
+// time, in front (their offsets are negative, far behind as unsigned ones); they and the
+// columns from `width` on read as zero and are not written.
 template <typename T>
 struct Rows {
-    T *p;                // the head's values in the sequence's first row of the walk
+    T *p;                // the head's values in the walk's first row
     int64_t ld;          // values between rows, negative against time
     int width;
+    unsigned char *next; // lowest row of the next whole chunk
+    int64_t step;        // bytes between chunks
+    int bytes, back;     // between rows; the same against time, else 0
 
-    // A buffer of the n rows of a chunk from row t on: those past the end lie outside it,
-    // behind it or, against time, in front (their offsets are negative, far behind as
-    // unsigned ones), read as zero and are not written.  Offsets are those of offset() plus shift().
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(int64_t t, int n) const {
-        const int bytes = static_cast<int>(ld < 0 ? -ld : ld) * static_cast<int>(sizeof(T));
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<std::remove_const_t<T> *>(p + (t + (ld < 0 ? n - 1 : 0)) * ld), 0,
-                                                 (n - 1) * bytes + width * static_cast<int>(sizeof(T)), 0x00020000);
+    __device__ __forceinline__ Rows(const void *head, int64_t first, int64_t ld_, int64_t sign, int width_)
+        : p(static_cast<T *>(const_cast<void *>(head)) + first * ld_), ld(sign * ld_), width(width_),
+          step(sign * ld_ * C * static_cast<int64_t>(sizeof(T))), bytes(static_cast<int>(ld_) * static_cast<int>(sizeof(T))),
+          back(sign < 0 ? bytes : 0) {}
+    __device__ __forceinline__ void seek(int64_t t) {
+        next = reinterpret_cast<unsigned char *>(p + t * ld) - static_cast<int64_t>(C - 1) * back;
     }
-    __device__ __forceinline__ int shift(int n) const {
-        return ld < 0 ? -(n - 1) * static_cast<int>(ld) * static_cast<int>(sizeof(T)) : 0;
-    }
+    // Offset of a value of a row of a chunk; in a chunk of n rows less missing(n).
     __device__ __forceinline__ int offset(int row, int value) const {
-        return value < width ? (row * static_cast<int>(ld) + value) * static_cast<int>(sizeof(T)) : INT32_MIN;
+        return value >= width ? INT32_MIN : (back ? C - 1 - row : row) * bytes + value * static_cast<int>(sizeof(T));
+    }
+    __device__ __forceinline__ int missing(int n) const { return (C - n) * back; }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(int n) const {
+        return __builtin_amdgcn_make_buffer_rsrc(next + missing(n), 0, (n - 1) * bytes + width * static_cast<int>(sizeof(T)),
+                                                 0x00020000);
     }
 };
 
-// A tile's way from memory: columns from `width` on and rows from n on are 0.
+// A tile's way from memory.
 template <typename S, typename L>
 struct Feed {
     typedef typename S::Type T;
     typedef __attribute__((address_space(3))) void Lds;
     static constexpr int N = L::kBytes / 1024 / S::WAVES;    // instructions of 1024 bytes a wave
+    int off[S::VEC ? N : 1];
     u32x4 r[S::VEC ? 1 : N];
 
     // Row and chunk of this lane's 16 bytes of instruction i.
@@ -278,20 +328,30 @@ struct Feed {
     static __device__ __forceinline__ int chunk(int i) {
         return static_cast<int>(threadIdx.x) % L::kChunks ^ L::swizzle(row(i));
     }
-    // Straight into LDS.
-    static __device__ __forceinline__ void send(const Rows<const T> &R, int64_t t, int n, int wave,
-                                                unsigned char *__restrict__ tile) {
-#if defined(__HIP_DEVICE_COMPILE__)   // with the builtin in it, the host pass leaves out the kernel's handle
-        const auto rsrc = R.buffer(t, n);
-        const int shift = R.shift(n);
+    __device__ __forceinline__ explicit Feed(const Rows<T> &R) {
+        if constexpr (S::VEC)
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds *)(tile + (i * S::WAVES + wave) * 1024), 16,
-                                                     R.offset(row(i), chunk(i) * S::Keys::E) + shift, 0, 0, 0);
+            for (int i = 0; i < N; ++i) off[i] = R.offset(row(i), chunk(i) * L::E);
+    }
+    // Straight into LDS.
+    __device__ __forceinline__ void send(Rows<T> &R, int n, int wave, unsigned char *__restrict__ tile) const {
+#if defined(__HIP_DEVICE_COMPILE__)   // with the builtin in it, the host pass leaves out the kernel's handle
+        const auto rsrc = R.buffer(n);
+        if (n == C) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds *)(tile + (i * S::WAVES + wave) * 1024), 16, off[i], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds *)(tile + (i * S::WAVES + wave) * 1024), 16,
+                                                         off[i] - R.missing(n), 0, 0, 0);
+        }
+        R.next += R.step;
 #endif
     }
     // Through registers, element by element.
-    __device__ __forceinline__ void fetch(const Rows<const T> &R, int64_t t, int n) {
+    __device__ __forceinline__ void fetch(const Rows<T> &R, int64_t t, int n) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             T v[L::E] = {};
@@ -314,24 +374,49 @@ struct Feed {
 // other waves.
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N < 63 ? N : 63) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
 }
 
-// Eight outputs side by side: as whole vectors, or one by one up to `left`.
-__device__ __forceinline__ void store_vectors(const Rows<uint16_t> &o, int64_t t, int n, int row, int value, const float *f) {
-    bf16x8 b;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) b[j] = static_cast<__bf16>(f[j]);
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, b), o.buffer(t, n), o.offset(row, value) + o.shift(n), 0, 0);
+// A wave's outputs: lane l holds columns 8 (l / 32) + {0..7} and those 16 further on of row
+// l % 32.  Lanes swap halves so that one store writes whole 64 or 128 bytes of 16 rows: row
+// 16 i + l % 16, columns out_column(l) + {0..7}.
+__device__ __forceinline__ int out_column(int lane) { return 8 * (lane / 32) + 16 * (lane / 16 % 2); }
+__device__ __forceinline__ void swap_rows(uint32_t &a, uint32_t &b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
 }
-__device__ __forceinline__ void store_vectors(const Rows<float> &o, int64_t t, int n, int row, int value, const float *f) {
+__device__ __forceinline__ void store_vectors(__amdgpu_buffer_rsrc_t to, const int (&off)[2], int missing, const float *f, uint16_t) {
+    bf16x8 x, y;
+    pack(x, f);
+    pack(y, f + 8);
+    u32x4 v[2] = {__builtin_bit_cast(u32x4, x), __builtin_bit_cast(u32x4, y)};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 4; ++j) {
+        uint32_t a = v[0][j], b = v[1][j];
+        swap_rows(a, b);
+        v[0][j] = a;
+        v[1][j] = b;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) __builtin_amdgcn_raw_buffer_store_b128(v[i], to, off[i] - missing, 0, 0);
+}
+// In float32 a lane's eight columns are two vectors, and rows may end between them.
+__device__ __forceinline__ void store_vectors(__amdgpu_buffer_rsrc_t to, const int (&off)[4], int missing, const float *f, float) {
+    uint32_t v[2][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[0][j] = __float_as_uint(f[j]);
+        v[1][j] = __float_as_uint(f[8 + j]);
+        swap_rows(v[0][j], v[1][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
         __builtin_amdgcn_raw_buffer_store_b128(
-            u32x4{__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3])},
-            o.buffer(t, n), o.offset(row, value + 4 * i) + o.shift(n), 0, 0);
+            u32x4{v[i / 2][4 * (i % 2)], v[i / 2][4 * (i % 2) + 1], v[i / 2][4 * (i % 2) + 2], v[i / 2][4 * (i % 2) + 3]}, to,
+            off[i] - missing, 0, 0);
 }
 template <typename T>
 __device__ __forceinline__ void store8(T *p, const float *f, int left) {
@@ -340,43 +425,102 @@ __device__ __forceinline__ void store8(T *p, const float *f, int left) {
         if (j < left) Io<T>::store(p, j, f[j]);
 }
 
-// OUT: the walk with its outputs; else for the segments' states alone.
-template <typename S, bool OUT>
-__global__ __launch_bounds__(S::threads, S::waves_a_simd(OUT)) void attention_walk_kernel(const Walks W) {
+// Workgroups go to the eight XCDs in turn: each gets a run of consecutive positions, so
+// that walks over one head's rows share its L2.
+__device__ __forceinline__ int64_t position() {
+    const int n = gridDim.x, x = blockIdx.x % 8;
+    return static_cast<int64_t>(x) * (n / 8) + min(x, n % 8) + blockIdx.x / 8;
+}
+
+// What a workgroup walks.
+struct Place {
+    int role, slice, seg;
+    int64_t h, b;
+    __device__ __forceinline__ explicit Place(const Walks &W) {
+        int slices = 0;
+        for (int i = 0; i < W.count; ++i) slices = max(slices, W.w[i].slices);
+        // below 2^32: the grid is
+        uint32_t at = static_cast<uint32_t>(position());
+        role = at % W.count;
+        at /= W.count;
+        slice = at % slices;
+        at /= slices;
+        h = at % static_cast<uint32_t>(W.heads);
+        at /= static_cast<uint32_t>(W.heads);
+        seg = at % W.segments;
+        b = at / W.segments;
+    }
+};
+
+// The state of a lane: column column_of(lane % 32) of the wave's 32; element j of block kb
+// is row 32 kb + 16 (j / 8) + 8 (lane / 32) + j % 8.
+__device__ __forceinline__ int state_row(int kb, int j, int half) { return 32 * kb + 16 * (j / 8) + 8 * half + j % 8; }
+
+// Nothing moves over this: left alone, the compiler reads every fragment from LDS just
+// before its product and waits for each.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// X <- g X + (keys)^T (weights * values): the keys exact, their partners in bfloat16 as the
+// sum of two roundings, which hold them to 2^-16.
+template <typename S, typename Frag, int KB>
+__device__ __forceinline__ void advance(f32x16 (&X)[KB], const unsigned char *Ks, const Frag (&vf)[2], const float *weight,
+                                        float g, int lane) {
+    typedef typename S::Type T;
+    constexpr int kAhead = KB < 4 ? KB : 4;          // fragments under way
+    Frag a[kAhead];
+    auto load = [&](int i) { a[i % kAhead] = load_col<typename S::Keys>(Ks, i / KB * 16, i % KB * 32, lane, T()); };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i);
+    in_order();
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) X[kb][j] *= g;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        float u[8];
+        Frag up, rest;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = weight[8 * s + j] * get(vf[s], j);
+        pack(up, u);
+        if (sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] -= get(up, j);
+            pack(rest, u);
+        }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            const int i = s * KB + kb;
+            mma(X[kb], a[i % kAhead], up);
+            if (sizeof(T) == 2) mma(X[kb], a[i % kAhead], rest);
+            if (i + kAhead < 2 * KB) load(i + kAhead);
+            in_order();
+        }
+    }
+}
+
+template <typename S>
+__global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_walk_kernel(const Walks W) {
     typedef typename S::Type T;
     typedef typename S::Frag Frag;
-    constexpr int KB = S::KP / 32, KS = S::KP / 16, CS = C / 16;
+    constexpr int KB = S::KB, KS = 2 * KB;
+    constexpr int kStages = S::stages(true), kTiles = S::tiles(true), kLoads = S::loads(true);
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    constexpr int kStages = S::stages(OUT), kTiles = S::tiles(OUT), kLoads = S::loads(OUT);
-    constexpr int kStores = OUT ? S::stores : 0;
 
-    // workgroups go to the eight XCDs in turn: each gets a run of consecutive
-    // positions, so that the walks over one head's rows share its L2
-    const int n_ids = gridDim.x, x = blockIdx.x % 8;
-    int64_t at = static_cast<int64_t>(x) * (n_ids / 8) + min(x, n_ids % 8) + blockIdx.x / 8;
-    int role = 0;
-    if (W.count > 1) {
-        role = static_cast<int>(at % W.count);
-        at /= W.count;
-    }
-    const Walk &w = W.w[role];
-    const int most = max(max(W.w[0].slices, W.w[1].slices), W.w[2].slices);
-    const int slice = static_cast<int>(at % most);
-    at /= most;
-    const int64_t h = at % W.heads;
-    at /= W.heads;
-    const int seg = static_cast<int>(at % W.segments);
-    const int64_t b = at / W.segments;
-    if (slice >= w.slices) return;
+    const Place at(W);
+    const Walk &w = W.w[at.role];
+    const int seg = at.seg;
+    const int64_t h = at.h, b = at.b;
+    if (at.slice >= w.slices) return;
     int64_t start, len;
     sequence(W, b, &start, &len);
     const int64_t t0 = seg * W.segment;
     const bool tail = seg == W.segments - 1;       // walks to the end, however far
     const int64_t t1 = tail ? len : min(len, t0 + W.segment);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, half = lane / 32, col = lane % 32;
-    const int v0 = slice * S::VP, width = min(S::VP, w.B - v0);
+    const int v0 = at.slice * S::VP, width = min(S::VP, w.B - v0);
 
-    if (OUT && W.cu && ((b == 0 && seg == 0) || (b == W.seqs - 1 && tail))) {
+    if (W.cu && ((b == 0 && seg == 0) || (b == W.seqs - 1 && tail))) {
         // rows in front of the first sequence and behind the last one
         for (int side = 0; side < 2; ++side) {
             if (side == 0 ? !(b == 0 && seg == 0) : !(b == W.seqs - 1 && tail)) continue;
@@ -386,105 +530,114 @@ __global__ __launch_bounds__(S::threads, S::waves_a_simd(OUT)) void attention_wa
                 o[(lo + id / width) * W.heads * w.B + id % width] = T(0);
         }
     }
-    if (OUT ? (t0 >= len && seg > 0) : (tail || t0 + W.segment >= len)) return;   // nothing, or nothing behind it
+    if (t0 >= len && seg > 0) return;
+
+    const int64_t row_first = w.reverse ? start + len - 1 : start, sign = w.reverse ? -1 : 1;
+    const int64_t lda = W.heads * w.A, ldb = W.heads * w.B;
+    Rows<T> q(static_cast<const T *>(w.q) + h * w.A, row_first, lda, sign, w.A);
+    Rows<T> k(static_cast<const T *>(w.k) + h * w.A, row_first, lda, sign, w.A);
+    Rows<T> v(static_cast<const T *>(w.v) + h * w.B + v0, row_first, ldb, sign, width);
+    Rows<T> o(static_cast<const T *>(w.o) + h * w.B + v0, row_first, ldb, sign, width);
+    q.seek(t0);
+    k.seek(t0);
+    v.seek(t0);
+    o.seek(t0);
+    Feed<S, typename S::Keys> kin(k), qin(q);
+    Feed<S, typename S::Values> vin(v);
+    const int my_out = 32 * wave + 8 * half;      // first of the outputs of row col
+    constexpr int kStores = S::stores;
+    int out_off[kStores];                         // of the vectors that this lane stores
+#pragma unroll
+    for (int i = 0; i < kStores; ++i)
+        out_off[i] = o.offset(16 * (2 * i / kStores) + lane % 16, 32 * wave + out_column(lane) + (kStores == 4 ? 4 * (i % 2) : 0));
+    const int count = static_cast<int>((t1 - t0 + C - 1) / C), n_last = static_cast<int>(t1 - t0) - (count - 1) * C;
+    auto steps = [&](int c) { return c == count - 1 ? n_last : C; };
+    auto send = [&](int c, int stage) {
+        unsigned char *const to = smem + stage * kTiles;
+        kin.send(k, steps(c), wave, to);
+        vin.send(v, steps(c), wave, to + S::Keys::kBytes);
+        qin.send(q, steps(c), wave, to + S::Keys::kBytes + S::Values::kBytes);
+    };
+    auto fetch = [&](int c) {
+        kin.fetch(k, t0 + c * C, steps(c));
+        vin.fetch(v, t0 + c * C, steps(c));
+        qin.fetch(q, t0 + c * C, steps(c));
+    };
+    if constexpr (S::VEC) {
+        for (int c = 0; c < kStages - 1; ++c)
+            if (c < count) send(c, c);
+    } else {
+        if (count > 0) fetch(0);
+    }
 
     const float ld = decay_log2(W.log_decay, h);
     const int e = w.early;
     auto power = [&](int n) { return fast_exp2(ld * static_cast<float>(n)); };
     const int my_v = v0 + 32 * wave + column_of(col);    // column of this lane's state
-    const int64_t bh = b * W.heads + h;
-
-    // element j of block kb of the state: row 32 kb + 16 (j / 8) + 8 half + j % 8
+    const int64_t bh = b * W.heads + h, states = static_cast<int64_t>(w.A) * w.B;
     f32x16 X[KB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int j = 0; j < 16; ++j) X[kb][j] = 0.0f;
-    if (OUT && (seg > 0 || w.first)) {
-        const int64_t sa = seg > 0 ? w.seg_sa : w.first_sa, sb = seg > 0 ? w.seg_sb : w.first_sb;
-        const int64_t states = static_cast<int64_t>(w.A) * w.B;
-        const float *from = seg > 0 ? w.segments + ((b * (W.segments - 1) + seg - 1) * W.heads + h) * states
-                                    : w.first + bh * states;
-        if (my_v < w.B) {
+    if (seg > 0 || w.first) {
+        // at most 256 x 256 values; what the state does not have reads as zero
+        const float *from = seg > 0 ? w.segments + ((b * (W.segments - 1) + seg - 1) * W.heads + h) * states : w.first + bh * states;
+        const int sa = static_cast<int>(seg > 0 ? w.seg_sa : w.first_sa), sb = static_cast<int>(seg > 0 ? w.seg_sb : w.first_sb);
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(from), 0, static_cast<int>(states) * 4, 0x00020000);
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int a = 32 * kb + 16 * (j / 8) + 8 * half + j % 8;
-                    if (a < w.A) X[kb][j] = from[a * sa + my_v * sb];
-                }
-        }
+            for (int j = 0; j < 16; ++j) {
+                const int a = state_row(kb, j, half);
+                const int off = a < w.A && my_v < w.B ? (a * sa + my_v * sb) * 4 : INT32_MIN;
+                X[kb][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, off, 0, 0));
+            }
     }
 
-    // decays inside a chunk: of outputs (this lane's is col) from its inputs and from the
-    // state in front, and of the inputs to the state behind
+    // decays inside a chunk: of outputs (this lane's is col) from its inputs (0 from later
+    // ones) and from the state in front, and of the inputs to the state behind
     float inside[16], weight[16];
+    Mask<Frag> earlier[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) earlier[s] = mask_of(Frag{}, col - 16 * s - 4 * half);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         const int row = acc_row(j) + 4 * half;
-        inside[j] = w.inner * power(max(col - row, 0));
+        inside[j] = row <= col ? w.inner * w.scale * power(col - row) : 0.0f;
         weight[j] = w.inner * power(C - e - row);
     }
-    const float front = power(col + e);
+    const float front = w.scale * power(col + e);
     float whole = power(C);
 
-    const int64_t row_first = w.reverse ? start + len - 1 : start, sign = w.reverse ? -1 : 1;
-    const int64_t lda = W.heads * w.A, ldb = W.heads * w.B;
-    const Rows<const T> q{static_cast<const T *>(w.q) + row_first * lda + h * w.A, sign * lda, w.A},
-        k{static_cast<const T *>(w.k) + row_first * lda + h * w.A, sign * lda, w.A},
-        v{static_cast<const T *>(w.v) + row_first * ldb + h * w.B + v0, sign * ldb, width};
-    const Rows<T> o{OUT ? static_cast<T *>(w.o) + row_first * ldb + h * w.B + v0 : nullptr, sign * ldb, width};
-    const int my_out = 32 * wave + 8 * half;      // first of the outputs of row col
-    Feed<S, typename S::Keys> kin, qin;
-    Feed<S, typename S::Values> vin;
-    auto steps = [&](int64_t t) { return static_cast<int>(min(int64_t(C), t1 - t)); };
-    auto send = [&](int64_t t, int stage) {
-        unsigned char *const to = smem + stage * kTiles;
-        kin.send(k, t, steps(t), wave, to);
-        vin.send(v, t, steps(t), wave, to + S::Keys::kBytes);
-        if (OUT) qin.send(q, t, steps(t), wave, to + S::Keys::kBytes + S::Values::kBytes);
-    };
-    auto fetch = [&](int64_t t) {
-        kin.fetch(k, t, steps(t));
-        vin.fetch(v, t, steps(t));
-        if (OUT) qin.fetch(q, t, steps(t));
-    };
-    if (t0 < t1) {
-        if (S::VEC) {
-            for (int ahead = 0; ahead < kStages - 1; ++ahead)
-                if (t0 + ahead * C < t1) send(t0 + ahead * C, ahead);
-        } else {
-            fetch(t0);
-        }
-    }
-    int stage = 0, last_stage = kStages - 1;
-    for (int64_t t = t0; t < t1; t += C) {
-        const int n = steps(t);
-        const unsigned char *const Ks = smem + stage * kTiles, *const Vs = Ks + S::Keys::kBytes, *const Qs = Vs + S::Values::kBytes;
+    int stage = 0, to_fill = kStages - 1;
+    for (int c = 0; c < count; ++c) {
+        const int n = steps(c);
+        unsigned char *const Ks = smem + stage * kTiles, *const Vs = Ks + S::Keys::kBytes, *const Qs = Vs + S::Values::kBytes;
         if constexpr (S::VEC) {
             // What is under way behind this chunk's loads may stay so: those of the next
-            // chunk and the outputs of the one before, which were sent after them.  Then
-            // every wave has read the stage that the next loads go to.
+            // chunks and the outputs sent after them.  Then every wave has read the stage
+            // that the next loads go to.
             if constexpr (kStages == 1) {
                 wait_and_meet<0>();
-                send(t, 0);
+                send(c, 0);
                 wait_and_meet<0>();
             } else {
-                if (kStages == 2 || t + C >= t1) wait_and_meet<0>();
-                else if (t == t0) wait_and_meet<kLoads>();
-                else wait_and_meet<kLoads + kStores>();
-                if (t + (kStages - 1) * C < t1) send(t + (kStages - 1) * C, last_stage);
+                constexpr int kAhead = kStages - 2;
+                if (kAhead == 0 || c + kAhead >= count) wait_and_meet<0>();
+                else if (c < kAhead) wait_and_meet<kAhead * kLoads>();
+                else wait_and_meet<kAhead * (kLoads + S::stores)>();
+                if (c + kStages - 1 < count) send(c + kStages - 1, to_fill);
             }
         } else {
-            unsigned char *const to = smem + stage * kTiles;
             if (kStages == 1) __syncthreads();
-            kin.store(to);
-            vin.store(to + S::Keys::kBytes);
-            if (OUT) qin.store(to + S::Keys::kBytes + S::Values::kBytes);
+            kin.store(Ks);
+            vin.store(Vs);
+            qin.store(Qs);
             __syncthreads();                      // who reads the other stage has read it
-            if (t + C < t1) fetch(t + C);
+            if (c + 1 < count) fetch(c + 1);
         }
-        last_stage = stage;
+        to_fill = stage;
         stage = stage == kStages - 1 ? 0 : stage + 1;
         if (n < C) {                              // the last chunk
             whole = power(n);
@@ -492,101 +645,176 @@ __global__ __launch_bounds__(S::threads, S::waves_a_simd(OUT)) void attention_wa
             for (int j = 0; j < 16; ++j) weight[j] = w.inner * power(max(n - e - acc_row(j) - 4 * half, 0));
         }
 
-        // The products leave out later inputs by a factor 0, which an infinite or NaN v
-        // would carry to earlier outputs of its chunk.  Such values are taken out, and what
-        // they reach is set to NaN: their column from their step on.
-        Frag vf[CS];
-        bool odd = false;
-        int reached = C;                          // first such step of this lane's column
+        constexpr int kAhead = KS < 4 ? KS : 4;   // pairs of fragments under way
+        Frag vf[2], qf[kAhead], kf[kAhead];
+        auto load = [&](int i) {
+            qf[i % kAhead] = load_row<typename S::Keys>(Qs, col, 16 * i + 8 * half, T());
+            kf[i % kAhead] = load_row<typename S::Keys>(Ks, col, 16 * i + 8 * half, T());
+        };
 #pragma unroll
-        for (int s = 0; s < CS; ++s) {
-            vf[s] = load_col<typename S::Values>(Vs, 16 * s, 32 * wave, lane, T());
-            odd |= any_odd(vf[s]);
+        for (int s = 0; s < kAhead; ++s) load(s);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) vf[s] = load_col<typename S::Values>(Vs, 16 * s, 32 * wave, lane, T());
+        in_order();
+        f32x16 G, O;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) G[j] = O[j] = 0.0f;
+        // The state enters as an operand of the I/O dtype: in bfloat16 half a step, 2^-8 of
+        // each of its values, like the rounding of the output.
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            mma(G, kf[s % kAhead], qf[s % kAhead]);
+            mma(O, from_acc<Frag>(X[s / 2], s % 2), qf[s % kAhead]);
+            if (s + kAhead < KS) load(s + kAhead);
+            in_order();
         }
-        if (__any(odd)) {
+        advance<S>(X, Ks, vf, weight, whole, lane);
 #pragma unroll
-            for (int s = CS - 1; s >= 0; --s) reached = clean(vf[s], 16 * s + 4 * half, reached);
-            reached = min(reached, __shfl_xor(reached, 32));
+        for (int j = 0; j < 16; ++j) {
+            O[j] *= front;
+            G[j] *= inside[j];
         }
-        if (OUT) {
-            f32x16 G, O;
+        // later inputs leave nothing, whatever their products hold
+        Frag pf[2] = {from_acc<Frag>(G, 0), from_acc<Frag>(G, 1)};
 #pragma unroll
-            for (int j = 0; j < 16; ++j) G[j] = O[j] = 0.0f;
-            // The state enters as an operand of the I/O dtype: in bfloat16 half a step, 2^-8
-            // of each of its values, like the rounding of the output.
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const Frag qf = load_row<typename S::Keys>(Qs, col, 16 * s + 8 * half, T());
-                mma(G, load_row<typename S::Keys>(Ks, col, 16 * s + 8 * half, T()), qf);
-                mma(O, from_acc<Frag>(X[s / 2], s % 2), qf);
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) O[j] *= front;
-            // later inputs leave nothing, whatever their products hold
-#pragma unroll
-            for (int j = 0; j < 16; ++j) G[j] = acc_row(j) + 4 * half <= col ? G[j] * inside[j] : 0.0f;
-#pragma unroll
-            for (int s = 0; s < CS; ++s) mma(O, vf[s], from_acc<Frag>(G, s));
-            if (__any(odd)) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (col >= __shfl(reached, acc_row(j) + 4 * half)) O[j] = __builtin_nanf("");
-            }
+        for (int s = 0; s < 2; ++s) keep(pf[s], earlier[s]);
+        auto put = [&](const f32x16 &r) {
             float out[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) out[j] = O[j] * w.scale;
+            for (int j = 0; j < 16; ++j) out[j] = r[j];
             if constexpr (S::VEC) {
-#pragma unroll
-                for (int s = 0; s < CS; ++s) store_vectors(o, t, n, col, my_out + 16 * s, out + 8 * s);
+                store_vectors(o.buffer(n), out_off, o.missing(n), out, T());
             } else if (col < n) {
-                T *const to = o.p + (t + col) * o.ld + my_out;
-#pragma unroll
-                for (int s = 0; s < CS; ++s) store8(to + 16 * s, out + 8 * s, width - my_out - 16 * s);
+                T *const to = o.p + (t0 + c * C + col) * o.ld + my_out;
+                store8(to, out, width - my_out);
+                store8(to + 16, out + 8, width - my_out - 16);
             }
+        };
+        // The products leave out later inputs by a factor 0, which an infinite or NaN v would
+        // carry to earlier outputs of its chunk.  Such values are taken out, and their column
+        // is set to NaN from their step on.
+        const bool odd = any_odd(vf[0], vf[1]);
+        if (!__any(odd)) {
+            mma(O, vf[0], pf[0]);
+            mma(O, vf[1], pf[1]);
+            put(O);
+        } else {
+            int reached = clean(vf[0], 4 * half, clean(vf[1], 16 + 4 * half, C));
+            reached = min(reached, __shfl_xor(reached, 32));
+            mma(O, vf[0], pf[0]);
+            mma(O, vf[1], pf[1]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (col >= __shfl(reached, acc_row(j) + 4 * half)) O[j] = __builtin_nanf("");
+            put(O);
         }
-        // The state: k_j exact, its partner g^(n-e-j) v_j in bfloat16 as the sum of two
-        // roundings, which hold it to 2^-16.
-        const float f = reached < C ? __builtin_nanf("") : whole;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) X[kb][j] *= f;
-#pragma unroll
-        for (int s = 0; s < CS; ++s) {
-            Frag up, rest;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float u = weight[8 * s + j] * get(vf[s], j);
-                set(up, j, u);
-                set(rest, j, u - get(up, j));
-            }
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                const Frag a = load_col<typename S::Keys>(Ks, 16 * s, 32 * kb, lane, T());
-                mma(X[kb], a, up);
-                if (sizeof(T) == 2) mma(X[kb], a, rest);
-            }
-        }
+        o.next += o.step;
     }
 
-    if (OUT && !w.last) return;
-    if (OUT && !(t1 == len && (t1 > t0 || seg == 0))) return;
-    const int64_t states = static_cast<int64_t>(w.A) * w.B;
-    float *to = OUT ? w.last + bh * states : w.segments + ((b * (W.segments - 1) + seg) * W.heads + h) * states;
-    const int64_t sa = OUT ? w.last_sa : w.seg_sa, sb = OUT ? w.last_sb : w.seg_sb;
-    if (my_v < w.B) {
+    if (!w.last || t1 != len || (t1 <= t0 && seg > 0) || my_v >= w.B) return;
+    float *to = w.last + bh * states;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int a = 32 * kb + 16 * (j / 8) + 8 * half + j % 8;
-                if (a < w.A) to[a * sa + my_v * sb] = X[kb][j];
-            }
-    }
+        for (int j = 0; j < 16; ++j) {
+            const int a = state_row(kb, j, half);
+            if (a < w.A) to[a * w.last_sa + my_v * w.last_sb] = X[kb][j];
+        }
 }
 
-// X_{s+1} = g^T X_s + local_s in place: slot s receives the state in front of segment
-// s + 1.
+// The walk of a segment for its state alone, from zero: for those that others follow, which
+// are whole chunks.
+template <typename S>
+__global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_state_kernel(const Walks W) {
+    typedef typename S::Type T;
+    typedef typename S::Frag Frag;
+    constexpr int KB = S::KB, kStages = S::stages(false), kTiles = S::tiles(false), kLoads = S::loads(false);
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+
+    const Place at(W);
+    const Walk &w = W.w[at.role];
+    const int seg = at.seg;
+    const int64_t h = at.h, b = at.b;
+    if (at.slice >= w.slices || seg == W.segments - 1) return;
+    int64_t start, len;
+    sequence(W, b, &start, &len);
+    const int64_t t0 = seg * W.segment;
+    if (t0 + W.segment >= len) return;
+    const int count = static_cast<int>(W.segment / C);
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, half = lane / 32, col = lane % 32;
+    const int v0 = at.slice * S::VP, width = min(S::VP, w.B - v0), my_v = v0 + 32 * wave + column_of(col);
+    const int64_t row_first = w.reverse ? start + len - 1 : start, sign = w.reverse ? -1 : 1;
+    Rows<T> k(static_cast<const T *>(w.k) + h * w.A, row_first, W.heads * w.A, sign, w.A);
+    Rows<T> v(static_cast<const T *>(w.v) + h * w.B + v0, row_first, W.heads * w.B, sign, width);
+    k.seek(t0);
+    v.seek(t0);
+    Feed<S, typename S::Keys> kin(k);
+    Feed<S, typename S::Values> vin(v);
+    auto send = [&](int stage) {
+        kin.send(k, C, wave, smem + stage * kTiles);
+        vin.send(v, C, wave, smem + stage * kTiles + S::Keys::kBytes);
+    };
+    auto fetch = [&](int c) {
+        kin.fetch(k, t0 + c * C, C);
+        vin.fetch(v, t0 + c * C, C);
+    };
+    if constexpr (S::VEC) {
+        for (int c = 0; c < kStages - 1; ++c)
+            if (c < count) send(c);
+    } else {
+        fetch(0);
+    }
+    const float ld = decay_log2(W.log_decay, h), whole = fast_exp2(ld * C);
+    float weight[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) weight[j] = w.inner * fast_exp2(ld * (C - w.early - acc_row(j) - 4 * half));
+    const int64_t states = static_cast<int64_t>(w.A) * w.B;
+    f32x16 X[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) X[kb][j] = 0.0f;
+
+    int stage = 0, to_fill = kStages - 1;
+    for (int c = 0; c < count; ++c) {
+        unsigned char *const Ks = smem + stage * kTiles, *const Vs = Ks + S::Keys::kBytes;
+        if constexpr (S::VEC) {
+            if constexpr (kStages == 1) {
+                wait_and_meet<0>();
+                send(0);
+                wait_and_meet<0>();
+            } else {
+                if (kStages == 2 || c + kStages - 2 >= count) wait_and_meet<0>();
+                else wait_and_meet<(kStages - 2) * kLoads>();
+                if (c + kStages - 1 < count) send(to_fill);
+            }
+        } else {
+            if (kStages == 1) __syncthreads();
+            kin.store(Ks);
+            vin.store(Vs);
+            __syncthreads();
+            if (c + 1 < count) fetch(c + 1);
+        }
+        to_fill = stage;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        Frag vf[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) vf[s] = load_col<typename S::Values>(Vs, 16 * s, 32 * wave, lane, T());
+        advance<S>(X, Ks, vf, weight, whole, lane);
+    }
+    if (my_v >= w.B) return;
+    float *const to = w.segments + ((b * (W.segments - 1) + seg) * W.heads + h) * states;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int a = state_row(kb, j, half);
+            if (a < w.A) to[a * w.seg_sa + my_v * w.seg_sb] = X[kb][j];
+        }
+}
+
+// X_{s+1} = g^n X_s + sum_s in place: slot s receives the state in front of segment s + 1.
 __global__ __launch_bounds__(256) void attention_fold_kernel(const Walks W) {
     const Walk &w = W.w[blockIdx.z];
     const int64_t bh = blockIdx.y, b = bh / W.heads, h = bh % W.heads;
@@ -595,7 +823,7 @@ __global__ __launch_bounds__(256) void attention_fold_kernel(const Walks W) {
     if (id >= states) return;
     int64_t start, len;
     sequence(W, b, &start, &len);
-    // segments that end before the sequence does
+    // segments that others follow
     const int64_t full = len <= 0 ? 0 : min(int64_t(W.segments - 1), (len - 1) / W.segment);
     const float g = fast_exp2(decay_log2(W.log_decay, h) * static_cast<float>(W.segment));
     const int64_t a = id / w.B, c = id % w.B;
@@ -603,12 +831,12 @@ __global__ __launch_bounds__(256) void attention_fold_kernel(const Walks W) {
     float *p = w.segments + (b * (W.segments - 1) * W.heads + h) * states + a * w.seg_sa + c * w.seg_sb;
     const int64_t next = W.heads * states;
     for (int64_t s = 0; s < full; s += 8, p += 8 * next) {
-        float local[8];
+        float sum[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) local[i] = s + i < full ? p[i * next] : 0.0f;
+        for (int i = 0; i < 8; ++i) sum[i] = s + i < full ? p[i * next] : 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            x = fmaf(g, x, local[i]);
+            x = fmaf(g, x, sum[i]);
             if (s + i < full) p[i * next] = x;
         }
     }
@@ -619,81 +847,96 @@ __global__ __launch_bounds__(256) void attention_fold_kernel(const Walks W) {
 int waves_of(int64_t B) { return B <= 64 ? 2 : 4; }
 int slices_of(int64_t B) { return static_cast<int>((B + 32 * waves_of(B) - 1) / (32 * waves_of(B))); }
 
-constexpr int64_t kSlots = 512;   // workgroups that the device holds at once
+// Blocks of 32 that A is rounded up to.
+int blocks_of(int64_t A) { return A <= 64 ? 2 : A <= 96 ? 3 : A <= 128 ? 4 : A <= 192 ? 6 : 8; }
 
-// Segments of a sequence and their steps: as many as give every compute unit two
-// workgroups of the forward, all at once.
-void cut(const AttentionArgs &a, bool bwd, int *segments, int64_t *steps) {
-    const int64_t walks = std::max<int64_t>(1, a.seqs * a.heads * slices_of(a.value));
-    const int64_t n = std::max<int64_t>(1, std::min((bwd ? kSlots / 2 : kSlots) / walks, a.seqlen / (4 * C)));
-    *steps = std::max<int64_t>(C, ((a.seqlen + n - 1) / n + C - 1) / C * C);
-    *segments = static_cast<int>(std::max<int64_t>(1, (a.seqlen + *steps - 1) / *steps));
+// Segments of a sequence and their steps: so many that the device's 256 compute units have
+// a forward workgroup each; backward, where three walks share a launch, half as many.  More
+// of them cost more in states, each written once, folded and read again, than two
+// workgroups a unit gain: 2 x 4096 x 20 x 128 in bfloat16 87 us with 6 segments and 91 us
+// with 12, backward 168 us with 3 and 169 us with 6, 131072 steps of 4 heads 200 and 211 us.
+// Sequences of different lengths are cut by what all rows together give a workgroup, the
+// longest into at most four times what it would be cut into otherwise (7 sequences of 431
+// steps in the mean, backward in float32 131 us, cut as if all were as long 154 us).
+constexpr int64_t kWorkgroups = 256;
+void cut(const AttentionArgs &a, bool bwd, Walks *W) {
+    const int64_t slices = std::max(slices_of(a.value), bwd ? slices_of(a.key) : 0), heads = std::max<int64_t>(1, a.heads) * slices;
+    const int64_t walks = std::max<int64_t>(1, a.seqs) * heads, each = bwd ? kWorkgroups / 2 : kWorkgroups;
+    int64_t n = std::min(each / walks, a.seqlen / (4 * C));
+    if (a.total != a.seqs * a.seqlen) {
+        const int64_t share = std::max<int64_t>(2 * C, (a.total * heads + each - 1) / each);
+        n = std::min((a.seqlen + share - 1) / share, 4 * each / walks);
+    }
+    n = std::max<int64_t>(1, n);
+    W->segment = std::max<int64_t>(C, ((a.seqlen + n - 1) / n + C - 1) / C * C);
+    W->segments = static_cast<int>(std::max<int64_t>(1, (a.seqlen + W->segment - 1) / W->segment));
 }
 
-template <typename S, bool OUT>
-hipError_t launch_walks(const Walks &W, hipStream_t stream) {
-    int most = 0;
-    for (int i = 0; i < W.count; ++i) most = std::max(most, W.w[i].slices);
-    const int64_t n = W.seqs * W.segments * W.heads * most * W.count;
-    constexpr int lds = S::stages(OUT) * S::tiles(OUT);
+template <typename K>
+hipError_t launch(K kernel, int64_t blocks, int threads, int lds, const Walks &W, hipStream_t stream) {
     if (lds > 65536)
-        if (const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attention_walk_kernel<S, OUT>),
+        if (const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds))
             return e;
-    hipLaunchKernelGGL((attention_walk_kernel<S, OUT>), dim3(static_cast<uint32_t>(n)), dim3(S::threads), lds, stream, W);
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(threads), lds, stream, W);
     return hipGetLastError();
 }
 
-// What instantiates the kernel for a walk: A rounded up, waves, whole vectors.
+// What instantiates the kernels for a walk: A rounded up, waves, whole vectors.
 struct Kind {
-    int keys, waves;
+    int blocks, waves;
     bool vec;
-    bool operator==(const Kind &k) const { return keys == k.keys && waves == k.waves && vec == k.vec; }
+    bool operator==(const Kind &k) const { return blocks == k.blocks && waves == k.waves && vec == k.vec; }
 };
 
-template <bool OUT>
-Kind kind_of(const Walk &w, int size) {
+Kind kind_of(const Walk &w, int size, bool out) {
     const auto p = [](const void *a) { return reinterpret_cast<uintptr_t>(a); };
-    const uintptr_t at = p(w.k) | p(w.v) | (OUT ? p(w.q) | p(w.o) : 0);
-    return Kind{w.A <= 64 ? 64 : w.A <= 128 ? 128 : 256, waves_of(w.B), (at | (w.A | w.B) * size) % 16 == 0};
+    const uintptr_t at = p(w.k) | p(w.v) | (out ? p(w.q) | p(w.o) : 0);
+    return Kind{blocks_of(w.A), waves_of(w.B), (at | (w.A | w.B) * size) % 16 == 0};
 }
 
-template <typename T, bool OUT, bool VEC>
-hipError_t launch_group(const Walks &W, const Kind &k, hipStream_t stream) {
-    if (k.waves == 2) {
-        if (k.keys == 64) return launch_walks<Shape<T, 64, 2, VEC>, OUT>(W, stream);
-        if (k.keys == 128) return launch_walks<Shape<T, 128, 2, VEC>, OUT>(W, stream);
-        return launch_walks<Shape<T, 256, 2, VEC>, OUT>(W, stream);
+template <typename S>
+hipError_t launch_shape(const Walks &W, bool out, hipStream_t stream) {
+    int most = 0;
+    for (int i = 0; i < W.count; ++i) most = std::max(most, W.w[i].slices);
+    const int64_t blocks = W.seqs * W.segments * W.heads * most * W.count;   // below 2^24
+    const int lds = S::stages(out) * S::tiles(out);
+    return out ? launch(attention_walk_kernel<S>, blocks, S::threads, lds, W, stream)
+               : launch(attention_state_kernel<S>, blocks, S::threads, lds, W, stream);
+}
+
+template <typename T, int WAVES, bool VEC>
+hipError_t launch_kind(const Walks &W, const Kind &k, bool out, hipStream_t stream) {
+    switch (k.blocks) {
+        case 2: return launch_shape<Shape<T, 2, WAVES, VEC>>(W, out, stream);
+        case 3: return launch_shape<Shape<T, 3, WAVES, VEC>>(W, out, stream);
+        case 4: return launch_shape<Shape<T, 4, WAVES, VEC>>(W, out, stream);
+        case 6: return launch_shape<Shape<T, 6, WAVES, VEC>>(W, out, stream);
+        default: return launch_shape<Shape<T, 8, WAVES, VEC>>(W, out, stream);
     }
-    if (k.keys == 64) return launch_walks<Shape<T, 64, 4, VEC>, OUT>(W, stream);
-    if (k.keys == 128) return launch_walks<Shape<T, 128, 4, VEC>, OUT>(W, stream);
-    return launch_walks<Shape<T, 256, 4, VEC>, OUT>(W, stream);
 }
 
-// Walks of one kind share a launch.
-template <typename T, bool OUT>
-hipError_t launch_all(const Walks &W, hipStream_t stream) {
+// Walks of one kind share a launch: with their outputs, or for the states in front of
+// their segments.
+template <typename T>
+hipError_t launch_all(const Walks &W, bool out, hipStream_t stream) {
     bool done[3] = {false, false, false};
     for (int i = 0; i < W.count; ++i) {
         if (done[i]) continue;
-        const Kind kind = kind_of<OUT>(W.w[i], sizeof(T));
+        const Kind kind = kind_of(W.w[i], sizeof(T), out);
         Walks G = W;
         G.count = 0;
         for (int j = i; j < W.count; ++j)
-            if (!done[j] && kind_of<OUT>(W.w[j], sizeof(T)) == kind) {
+            if (!done[j] && kind_of(W.w[j], sizeof(T), out) == kind) {
                 G.w[G.count++] = W.w[j];
                 done[j] = true;
             }
         for (int j = G.count; j < 3; ++j) G.w[j] = G.w[0];
-        if (const hipError_t e = kind.vec ? launch_group<T, OUT, true>(G, kind, stream) : launch_group<T, OUT, false>(G, kind, stream))
-            return e;
+        const hipError_t e = kind.waves == 2 ? (kind.vec ? launch_kind<T, 2, true>(G, kind, out, stream) : launch_kind<T, 2, false>(G, kind, out, stream))
+                                             : (kind.vec ? launch_kind<T, 4, true>(G, kind, out, stream) : launch_kind<T, 4, false>(G, kind, out, stream));
+        if (e != hipSuccess) return e;
     }
     return hipSuccess;
-}
-
-template <bool OUT>
-hipError_t launch_all(const Walks &W, bool f32, hipStream_t stream) {
-    return f32 ? launch_all<float, OUT>(W, stream) : launch_all<uint16_t, OUT>(W, stream);
 }
 
 Walks common(const AttentionArgs &a, bool bwd) {
@@ -701,17 +944,26 @@ Walks common(const AttentionArgs &a, bool bwd) {
     W.cu = a.cu_seqlens;
     W.log_decay = a.log_decay;
     W.seqs = a.seqs; W.seqlen = a.seqlen; W.total = a.total; W.heads = a.heads;
-    cut(a, bwd, &W.segments, &W.segment);
+    cut(a, bwd, &W);
     return W;
 }
 
-hipError_t fold(const Walks &W, hipStream_t stream) {
-    int64_t states = 0;
-    for (int i = 0; i < W.count; ++i) states = std::max(states, static_cast<int64_t>(W.w[i].A) * W.w[i].B);
+// The states in front of the segments of W's walks.
+hipError_t prepare(const Walks &W, bool f32, hipStream_t stream) {
+    if (W.segments == 1) return hipSuccess;
+    hipError_t e = f32 ? launch_all<float>(W, false, stream) : launch_all<uint16_t>(W, false, stream);
+    if (e != hipSuccess) return e;
+    int64_t most = 0;
+    for (int i = 0; i < W.count; ++i) most = std::max(most, static_cast<int64_t>(W.w[i].A) * W.w[i].B);
     hipLaunchKernelGGL(attention_fold_kernel,
-                       dim3(static_cast<uint32_t>((states + 255) / 256), static_cast<uint32_t>(W.seqs * W.heads), W.count),
+                       dim3(static_cast<uint32_t>((most + 255) / 256), static_cast<uint32_t>(W.seqs * W.heads), W.count),
                        dim3(256), 0, stream, W);
     return hipGetLastError();
+}
+
+// Floats of a walk's states in the workspace.
+int64_t floats_of(const AttentionArgs &a, const Walks &W) {
+    return static_cast<int64_t>(W.segments - 1) * a.seqs * a.heads * a.key * a.value;
 }
 
 // ---- one step ------------------------------------------------------------------
@@ -792,26 +1044,24 @@ hipError_t step(const AttentionArgs &a, hipStream_t stream) {
 }  // namespace
 
 size_t linear_attention_workspace(const AttentionArgs &a, bool bwd) {
-    const Walks W = common(a, bwd);
-    return static_cast<size_t>(W.segments - 1) * a.seqs * a.heads * a.key * a.value * sizeof(float) * (bwd ? 2 : 1);
+    return static_cast<size_t>(floats_of(a, common(a, bwd))) * sizeof(float) * (bwd ? 2 : 1);
 }
 
 hipError_t launch_linear_attention_fwd(const AttentionArgs &a, void *workspace, hipStream_t stream) {
     Walks W = common(a, false);
+    const bool f32 = a.io == IO_F32;
     const size_t bytes = linear_attention_workspace(a, false);
     void *ws = workspace;
     if (bytes && !ws)
         if (const hipError_t e = scratch_alloc(&ws, bytes, stream)) return e;
     const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
+    float *S = static_cast<float *>(ws);
     W.count = 1;
-    W.w[0] = Walk{a.q, a.k, a.v, a.o, a.h0, a.h_last, static_cast<float *>(ws), V, 1, V, 1, V, 1, K, V,
+    W.w[0] = Walk{a.q, a.k, a.v, a.o, a.h0, a.h_last, S, V, 1, V, 1, V, 1, K, V,
                   slices_of(V), 1, 0, 1.0f, a.scale};
-    hipError_t e = hipSuccess;
-    if (W.segments > 1) {
-        e = launch_all<false>(W, a.io == IO_F32, stream);
-        if (e == hipSuccess) e = fold(W, stream);
-    }
-    if (e == hipSuccess) e = launch_all<true>(W, a.io == IO_F32, stream);
+    W.w[1] = W.w[2] = W.w[0];
+    hipError_t e = prepare(W, f32, stream);
+    if (e == hipSuccess) e = f32 ? launch_all<float>(W, true, stream) : launch_all<uint16_t>(W, true, stream);
     if (bytes && !workspace) {
         const hipError_t f = scratch_free(ws, stream);
         if (e == hipSuccess) e = f;
@@ -821,30 +1071,27 @@ hipError_t launch_linear_attention_fwd(const AttentionArgs &a, void *workspace, 
 
 hipError_t launch_linear_attention_bwd(const AttentionArgs &a, void *workspace, hipStream_t stream) {
     Walks W = common(a, true);
+    const bool f32 = a.io == IO_F32;
     const size_t bytes = linear_attention_workspace(a, true);
     void *ws = workspace;
     if (bytes && !ws)
         if (const hipError_t e = scratch_alloc(&ws, bytes, stream)) return e;
     const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
-    float *S = static_cast<float *>(ws), *R = S + bytes / 2 / sizeof(float);
+    float *S = static_cast<float *>(ws), *R = S + floats_of(a, W);
     // S^T in (V, K) as the first walk forms it; R in (K, V) as the third does
     const Walk dq{a.dout, a.v, a.k, a.dq, a.h0, nullptr, S, 1, V, 0, 0, K, 1, V, K, slices_of(K), 1, 0, 1.0f, a.scale};
     const Walk dk{a.v, a.dout, a.q, a.dk, a.dh_last, nullptr, R, 1, V, 0, 0, 1, V, V, K, slices_of(K), 0, 1, a.scale, 1.0f};
     const Walk dv{a.k, a.q, a.dout, a.dv, a.dh_last, a.dh0, R, V, 1, V, 1, V, 1, K, V, slices_of(V), 0, 1, a.scale, 1.0f};
-    hipError_t e = hipSuccess;
-    if (W.segments > 1) {
-        W.count = 2;
-        W.w[0] = dq;
-        W.w[1] = dv;
-        W.w[2] = dq;
-        e = launch_all<false>(W, a.io == IO_F32, stream);
-        if (e == hipSuccess) e = fold(W, stream);
-    }
+    W.count = 2;
+    W.w[0] = dq;
+    W.w[1] = dv;
+    W.w[2] = dq;
+    hipError_t e = prepare(W, f32, stream);
     W.count = 3;
     W.w[0] = dq;
     W.w[1] = dk;
     W.w[2] = dv;
-    if (e == hipSuccess) e = launch_all<true>(W, a.io == IO_F32, stream);
+    if (e == hipSuccess) e = f32 ? launch_all<float>(W, true, stream) : launch_all<uint16_t>(W, true, stream);
     if (bytes && !workspace) {
         const hipError_t f = scratch_free(ws, stream);
         if (e == hipSuccess) e = f;
