@@ -350,18 +350,24 @@ struct Feed {
         R.next += R.step;
 #endif
     }
-    // Through registers, element by element.
+    // Through registers: rows begin at any element.
     __device__ __forceinline__ void fetch(const Rows<T> &R, int64_t t, int n) {
+        typedef u32x4 Any __attribute__((aligned(2)));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            T v[L::E] = {};
-            if (row(i) < n) {
-                const T *p = R.p + (t + row(i)) * R.ld;
+            r[i] = u32x4{0, 0, 0, 0};
+            const int c = chunk(i) * L::E;
+            if (row(i) >= n || c >= R.width) continue;
+            const T *p = R.p + (t + row(i)) * R.ld + c;
+            if (c + L::E <= R.width) {
+                r[i] = *reinterpret_cast<const Any *>(p);
+            } else {
+                T v[L::E] = {};
 #pragma unroll
                 for (int x = 0; x < L::E; ++x)
-                    if (chunk(i) * L::E + x < R.width) v[x] = p[chunk(i) * L::E + x];
+                    if (c + x < R.width) v[x] = p[x];
+                r[i] = *reinterpret_cast<const u32x4 *>(v);
             }
-            r[i] = *reinterpret_cast<const u32x4 *>(v);
         }
     }
     __device__ __forceinline__ void store(unsigned char *tile) const {
@@ -418,11 +424,24 @@ __device__ __forceinline__ void store_vectors(__amdgpu_buffer_rsrc_t to, const i
             u32x4{v[i / 2][4 * (i % 2)], v[i / 2][4 * (i % 2) + 1], v[i / 2][4 * (i % 2) + 2], v[i / 2][4 * (i % 2) + 3]}, to,
             off[i] - missing, 0, 0);
 }
-template <typename T>
-__device__ __forceinline__ void store8(T *p, const float *f, int left) {
+// The same without whole vectors: eight columns side by side of which `left` exist.
+__device__ __forceinline__ void store8(uint16_t *p, const float *f, int left) {
+    typedef u32x4 Any __attribute__((aligned(2)));
+    bf16x8 b;
+    pack(b, f);
+    const u32x4 v = __builtin_bit_cast(u32x4, b);
+    if (left >= 8) {
+        *reinterpret_cast<Any *>(p) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = static_cast<uint16_t>(v[j / 2] >> 16 * (j % 2));
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float *f, int left) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (j < left) Io<T>::store(p, j, f[j]);
+        if (j < left) p[j] = f[j];
 }
 
 // Workgroups go to the eight XCDs in turn: each gets a run of consecutive positions, so
@@ -461,7 +480,8 @@ __device__ __forceinline__ int state_row(int kb, int j, int half) { return 32 * 
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // X <- g X + (keys)^T (weights * values): the keys exact, their partners in bfloat16 as the
-// sum of two roundings, which hold them to 2^-16.
+// sum of three roundings, which hold a float32: with two the state is off by 4e-6, with
+// three by what float32 sums are, 3e-7.
 template <typename S, typename Frag, int KB>
 __device__ __forceinline__ void advance(f32x16 (&X)[KB], const unsigned char *Ks, const Frag (&vf)[2], const float *weight,
                                         float g, int lane) {
@@ -479,20 +499,21 @@ __device__ __forceinline__ void advance(f32x16 (&X)[KB], const unsigned char *Ks
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         float u[8];
-        Frag up, rest;
+        constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
+        Frag part[kParts];
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = weight[8 * s + j] * get(vf[s], j);
-        pack(up, u);
-        if (sizeof(T) == 2) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] -= get(up, j);
-            pack(rest, u);
+        for (int i = 0; i < kParts; ++i) {
+            pack(part[i], u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] -= get(part[i], j);
         }
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             const int i = s * KB + kb;
-            mma(X[kb], a[i % kAhead], up);
-            if (sizeof(T) == 2) mma(X[kb], a[i % kAhead], rest);
+#pragma unroll
+            for (int j = 0; j < kParts; ++j) mma(X[kb], a[i % kAhead], part[j]);
             if (i + kAhead < 2 * KB) load(i + kAhead);
             in_order();
         }
