@@ -720,7 +720,7 @@ typedef struct {
  * values; inside a chunk the decayed products q.k, and the state as it meets q,
  * enter as bfloat16 where `io` is bfloat16 (float32 otherwise), while the state
  * itself is carried in float32.  Results are repeatable bit for bit.  A v that is
- * infinite or NaN makes its own column NaN from its step on, in o and in the state;
+ * infinite or NaN makes its own column NaN from its step on in o, and not finite in the state;
  * a q or k that is not finite reaches what the formula says it does.
  * Errors as for mssm_selective_scan_fwd; also MSSM_ERR_INVALID_ARG for a scale
  * that is not finite, key or value < 1, or total != seqs * seqlen without

@@ -20,6 +20,18 @@
 //   X_{s+1} = g^n X_s + sum_s  (n steps a segment),
 // and the third walks every segment from the state in front of it.  Everything is summed
 // in an order that depends on the sizes alone.
+//
+// A chunk's products run on the matrix cores from tiles in LDS, which its rows reach
+// without passing registers, two or three chunks ahead; the transposed operands come from
+// transposing LDS reads, and accumulators feed the next product as they are, the order of
+// a contraction being free.  Every wave has 32 columns of values with their part of the
+// state, and forms q.k again for itself: shared through LDS it would cost a barrier a chunk.
+//
+// Bound by memory and the chunk's chain of products about equally: at 2 x 8448 x 20 x 128
+// in bfloat16 the third launch takes 85 us, its loads and stores alone 81 us, without loads
+// 70 us.  Whole calls: 2 x 4096 x 20 x 128 forward 102 us, backward 196 us, 131072 steps of
+// 4 heads 253 us; 7 packed sequences of 5 heads, 80 and 72 wide, in float32 backward 128 us;
+// one step of 64 sequences 26 us (6.4 TB/s over the states), of one 4 us on the device.
 #include <algorithm>
 #include <type_traits>
 
@@ -481,7 +493,7 @@ __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); 
 
 // X <- g X + (keys)^T (weights * values): the keys exact, their partners in bfloat16 as the
 // sum of three roundings, which hold a float32: with two the state is off by 4e-6, with
-// three by what float32 sums are, 3e-7.
+// three by what float32 sums are, 3e-7 (2 x 4096 x 20 x 128 forward 90 us and 102 us).
 template <typename S, typename Frag, int KB>
 __device__ __forceinline__ void advance(f32x16 (&X)[KB], const unsigned char *Ks, const Frag (&vf)[2], const float *weight,
                                         float g, int lane) {
@@ -874,7 +886,8 @@ int blocks_of(int64_t A) { return A <= 64 ? 2 : A <= 96 ? 3 : A <= 128 ? 4 : A <
 // Segments of a sequence and their steps: so many that the device's 256 compute units have
 // a forward workgroup each; backward, where three walks share a launch, half as many.  More
 // of them cost more in states, each written once, folded and read again, than two
-// workgroups a unit gain: 2 x 4096 x 20 x 128 in bfloat16 87 us with 6 segments and 91 us
+// workgroups a unit gain (taken with two terms of the state, where the rest of the walk is
+// the same): 2 x 4096 x 20 x 128 in bfloat16 87 us with 6 segments and 91 us
 // with 12, backward 168 us with 3 and 169 us with 6, 131072 steps of 4 heads 200 and 211 us.
 // Sequences of different lengths are cut by what all rows together give a workgroup, the
 // longest into at most four times what it would be cut into otherwise (7 sequences of 431

