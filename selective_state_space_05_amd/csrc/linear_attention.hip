@@ -29,8 +29,8 @@
 //
 // Bound by memory and the chunk's chain of products about equally: at 2 x 8448 x 20 x 128
 // in bfloat16 the third launch takes 85 us, its loads and stores alone 81 us, without loads
-// 70 us.  Whole calls: 2 x 4096 x 20 x 128 forward 102 us, backward 196 us, 131072 steps of
-// 4 heads 253 us; 7 packed sequences of 5 heads, 80 and 72 wide, in float32 backward 128 us;
+// 70 us.  Whole calls: 2 x 4096 x 20 x 128 forward 96 us, backward 193 us, 131072 steps of
+// 4 heads 235 us; 7 packed sequences of 5 heads, 80 and 72 wide, in float32 backward 154 us;
 // one step of 64 sequences 26 us (6.4 TB/s over the states), of one 4 us on the device.
 #include <algorithm>
 #include <type_traits>
@@ -493,7 +493,7 @@ __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); 
 
 // X <- g X + (keys)^T (weights * values): the keys exact, their partners in bfloat16 as the
 // sum of three roundings, which hold a float32: with two the state is off by 4e-6, with
-// three by what float32 sums are, 3e-7 (2 x 4096 x 20 x 128 forward 90 us and 102 us).
+// three by what float32 sums are, 3e-7 (2 x 4096 x 20 x 128 forward 90 us and 96 us).
 template <typename S, typename Frag, int KB>
 __device__ __forceinline__ void advance(f32x16 (&X)[KB], const unsigned char *Ks, const Frag (&vf)[2], const float *weight,
                                         float g, int lane) {
