@@ -807,8 +807,9 @@ typedef struct {
  * Values are compared in float64, logits exactly; the sum of the exponentials is
  * float32.  Errors: as for mssm_layer_norm_fwd; also MSSM_ERR_INVALID_ARG for
  * beams, vocab or count < 1 or count > beams * vocab, MSSM_ERR_UNSUPPORTED for
- * beams > MSSM_MAX_BEAMS, count > MSSM_MAX_BEAM_COUNT, vocab >= 2^30 or
- * batch * beams * vocab >= 2^36.  batch == 0: nothing to do, MSSM_OK.
+ * beams > MSSM_MAX_BEAMS, count > MSSM_MAX_BEAM_COUNT, vocab >= 2^30, batch >= 2^24
+ * or 2^24 or more pieces of 4096 words in all beams' vocabularies.  batch == 0:
+ * nothing to do, MSSM_OK.
  */
 MSSM_API mssm_status mssm_beam_select(const void *logits, const float *scores,
                                 float *out_scores, int64_t *out_tokens,
@@ -833,7 +834,7 @@ MSSM_API int64_t mssm_beam_select_workspace(mssm_beam_dims dims, mssm_dtypes dty
  * The host arrays may be reused when the call returns.  dims.vocab and
  * dims.count are ignored.  Errors: MSSM_ERR_INVALID_ARG for a null pointer, a
  * negative size or states that overlap each other or origins;
- * MSSM_ERR_UNSUPPORTED for beams > MSSM_MAX_BEAMS or a state whose entries have
+ * MSSM_ERR_UNSUPPORTED for beams > MSSM_MAX_BEAMS, batch >= 2^24 or a state whose entries have
  * 2^24 or more pieces of 256 times 16 bytes (4 or 1, where its address or row is
  * not a multiple of 16 or 4 bytes).  batch == 0 or count == 0: nothing to do.
  */

@@ -30,8 +30,8 @@
 // Bound by memory and the chunk's chain of products about equally: at 2 x 8448 x 20 x 128
 // in bfloat16 the third launch takes 85 us, its loads and stores alone 81 us, without loads
 // 70 us.  Whole calls: 2 x 4096 x 20 x 128 forward 96 us, backward 193 us, 131072 steps of
-// 4 heads 235 us; 7 packed sequences of 5 heads, 80 and 72 wide, in float32 backward 154 us;
-// one step of 64 sequences 26 us (6.4 TB/s over the states), of one 4 us on the device.
+// 4 heads 231 us; 7 packed sequences of 5 heads, 80 and 72 wide, in float32 backward 137 us;
+// one step of 64 sequences 27 us (6.2 TB/s over the states), of one 4 us on the device.
 #include <algorithm>
 #include <type_traits>
 
@@ -1002,14 +1002,17 @@ int64_t floats_of(const AttentionArgs &a, const Walks &W) {
 
 // ---- one step ------------------------------------------------------------------
 
-// A workgroup holds LANES x VEC columns of one state; groups of LANES lanes take the
-// rows in turn.
-template <typename T, int VEC, int LANES>
+// A workgroup holds 32 columns of one state, VEC of them a lane; groups of lanes take the
+// rows in turn.  Bound by the state's bytes, or by one workgroup's loads where states are
+// few.  Whole lines of 128 columns give a workgroup four times the loads in turn and gain
+// nothing back: 20, 320, 640 and 1280 states of 128 x 128 take 3.7, 11.4, 20.0 and 35.5 us,
+// with 128 columns 6.4, 14.5, 19.5 and 35.6 us.
+template <typename T, int VEC>
 __global__ __launch_bounds__(256) void attention_step_kernel(float *__restrict__ state, const T *__restrict__ q,
                                                              const T *__restrict__ k, const T *__restrict__ v,
                                                              const float *__restrict__ log_decay, float scale,
                                                              T *__restrict__ o, int heads, int K, int V, int slices) {
-    constexpr int GROUPS = 256 / LANES, COLS = LANES * VEC;
+    constexpr int COLS = 32, LANES = COLS / VEC, GROUPS = 256 / LANES;
     __shared__ float sum[GROUPS][COLS];
     const int64_t bh = blockIdx.x / slices;
     const int slice = blockIdx.x % slices, h = static_cast<int>(bh % heads);
@@ -1060,18 +1063,13 @@ __global__ __launch_bounds__(256) void attention_step_kernel(float *__restrict__
 
 template <typename T>
 hipError_t step(const AttentionArgs &a, hipStream_t stream) {
-    const int64_t bh = a.seqs * a.heads;
-    auto go = [&](auto kernel, int cols) {
-        const int64_t slices = (a.value + cols - 1) / cols;
-        hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(bh * slices)), dim3(256), 0, stream, a.h_last,
-                           static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
-                           a.log_decay, a.scale, static_cast<T *>(a.o), static_cast<int>(a.heads),
-                           static_cast<int>(a.key), static_cast<int>(a.value), static_cast<int>(slices));
-    };
+    const int64_t slices = (a.value + 31) / 32;
     const bool vec = a.value % 4 == 0 && reinterpret_cast<uintptr_t>(a.h_last) % 16 == 0;
-    if (!vec) go(attention_step_kernel<T, 1, 32>, 32);
-    else if (bh * ((a.value + 127) / 128) >= 256) go(attention_step_kernel<T, 4, 32>, 128);
-    else go(attention_step_kernel<T, 4, 8>, 32);
+    hipLaunchKernelGGL((vec ? attention_step_kernel<T, 4> : attention_step_kernel<T, 1>),
+                       dim3(static_cast<uint32_t>(a.seqs * a.heads * slices)), dim3(256), 0, stream, a.h_last,
+                       static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
+                       a.log_decay, a.scale, static_cast<T *>(a.o), static_cast<int>(a.heads),
+                       static_cast<int>(a.key), static_cast<int>(a.value), static_cast<int>(slices));
     return hipGetLastError();
 }
 

@@ -149,6 +149,8 @@ def test_sizes_out_of_the_operators_ranges(L):
     assert beam(L, beams=33) == UNSUPPORTED
     assert beam(L, count=65, vocab=100) == UNSUPPORTED
     assert beam(L, batch=1 << 20, vocab=1 << 20) == UNSUPPORTED
+    assert beam(L, batch=1 << 24, vocab=64) == UNSUPPORTED
+    assert beam(L, batch=1 << 20, beams=16, vocab=64) == UNSUPPORTED
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -1.0, 0.0])
