@@ -230,6 +230,7 @@ struct Walk {
     const float *first;      // may be null -> 0
     float *last;             // may be null
     float *segments;         // in the workspace: in front of every segment but the first, the state
+    float *kept;             // there too: receives `first` before anything is written; may be null
     int64_t first_sa, first_sb;
     int64_t last_sa, last_sb;
     int64_t seg_sa, seg_sb;  // strides of the workspace's states
@@ -848,6 +849,8 @@ __global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_state_ke
 }
 
 // X_{s+1} = g^n X_s + sum_s in place: slot s receives the state in front of segment s + 1.
+// States that are advanced in place are copied first: the walk of a first segment may begin
+// after that of the last one, in the same launch, has written over them.
 __global__ __launch_bounds__(256) void attention_fold_kernel(const Walks W) {
     const Walk &w = W.w[blockIdx.z];
     const int64_t bh = blockIdx.y, b = bh / W.heads, h = bh % W.heads;
@@ -860,7 +863,9 @@ __global__ __launch_bounds__(256) void attention_fold_kernel(const Walks W) {
     const int64_t full = len <= 0 ? 0 : min(int64_t(W.segments - 1), (len - 1) / W.segment);
     const float g = fast_exp2(decay_log2(W.log_decay, h) * static_cast<float>(W.segment));
     const int64_t a = id / w.B, c = id % w.B;
-    float x = w.first ? w.first[bh * states + a * w.first_sa + c * w.first_sb] : 0.0f;
+    const int64_t at = bh * states + a * w.first_sa + c * w.first_sb;
+    float x = w.first ? w.first[at] : 0.0f;
+    if (w.kept) w.kept[at] = x;
     float *p = w.segments + (b * (W.segments - 1) * W.heads + h) * states + a * w.seg_sa + c * w.seg_sb;
     const int64_t next = W.heads * states;
     for (int64_t s = 0; s < full; s += 8, p += 8 * next) {
@@ -1075,8 +1080,11 @@ hipError_t step(const AttentionArgs &a, hipStream_t stream) {
 
 }  // namespace
 
+// The forward's holds a copy of h0 too, since the query does not know whether h0 is h_last.
 size_t linear_attention_workspace(const AttentionArgs &a, bool bwd) {
-    return static_cast<size_t>(floats_of(a, common(a, bwd))) * sizeof(float) * (bwd ? 2 : 1);
+    const Walks W = common(a, bwd);
+    const int64_t floats = floats_of(a, W), copy = W.segments > 1 ? a.seqs * a.heads * a.key * a.value : 0;
+    return static_cast<size_t>(bwd ? 2 * floats : floats + copy) * sizeof(float);
 }
 
 hipError_t launch_linear_attention_fwd(const AttentionArgs &a, void *workspace, hipStream_t stream) {
@@ -1089,10 +1097,12 @@ hipError_t launch_linear_attention_fwd(const AttentionArgs &a, void *workspace, 
     const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
     float *S = static_cast<float *>(ws);
     W.count = 1;
-    W.w[0] = Walk{a.q, a.k, a.v, a.o, a.h0, a.h_last, S, V, 1, V, 1, V, 1, K, V,
+    float *const kept = W.segments > 1 && a.h0 && a.h0 == a.h_last ? S + floats_of(a, W) : nullptr;
+    W.w[0] = Walk{a.q, a.k, a.v, a.o, a.h0, a.h_last, S, kept, V, 1, V, 1, V, 1, K, V,
                   slices_of(V), 1, 0, 1.0f, a.scale};
     W.w[1] = W.w[2] = W.w[0];
     hipError_t e = prepare(W, f32, stream);
+    if (kept) W.w[0].first = W.w[1].first = W.w[2].first = kept;
     if (e == hipSuccess) e = f32 ? launch_all<float>(W, true, stream) : launch_all<uint16_t>(W, true, stream);
     if (bytes && !workspace) {
         const hipError_t f = scratch_free(ws, stream);
@@ -1111,9 +1121,9 @@ hipError_t launch_linear_attention_bwd(const AttentionArgs &a, void *workspace, 
     const int K = static_cast<int>(a.key), V = static_cast<int>(a.value);
     float *S = static_cast<float *>(ws), *R = S + floats_of(a, W);
     // S^T in (V, K) as the first walk forms it; R in (K, V) as the third does
-    const Walk dq{a.dout, a.v, a.k, a.dq, a.h0, nullptr, S, 1, V, 0, 0, K, 1, V, K, slices_of(K), 1, 0, 1.0f, a.scale};
-    const Walk dk{a.v, a.dout, a.q, a.dk, a.dh_last, nullptr, R, 1, V, 0, 0, 1, V, V, K, slices_of(K), 0, 1, a.scale, 1.0f};
-    const Walk dv{a.k, a.q, a.dout, a.dv, a.dh_last, a.dh0, R, V, 1, V, 1, V, 1, K, V, slices_of(V), 0, 1, a.scale, 1.0f};
+    const Walk dq{a.dout, a.v, a.k, a.dq, a.h0, nullptr, S, nullptr, 1, V, 0, 0, K, 1, V, K, slices_of(K), 1, 0, 1.0f, a.scale};
+    const Walk dk{a.v, a.dout, a.q, a.dk, a.dh_last, nullptr, R, nullptr, 1, V, 0, 0, 1, V, V, K, slices_of(K), 0, 1, a.scale, 1.0f};
+    const Walk dv{a.k, a.q, a.dout, a.dv, a.dh_last, a.dh0, R, nullptr, V, 1, V, 1, V, 1, K, V, slices_of(V), 0, 1, a.scale, 1.0f};
     W.count = 2;
     W.w[0] = dq;
     W.w[1] = dv;

@@ -1,0 +1,24 @@
+"""What the workspaces of the attention and beam-search entry points have room for, and
+refusals at the edges of their ranges.  No GPU."""
+from __future__ import annotations
+
+import pytest
+
+from selective_state_space_05_amd import _lib
+from test_abi import L, fake  # noqa: F401  (L is the library fixture)
+from test_abi_attention import attn_fwd
+
+
+@pytest.mark.parametrize("io", [0, 1])
+def test_workspace_holds_a_state_for_every_segment(L, io):
+    """256 steps of one head are two segments of 128.  Forward: a state in front of each,
+    the first one's for a call whose h0 is its h_last; backward: two in front of the second."""
+    dt, state = _lib.DTypes(io, 0), 2 * 3 * 16 * 24 * 4
+    dims = _lib.AttentionDims(2, 256, 512, 3, 16, 24)
+    assert L.mssm_linear_attention_workspace(dims, dt, 0) == 2 * state
+    assert L.mssm_linear_attention_workspace(dims, dt, 1) == 2 * state
+    at = fake(1 << 20) // 256 * 256
+    assert attn_fwd(L, io=io, seqlen=256, heads=3, key=16, value=24, workspace=at, bytes=state) == _lib.MSSM_ERR_INVALID_ARG
+    assert b"smaller" in L.mssm_last_error()
+    one = _lib.AttentionDims(2, 100, 200, 3, 16, 24)                # one segment
+    assert L.mssm_linear_attention_workspace(one, dt, 0) == 0

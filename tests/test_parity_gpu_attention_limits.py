@@ -1,0 +1,76 @@
+"""Linear attention, its norm and the beam search's operators at the edges of what
+their entry points allow.  Needs an MI355X; marked ``gpu``."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_parity_gpu_attention import IO, attention_inputs, dev, mssm, randn  # noqa: E402,F401  (fixtures among them)
+
+pytestmark = pytest.mark.gpu
+
+
+def announce(*what):
+    print("[attention limits]", *what, flush=True)
+
+
+# ---- states advanced in place ----------------------------------------------------------
+
+@pytest.mark.parametrize("shape", [(1, 3873, 20, 128, 128), (2, 700, 3, 40, 72), (3, 300, 1, 16, 24), (1, 2050, 2, 200, 130)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_states_in_place_over_several_segments(dev, mssm, shape, io):
+    """The workgroup that writes the final state is not the one that reads the initial one:
+    a state advanced in place is what a separate output holds, bit for bit."""
+    announce("in place", shape, io)
+    b, _, h, key, value = shape
+    x = attention_inputs(dev, shape, io)
+    h0 = randn(dev, b, h, key, value, seed=5, scale=3.0)
+    want, end = mssm.linear_attention_fwd(**x, h0=h0)
+    for _ in range(3):
+        state = h0.clone()
+        o, back = mssm.linear_attention_fwd(**x, h0=state, h_out=state)
+        assert back is state and torch.equal(o, want) and torch.equal(state, end)
+
+
+@pytest.mark.parametrize("longest", [None, 3959, 64])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_packed_states_in_place_over_several_segments(dev, mssm, io, longest):
+    """The same with more workgroups than the device holds at once, with sequences of no
+    step and of one among them."""
+    announce("packed in place", io, longest)
+    lengths = [1159, 684, 2298, 416, 0, 3959, 3723, 1, 1896, 2072, 2788]
+    cu = torch.tensor([0] + lengths, device=dev).cumsum(0)
+    total, n = sum(lengths), len(lengths)
+    x = attention_inputs(dev, (1, total, 8, 128, 128), io)
+    rows = (x["q"][0], x["k"][0], x["v"][0])
+    h0 = randn(dev, n, 8, 128, 128, seed=5, scale=3.0)
+    want, end = mssm.linear_attention_fwd(*rows, x["log_decay"], h0=h0, cu_seqlens=cu, max_seqlen=longest)
+    assert torch.equal(end[4], h0[4])
+    for _ in range(3):
+        state = h0.clone()
+        o, _ = mssm.linear_attention_fwd(*rows, x["log_decay"], h0=state, h_out=state, cu_seqlens=cu, max_seqlen=longest)
+        assert torch.equal(o, want) and torch.equal(state, end)
+
+
+def test_states_in_place_in_a_replayed_graph(dev, mssm):
+    """Every replay continues from where the one before it ended."""
+    announce("in place graph")
+    x = attention_inputs(dev, (2, 700, 2, 64, 64), "bf16")
+    h0 = randn(dev, 2, 2, 64, 64, seed=5)
+    state = h0.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mssm.linear_attention_fwd(**x, h0=state, h_out=state)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, _ = mssm.linear_attention_fwd(**x, h0=state, h_out=state)
+    state.copy_(h0)
+    want = h0
+    for turn in range(4):
+        graph.replay()
+        wo, want = mssm.linear_attention_fwd(**x, h0=want)
+        torch.cuda.synchronize()
+        assert torch.equal(o, wo) and torch.equal(state, want), turn
