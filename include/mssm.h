@@ -796,7 +796,10 @@ typedef struct {
  *
  *   value[j, v] = scores[j] + logits[j, v] - log sum_v exp(logits[j, v])
  *
- * in order, equal ones by the lowest j * vocab + v.  A beam whose score or
+ * in order: words of one beam by their logits, exactly, words of different beams
+ * by their values in float64, equal ones by the lowest j * vocab + v.  (With scores
+ * so large that float64 adds nothing to them, that is the first beam's best words.)
+ * A beam whose score or
  * log sum exp is not finite (a finished or empty beam, NaN or +infinity among
  * its logits, no finite logit) counts as -infinity for every word.
  *
@@ -804,8 +807,7 @@ typedef struct {
  *   scores   (batch, beams) float32                 required
  *   out_scores  (batch, count) float32              required (output): the values
  *   out_tokens, out_beams  (batch, count) int64     required (outputs): v and j
- * Values are compared in float64, logits exactly; the sum of the exponentials is
- * float32.  Errors: as for mssm_layer_norm_fwd; also MSSM_ERR_INVALID_ARG for
+ * The sum of the exponentials is float32.  Errors: as for mssm_layer_norm_fwd; also MSSM_ERR_INVALID_ARG for
  * beams, vocab or count < 1 or count > beams * vocab, MSSM_ERR_UNSUPPORTED for
  * beams > MSSM_MAX_BEAMS, count > MSSM_MAX_BEAM_COUNT, vocab >= 2^30, batch >= 2^24
  * or 2^24 or more pieces of 4096 words in all beams' vocabularies.  batch == 0:

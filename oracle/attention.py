@@ -118,10 +118,15 @@ def beam_values(logits, scores):
 
 
 def beam_select(logits, scores, count):
-    value = beam_values(logits, scores).flatten(1)
-    best, at = torch.sort(value, dim=1, descending=True, stable=True)
+    """By value, equal ones of one beam by logit, then by j * vocab + v."""
+    value = beam_values(logits, scores)
+    live = (value > float("-inf")).any(-1, keepdim=True)
     vocab = logits.shape[-1]
-    return best[:, :count], at[:, :count] % vocab, at[:, :count] // vocab
+    order = torch.where(live, f64(logits), torch.zeros_like(value)).sort(dim=-1, descending=True, stable=True).indices
+    at = (order + vocab * torch.arange(logits.shape[1], device=logits.device)[:, None]).flatten(1)
+    best, by_value = torch.sort(value.flatten(1).gather(1, at), dim=1, descending=True, stable=True)
+    at = at.gather(1, by_value)[:, :count]
+    return best[:, :count], at % vocab, at // vocab
 
 
 def state_reorder(state, origins):

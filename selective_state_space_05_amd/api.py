@@ -884,7 +884,8 @@ def linear_attention_update(state, q, k, v, log_decay, scale=1.0, out=None):
 def beam_select(logits, scores, count=None):
     """A beam search's selection over beams and vocabulary on the GPU: the
     ``count`` (None: as many as beams; at most 64) largest of scores[b, j] +
-    log_softmax(logits[b, j])[v] over j and v, equal ones by the lowest
+    log_softmax(logits[b, j])[v] over j and v: words of one beam by their
+    logits, exactly, words of different beams in float64, equal ones by the lowest
     j * vocab + v.
 
     logits: (batch, beams, vocab) float32 or bfloat16, up to 32 beams; scores:

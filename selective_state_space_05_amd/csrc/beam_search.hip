@@ -6,8 +6,10 @@
 // logits, so a first launch reads the logits once: every workgroup leaves, for a
 // piece of a beam's words, their maximum, sum of exponentials and at most 64 words
 // among which its `count` largest are.  A second launch joins a beam's pieces, forms
-// the values in float64, where a sum with the score merges no two logits, and ranks
-// the beams' words together.
+// the values in float64, and ranks the beams' words together.  A large score, or an lse
+// beside tiny logits, can merge values of different logits in float64 too: words of one
+// beam whose values are equal rank by their logits, so that the words left out before
+// are never among the best.
 //
 // What can be left out is found by bisection: t is the largest number that `count` of
 // the lanes' maxima reach, and a wave counts them with one comparison and one scalar
@@ -268,11 +270,20 @@ struct __attribute__((aligned(16))) Candidate {
     uint64_t place;     // beam and word
 };
 
+// Which of two words of equal value comes first: the lower beam's, the larger logit's, the
+// lower word.  `order` is the logit's.
+__device__ __forceinline__ bool before(uint64_t place, uint32_t order, uint64_t other, uint32_t other_order) {
+    const uint32_t beam = static_cast<uint32_t>(place >> 32), other_beam = static_cast<uint32_t>(other >> 32);
+    if (beam != other_beam) return beam < other_beam;
+    return order != other_order ? order > other_order : place < other;
+}
+
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     const Piece *__restrict__ in, const float *__restrict__ scores, float *__restrict__ out_scores,
     int64_t *__restrict__ out_tokens, int64_t *__restrict__ out_beams, int beams, int vocab, int count, int pieces) {
     __shared__ uint64_t lists[kMergeWaves * kList];
     __shared__ Candidate all[MSSM_MAX_BEAMS * kKeep];
+    __shared__ uint32_t orders[MSSM_MAX_BEAMS * kKeep];     // of the candidates' logits; 0 in a beam without values
     __shared__ int total;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int64_t entry = blockIdx.x;
@@ -314,6 +325,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             const int word = live ? word_of(key) : lane;
             all[at + lane] = Candidate{live ? score + (unordered(static_cast<uint32_t>(key >> 32)) - lse) : kLow,
                                        static_cast<uint64_t>(j) << 32 | static_cast<uint32_t>(word)};
+            orders[at + lane] = static_cast<uint32_t>(key >> 32);
         }
     }
     __syncthreads();
@@ -330,24 +342,37 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         __syncthreads();
         constexpr int kEach = MSSM_MAX_BEAMS * kKeep / kMergeThreads;
         Candidate c[kEach];
+        uint32_t order[kEach];
 #pragma unroll
         for (int r = 0; r < kEach; ++r)
-            if (r * kMergeThreads + static_cast<int>(threadIdx.x) < n) c[r] = all[r * kMergeThreads + threadIdx.x];
+            if (r * kMergeThreads + static_cast<int>(threadIdx.x) < n) {
+                c[r] = all[r * kMergeThreads + threadIdx.x];
+                order[r] = orders[r * kMergeThreads + threadIdx.x];
+            }
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < kEach; ++r)
-            if (r * kMergeThreads + static_cast<int>(threadIdx.x) < n && ordered(c[r].value) >= t) all[atomicAdd(&total, 1)] = c[r];
+            if (r * kMergeThreads + static_cast<int>(threadIdx.x) < n && ordered(c[r].value) >= t) {
+                const int to = atomicAdd(&total, 1);
+                all[to] = c[r];
+                orders[to] = order[r];
+            }
         __syncthreads();
     }
     const int left = total;
     for (int i = threadIdx.x; i < left; i += kMergeThreads) {
         const Candidate mine = all[i];
-        int rank = 0;
+        const uint32_t order = orders[i];
+        int rank = 0, same = 0;
 #pragma unroll 8
         for (int k = 0; k < left; ++k) {
-            const Candidate c = all[k];
-            rank += (c.value > mine.value) | ((c.value == mine.value) & (c.place < mine.place));
+            const double value = all[k].value;
+            rank += value > mine.value;
+            same += value == mine.value;
         }
+        if (same > 1)
+            for (int k = 0; k < left; ++k)
+                rank += all[k].value == mine.value && before(all[k].place, orders[k], mine.place, order);
         if (rank < count) {
             out_scores[entry * count + rank] = static_cast<float>(mine.value);
             out_tokens[entry * count + rank] = static_cast<uint32_t>(mine.place);

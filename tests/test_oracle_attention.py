@@ -128,3 +128,13 @@ def test_state_reorder():
     s = torch.arange(12).view(2, 3, 2)
     got = A.state_reorder(s, torch.tensor([[2, 0, 0], [1, 5, -1]]))
     assert got.tolist() == [[[4, 5], [0, 1], [0, 1]], [[8, 9], [8, 9], [10, 11]]]
+
+
+def test_beam_select_orders_merged_values_by_their_logits():
+    """Values that float64 cannot tell apart: by beam, then by logit, then by word."""
+    logits = torch.tensor([[[1.0, 3.0, 2.0, 3.0], [9.0, 8.0, 7.0, 10.0]]])
+    best, tokens, beams = A.beam_select(logits, torch.tensor([[-1e30, -1e30]]), 6)
+    assert tokens[0].tolist() == [1, 3, 2, 0, 3, 0] and beams[0].tolist() == [0, 0, 0, 0, 1, 1]
+    assert (best == torch.tensor(-1e30).double()).all()
+    tokens = A.beam_select(logits, torch.tensor([[float("-inf")] * 2]), 6)[1]
+    assert tokens[0].tolist() == [0, 1, 2, 3, 0, 1]

@@ -6,7 +6,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_parity_gpu_attention import IO, attention_inputs, dev, mssm, randn  # noqa: E402,F401  (fixtures among them)
+from oracle import attention as A  # noqa: E402
+from test_parity_gpu_attention import IO, NINF, U32, attention_inputs, dev, mssm, randn  # noqa: E402,F401  (fixtures among them)
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,31 @@ def test_states_in_place_in_a_replayed_graph(dev, mssm):
         wo, want = mssm.linear_attention_fwd(**x, h0=want)
         torch.cuda.synchronize()
         assert torch.equal(o, wo) and torch.equal(state, want), turn
+
+
+# ---- beams whose values merge -----------------------------------------------------------
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("beams,vocab,count", [(1, 300, 5), (3, 5000, 16), (2, 12345, 64), (32, 4097, 64), (4, 9, 30)])
+def test_beam_select_values_that_float64_merges(dev, mssm, io, beams, vocab, count):
+    """Mask scores that swallow every logit, and logits that vanish beside lse: words of a
+    beam still rank by their logits, and none of the best is left out on the way."""
+    announce("merged values", io, beams, vocab, count)
+    scores = torch.tensor([-1e30, torch.finfo(torch.float32).min, 3e38, 0.0, -1e15, -1e30, 0.0], device=dev)[:, None].repeat(1, beams)
+    # 2^42 apart where float64 holds multiples of 1/8 .. 1 and lse is off by 1e-6 at most
+    scores[4] -= torch.arange(beams, device=dev) * 2.0 ** 42
+    scores[5, 1:] = NINF
+    logits = randn(dev, len(scores), beams, vocab, seed=beams, dtype=IO[io], scale=3.0)
+    logits[3] *= 2.0 ** -70
+    logits[3, 1:] = NINF                                   # lse beside which the logits vanish, once
+    logits[6] = logits[6] * 2.0 ** -80
+    logits[6] = logits[6, :1]                              # and in beams that are alike
+    logits[0, 0, vocab // 2:] = -4.0                       # equal logits among them
+    best, tokens, origins = mssm.beam_select(logits, scores, count)
+    want, wt, wb = A.beam_select(logits, scores, count)
+    assert torch.equal(origins, wb) and torch.equal(tokens, wt)
+    live = want.isfinite()
+    assert torch.equal(best.isfinite(), live)
+    err = (best.double() - want).abs()[live]
+    # lse to 1e-5 (sums of up to 12345 exponentials), the score's rounding and the output's
+    assert (err <= 1e-5 + 2 * want[live].abs() * U32).all()
