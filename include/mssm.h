@@ -807,11 +807,11 @@ typedef struct {
  *   scores   (batch, beams) float32                 required
  *   out_scores  (batch, count) float32              required (output): the values
  *   out_tokens, out_beams  (batch, count) int64     required (outputs): v and j
- * The sum of the exponentials is float32.  Errors: as for mssm_layer_norm_fwd; also MSSM_ERR_INVALID_ARG for
- * beams, vocab or count < 1 or count > beams * vocab, MSSM_ERR_UNSUPPORTED for
- * beams > MSSM_MAX_BEAMS, count > MSSM_MAX_BEAM_COUNT, vocab >= 2^30, batch >= 2^24
- * or 2^24 or more pieces of 4096 words in all beams' vocabularies.  batch == 0:
- * nothing to do, MSSM_OK.
+ * The sum of the exponentials is float32.  Errors: as for mssm_layer_norm_fwd; also
+ * MSSM_ERR_INVALID_ARG for beams, vocab or count < 1 or count > beams * vocab,
+ * MSSM_ERR_UNSUPPORTED for beams > MSSM_MAX_BEAMS, count > MSSM_MAX_BEAM_COUNT,
+ * vocab >= 2^30, batch >= 2^23 or 2^24 or more pieces of 4096 words in all beams'
+ * vocabularies.  batch == 0: nothing to do, MSSM_OK.
  */
 MSSM_API mssm_status mssm_beam_select(const void *logits, const float *scores,
                                 float *out_scores, int64_t *out_tokens,

@@ -539,6 +539,8 @@ mssm_status check_selection(mssm_beam_dims d, mssm_dtypes dtypes) {
                     (long long)d.vocab, (long long)d.count, MSSM_MAX_BEAM_COUNT);
     if (d.count > d.beams * d.vocab)
         return fail(MSSM_ERR_INVALID_ARG, "count %lld exceeds beams * vocab", (long long)d.count);
+    if (d.batch >= (int64_t(1) << 23))    // its second launch has 512 threads an entry, below 2^32 in all
+        return fail(MSSM_ERR_UNSUPPORTED, "batch %lld reaches 2^23", (long long)d.batch);
     if (d.batch * d.beams * mssm::beam_select_pieces(d.vocab) >= (int64_t(1) << 24))
         return fail(MSSM_ERR_UNSUPPORTED, "batch %lld times beams %lld of %lld words is too large", (long long)d.batch,
                     (long long)d.beams, (long long)d.vocab);

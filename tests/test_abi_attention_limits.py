@@ -6,7 +6,7 @@ import pytest
 
 from selective_state_space_05_amd import _lib
 from test_abi import L, fake  # noqa: F401  (L is the library fixture)
-from test_abi_attention import attn_fwd
+from test_abi_attention import attn_fwd, beam, reorder
 
 
 @pytest.mark.parametrize("io", [0, 1])
@@ -22,3 +22,15 @@ def test_workspace_holds_a_state_for_every_segment(L, io):
     assert b"smaller" in L.mssm_last_error()
     one = _lib.AttentionDims(2, 100, 200, 3, 16, 24)                # one segment
     assert L.mssm_linear_attention_workspace(one, dt, 0) == 0
+
+
+def test_selection_refuses_more_entries_than_its_second_launch_takes(L):
+    """That launch has 512 threads an entry, and a launch is below 2^32 threads."""
+    dt = _lib.DTypes(0, 0)
+    assert L.mssm_beam_select_workspace(_lib.BeamDims((1 << 23) - 1, 1, 64, 4), dt) > 0
+    for batch in (1 << 23, (1 << 24) - 1):
+        assert beam(L, batch=batch, beams=1, vocab=64) == _lib.MSSM_ERR_UNSUPPORTED and b"batch" in L.mssm_last_error()
+        assert L.mssm_beam_select_workspace(_lib.BeamDims(batch, 1, 64, 4), dt) == -1
+    # the reordering's launch has 256 threads an entry and state
+    assert reorder(L, batch=1 << 24, rows=[16, 16]) == _lib.MSSM_ERR_UNSUPPORTED
+    assert reorder(L, batch=1 << 23, rows=[4097, 16]) == _lib.MSSM_ERR_UNSUPPORTED

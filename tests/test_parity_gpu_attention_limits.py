@@ -103,3 +103,18 @@ def test_beam_select_values_that_float64_merges(dev, mssm, io, beams, vocab, cou
     err = (best.double() - want).abs()[live]
     # lse to 1e-5 (sums of up to 12345 exponentials), the score's rounding and the output's
     assert (err <= 1e-5 + 2 * want[live].abs() * U32).all()
+
+
+def test_beam_select_of_the_most_entries(dev, mssm):
+    """One entry more is refused: 2^23 - 1 entries of one beam and three words."""
+    announce("most entries")
+    batch = (1 << 23) - 1
+    g = torch.Generator(device=dev).manual_seed(1)
+    logits = torch.randn(batch, 1, 3, generator=g, device=dev)
+    best, tokens, origins = mssm.beam_select(logits, torch.zeros(batch, 1, device=dev), 2)
+    want, at = logits[:, 0].double().log_softmax(-1).sort(dim=-1, descending=True, stable=True)
+    assert torch.equal(tokens, at[:, :2]) and not origins.any()
+    # float32 sums of three exponentials and the output's rounding of values up to 20
+    assert (best.double() - want[:, :2]).abs().max() <= 40 * U32
+    with pytest.raises(mssm.MssmError, match="2\\^23"):
+        mssm.beam_select(torch.empty(1 << 23, 1, 1, device=dev), torch.zeros(1 << 23, 1, device=dev))
