@@ -717,11 +717,12 @@ typedef struct {
  *   h_last     (seqs, heads, key, value) float32    nullable (output)
  * A sequence of no steps has h_last = h0.  Sequences are walked in chunks whose
  * products run on the matrix cores: float32 sums of exact products of bfloat16
- * values; inside a chunk the decayed products q.k, and the state as it meets q,
- * enter as bfloat16 where `io` is bfloat16 (float32 otherwise), while the state
- * itself is carried in float32.  Results are repeatable bit for bit.  A v that is
- * infinite or NaN makes its own column NaN from its step on in o, and not finite in the state;
- * a q or k that is not finite reaches what the formula says it does.
+ * values; where `io` is bfloat16 what is not (the decayed products q.k of a chunk,
+ * the state as it meets q, the decayed v) enters as the sum of two or three of them,
+ * 2^-18 off or less, so that results are off by their own storage.  The state itself is
+ * carried in float32.  Results are repeatable bit for bit.  A v that is infinite or NaN
+ * makes its own column NaN from its step on in o, and not finite in the state; a q or k
+ * that is not finite reaches what the formula says it does, as infinities or NaN.
  * Errors as for mssm_selective_scan_fwd; also MSSM_ERR_INVALID_ARG for a scale
  * that is not finite, key or value < 1, or total != seqs * seqlen without
  * cu_seqlens; MSSM_ERR_UNSUPPORTED for key or value > MSSM_MAX_HEAD_DIM,

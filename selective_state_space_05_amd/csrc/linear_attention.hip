@@ -29,8 +29,8 @@
 //
 // Bound by memory and the chunk's chain of products about equally: at 2 x 8448 x 20 x 128
 // in bfloat16 the third launch takes 85 us, its loads and stores alone 81 us, without loads
-// 70 us.  Whole calls: 2 x 4096 x 20 x 128 forward 96 us, backward 193 us, 131072 steps of
-// 4 heads 231 us; 7 packed sequences of 5 heads, 80 and 72 wide, in float32 backward 137 us;
+// 70 us.  Whole calls: 2 x 4096 x 20 x 128 forward 97 us, backward 213 us, 131072 steps of
+// 4 heads 243 us; 7 packed sequences of 5 heads, 80 and 72 wide, in float32 backward 137 us;
 // one step of 64 sequences 27 us (6.2 TB/s over the states), of one 4 us on the device.
 #include <algorithm>
 #include <type_traits>
@@ -84,14 +84,42 @@ __device__ __forceinline__ void pack(F8 &f, const float *v) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f.f[j] = v[j];
 }
-template <typename F>
-__device__ __forceinline__ F from_acc(const f32x16 &c, int s) {
+// v less f, exactly where f is v's rounding: a product of two with (-1, 0) or (0, -1) takes
+// one instruction a value, where taking f apart takes a second.  The factors are held in
+// registers: written into the instruction as constants they are read as float32 ones.
+__device__ __forceinline__ void take(float (&v)[8], const bf16x8 &f) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    uint32_t first = 0x0000bf80u, second = 0xbf800000u;
+    asm("" : "+s"(first), "+s"(second));
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const bf16x2 two = {f[j], f[j + 1]};
+        v[j] = __builtin_amdgcn_fdot2_f32_bf16(two, __builtin_bit_cast(bf16x2, first), v[j], false);
+        v[j + 1] = __builtin_amdgcn_fdot2_f32_bf16(two, __builtin_bit_cast(bf16x2, second), v[j + 1], false);
+    }
+}
+__device__ __forceinline__ void take(float (&)[8], const F8 &) {}
+
+// Eight values as the sum of N fragments, each the rounding of what those before left;
+// `each` sees a fragment before the next is formed.
+template <typename F, int N, typename G>
+__device__ __forceinline__ void split(F (&part)[N], const float *v, G each) {
+    float left[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) left[j] = v[j];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        pack(part[i], left);
+        each(part[i]);
+        if (i + 1 < N) take(left, part[i]);
+    }
+}
+template <typename F, int N, typename G>
+__device__ __forceinline__ void from_acc(F (&part)[N], const f32x16 &c, int s, G each) {
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c[8 * s + j];
-    F f;
-    pack(f, v);
-    return f;
+    split(part, v, each);
 }
 
 // Which of a fragment's contraction values {0..3, 8..11} are `last` or less, and what
@@ -516,12 +544,7 @@ __device__ __forceinline__ void advance(f32x16 (&X)[KB], const unsigned char *Ks
         Frag part[kParts];
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = weight[8 * s + j] * get(vf[s], j);
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-            pack(part[i], u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] -= get(part[i], j);
-        }
+        split(part, u, [](Frag &) {});
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             const int i = s * KB + kb;
@@ -693,12 +716,18 @@ __global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_walk_ker
         f32x16 G, O;
 #pragma unroll
         for (int j = 0; j < 16; ++j) G[j] = O[j] = 0.0f;
-        // The state enters as an operand of the I/O dtype: in bfloat16 half a step, 2^-8 of
-        // each of its values, like the rounding of the output.
+        // The state, and below the decayed products, enter as matrix operands: in bfloat16 as
+        // the sum of two roundings, 2^-18 off, which an output stored in bfloat16 hides (one
+        // alone moves outputs from 0.0017 to 0.0023 off in the root mean square; 2 x 4096 x 20 x
+        // 128 backward 194 us with one, 213 us with two).
+        constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
+            Frag xf[kTerms];
+            from_acc(xf, X[s / 2], s % 2, [](Frag &) {});
             mma(G, kf[s % kAhead], qf[s % kAhead]);
-            mma(O, from_acc<Frag>(X[s / 2], s % 2), qf[s % kAhead]);
+#pragma unroll
+            for (int i = 0; i < kTerms; ++i) mma(O, xf[i], qf[s % kAhead]);
             if (s + kAhead < KS) load(s + kAhead);
             in_order();
         }
@@ -709,9 +738,15 @@ __global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_walk_ker
             G[j] *= inside[j];
         }
         // later inputs leave nothing, whatever their products hold
-        Frag pf[2] = {from_acc<Frag>(G, 0), from_acc<Frag>(G, 1)};
+        Frag pf[2][kTerms];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) keep(pf[s], earlier[s]);
+        for (int s = 0; s < 2; ++s) from_acc(pf[s], G, s, [&](Frag &f) { keep(f, earlier[s]); });
+        auto add_inputs = [&] {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < kTerms; ++i) mma(O, vf[s], pf[s][i]);
+        };
         auto put = [&](const f32x16 &r) {
             float out[16];
 #pragma unroll
@@ -729,14 +764,12 @@ __global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_walk_ker
         // is set to NaN from their step on.
         const bool odd = any_odd(vf[0], vf[1]);
         if (!__any(odd)) {
-            mma(O, vf[0], pf[0]);
-            mma(O, vf[1], pf[1]);
+            add_inputs();
             put(O);
         } else {
             int reached = clean(vf[0], 4 * half, clean(vf[1], 16 + 4 * half, C));
             reached = min(reached, __shfl_xor(reached, 32));
-            mma(O, vf[0], pf[0]);
-            mma(O, vf[1], pf[1]);
+            add_inputs();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 if (col >= __shfl(reached, acc_row(j) + 4 * half)) O[j] = __builtin_nanf("");

@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import attention as A  # noqa: E402
-from test_parity_gpu_attention import IO, NINF, U32, attention_inputs, dev, mssm, randn  # noqa: E402,F401  (fixtures among them)
+from test_parity_gpu_attention import IO, NINF, U16, U32, attention_inputs, dev, mssm, randn, rms  # noqa: E402,F401  (fixtures among them)
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +118,40 @@ def test_beam_select_of_the_most_entries(dev, mssm):
     assert (best.double() - want[:, :2]).abs().max() <= 40 * U32
     with pytest.raises(mssm.MssmError, match="2\\^23"):
         mssm.beam_select(torch.empty(1 << 23, 1, 1, device=dev), torch.zeros(1 << 23, 1, device=dev))
+
+
+# ---- how near the values are -----------------------------------------------------------
+
+# every number of key blocks and of waves, whole vectors and not, one segment and several
+NEAR_SHAPES = [(1, 900, 2, 128, 128), (2, 200, 2, 64, 40), (1, 430, 3, 72, 200), (1, 300, 2, 33, 57), (1, 200, 2, 96, 64),
+               (1, 260, 1, 192, 256), (1, 170, 2, 256, 192), (1, 1500, 1, 120, 130)]
+
+
+@pytest.mark.parametrize("shape", NEAR_SHAPES)
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_linear_attention_is_off_by_its_storage_alone(dev, mssm, shape, io):
+    """States and their gradients are float32 sums; what enters matrix products in bfloat16
+    is split so that outputs and gradients are off by their own rounding and no more.
+
+    In the root mean square of the relative error.  States: the three terms that a
+    float32 is split into leave 2^-27, so what is left are float32 roundings with random
+    signs: an exponential, its argument, a factor a chunk and a few hundred sums, 16 U32.
+    (Two terms leave the square of a bfloat16's storage, 2.7e-6, as the next test shows.)
+    Outputs: two terms leave 2^-18 at most.  A value c that is off by a of the exact w is
+    stored within |round(c) - c| of itself, whose root mean square is that of w to a, and
+    is off by a more: 2 a beside the storage of w."""
+    announce("near", shape, io)
+    b, _, h, key, value = shape
+    x = attention_inputs(dev, shape, io)
+    h0, dlast = randn(dev, b, h, key, value, seed=5, scale=3.0), randn(dev, b, h, key, value, seed=6)
+    do = randn(dev, *x["v"].shape, seed=9, dtype=IO[io])
+    scale = key ** -0.5
+    o, last = mssm.linear_attention_fwd(**x, scale=scale, h0=h0)
+    g = mssm.linear_attention_bwd(**x, do=do, scale=scale, h0=h0, dh_last=dlast)
+    wo, wl = A.linear_attention(**x, scale=scale, h0=h0)
+    wg = A.linear_attention_grad(**x, do=do, scale=scale, h0=h0, dh_last=dlast)
+    off = (2.0 ** -18 if io == "bf16" else 0.0) + 16 * U32
+    for what, got, want in [("o", o, wo)] + [(n, g[n], wg[n]) for n in ("dq", "dk", "dv")]:
+        assert rms(got, want) <= rms(want.to(got.dtype), want) + 2 * off, what
+    for what, got, want in (("h_last", last, wl), ("dh0", g["dh0"], wg["dh0"])):
+        assert rms(got, want) <= 16 * U32, what
