@@ -265,25 +265,20 @@ __device__ __forceinline__ uint64_t ordered(double v) {
     return b >> 63 ? ~b : b | uint64_t(1) << 63;
 }
 
+// Of two of equal value comes first that of the lower place: the lower beam, in it the
+// larger logit; then the lower word.
 struct __attribute__((aligned(16))) Candidate {
     double value;
-    uint64_t place;     // beam and word
+    uint64_t place;     // beam, and the inverted order of the logit
 };
 
-// Which of two words of equal value comes first: the lower beam's, the larger logit's, the
-// lower word.  `order` is the logit's.
-__device__ __forceinline__ bool before(uint64_t place, uint32_t order, uint64_t other, uint32_t other_order) {
-    const uint32_t beam = static_cast<uint32_t>(place >> 32), other_beam = static_cast<uint32_t>(other >> 32);
-    if (beam != other_beam) return beam < other_beam;
-    return order != other_order ? order > other_order : place < other;
-}
 
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     const Piece *__restrict__ in, const float *__restrict__ scores, float *__restrict__ out_scores,
     int64_t *__restrict__ out_tokens, int64_t *__restrict__ out_beams, int beams, int vocab, int count, int pieces) {
     __shared__ uint64_t lists[kMergeWaves * kList];
     __shared__ Candidate all[MSSM_MAX_BEAMS * kKeep];
-    __shared__ uint32_t orders[MSSM_MAX_BEAMS * kKeep];     // of the candidates' logits; 0 in a beam without values
+    __shared__ int words[MSSM_MAX_BEAMS * kKeep];
     __shared__ int total;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int64_t entry = blockIdx.x;
@@ -324,8 +319,8 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             const uint64_t key = live ? list[lane] : 0;
             const int word = live ? word_of(key) : lane;
             all[at + lane] = Candidate{live ? score + (unordered(static_cast<uint32_t>(key >> 32)) - lse) : kLow,
-                                       static_cast<uint64_t>(j) << 32 | static_cast<uint32_t>(word)};
-            orders[at + lane] = static_cast<uint32_t>(key >> 32);
+                                       static_cast<uint64_t>(j) << 32 | ~static_cast<uint32_t>(key >> 32)};
+            words[at + lane] = word;
         }
     }
     __syncthreads();
@@ -342,12 +337,12 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         __syncthreads();
         constexpr int kEach = MSSM_MAX_BEAMS * kKeep / kMergeThreads;
         Candidate c[kEach];
-        uint32_t order[kEach];
+        int word[kEach];
 #pragma unroll
         for (int r = 0; r < kEach; ++r)
             if (r * kMergeThreads + static_cast<int>(threadIdx.x) < n) {
                 c[r] = all[r * kMergeThreads + threadIdx.x];
-                order[r] = orders[r * kMergeThreads + threadIdx.x];
+                word[r] = words[r * kMergeThreads + threadIdx.x];
             }
         __syncthreads();
 #pragma unroll
@@ -355,14 +350,14 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             if (r * kMergeThreads + static_cast<int>(threadIdx.x) < n && ordered(c[r].value) >= t) {
                 const int to = atomicAdd(&total, 1);
                 all[to] = c[r];
-                orders[to] = order[r];
+                words[to] = word[r];
             }
         __syncthreads();
     }
     const int left = total;
     for (int i = threadIdx.x; i < left; i += kMergeThreads) {
         const Candidate mine = all[i];
-        const uint32_t order = orders[i];
+        const int word = words[i];
         int rank = 0, same = 0;
 #pragma unroll 8
         for (int k = 0; k < left; ++k) {
@@ -370,12 +365,16 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             rank += value > mine.value;
             same += value == mine.value;
         }
-        if (same > 1)
-            for (int k = 0; k < left; ++k)
-                rank += all[k].value == mine.value && before(all[k].place, orders[k], mine.place, order);
+        if (same > 1) {
+#pragma unroll 8
+            for (int k = 0; k < left; ++k) {
+                const Candidate c = all[k];
+                rank += (c.value == mine.value) & ((c.place < mine.place) | ((c.place == mine.place) & (words[k] < word)));
+            }
+        }
         if (rank < count) {
             out_scores[entry * count + rank] = static_cast<float>(mine.value);
-            out_tokens[entry * count + rank] = static_cast<uint32_t>(mine.place);
+            out_tokens[entry * count + rank] = word;
             out_beams[entry * count + rank] = static_cast<int64_t>(mine.place >> 32);
         }
     }
