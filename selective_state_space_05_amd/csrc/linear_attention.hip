@@ -342,11 +342,15 @@ struct Rows {
     __device__ __forceinline__ void seek(int64_t t) {
         next = reinterpret_cast<unsigned char *>(p + t * ld) - static_cast<int64_t>(C - 1) * back;
     }
-    // Offset of a value of a row of a chunk; in a chunk of n rows less missing(n).
+    // Offset of a value of a row of a chunk; in a chunk of n rows less missing(n), which
+    // leaves one outside outside: unsigned, it stays past the buffer's 2^30 bytes or fewer.
     __device__ __forceinline__ int offset(int row, int value) const {
         return value >= width ? INT32_MIN : (back ? C - 1 - row : row) * bytes + value * static_cast<int>(sizeof(T));
     }
     __device__ __forceinline__ int missing(int n) const { return (C - n) * back; }
+    static __device__ __forceinline__ int less(int offset, int missing) {
+        return static_cast<int>(static_cast<uint32_t>(offset) - static_cast<uint32_t>(missing));
+    }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(int n) const {
         return __builtin_amdgcn_make_buffer_rsrc(next + missing(n), 0, (n - 1) * bytes + width * static_cast<int>(sizeof(T)),
                                                  0x00020000);
@@ -386,7 +390,7 @@ struct Feed {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (Lds *)(tile + (i * S::WAVES + wave) * 1024), 16,
-                                                         off[i] - R.missing(n), 0, 0, 0);
+                                                         R.less(off[i], R.missing(n)), 0, 0, 0);
         }
         R.next += R.step;
 #endif
@@ -448,7 +452,7 @@ __device__ __forceinline__ void store_vectors(__amdgpu_buffer_rsrc_t to, const i
         v[1][j] = b;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) __builtin_amdgcn_raw_buffer_store_b128(v[i], to, off[i] - missing, 0, 0);
+    for (int i = 0; i < 2; ++i) __builtin_amdgcn_raw_buffer_store_b128(v[i], to, Rows<uint16_t>::less(off[i], missing), 0, 0);
 }
 // In float32 a lane's eight columns are two vectors, and rows may end between them.
 __device__ __forceinline__ void store_vectors(__amdgpu_buffer_rsrc_t to, const int (&off)[4], int missing, const float *f, float) {
@@ -463,7 +467,7 @@ __device__ __forceinline__ void store_vectors(__amdgpu_buffer_rsrc_t to, const i
     for (int i = 0; i < 4; ++i)
         __builtin_amdgcn_raw_buffer_store_b128(
             u32x4{v[i / 2][4 * (i % 2)], v[i / 2][4 * (i % 2) + 1], v[i / 2][4 * (i % 2) + 2], v[i / 2][4 * (i % 2) + 3]}, to,
-            off[i] - missing, 0, 0);
+            Rows<float>::less(off[i], missing), 0, 0);
 }
 // The same without whole vectors: eight columns side by side of which `left` exist.
 __device__ __forceinline__ void store8(uint16_t *p, const float *f, int left) {
