@@ -312,11 +312,12 @@ struct Shape {
     // registers for two waves a SIMD, but for the largest states
     static constexpr int kWavesASimd = KB <= 2 || (KB <= 4 && sizeof(T) == 2) ? 2 : 1;
     // Bytes of a chunk's tiles in LDS, and how many chunks: loads of whole vectors go
-    // straight to LDS, up to three chunks ahead where there is room for two workgroups.
+    // straight to LDS, up to three chunks ahead where there is room for two workgroups.  The
+    // largest tiles, 80 KB, leave room for two chunks of one.
     static constexpr int tiles(bool out) { return (out ? 2 : 1) * Keys::kBytes + Values::kBytes; }
     static constexpr int stages(bool out) {
         const int fit = 160 * 1024 / kWavesASimd / tiles(out), most = VEC ? 4 : 2;
-        return fit < 1 ? 1 : fit < most ? fit : most;
+        return fit < most ? fit : most;
     }
     static constexpr int loads(bool out) { return tiles(out) / 1024 / WAVES; }   // of a wave and chunk
     static constexpr int stores = C * 32 * sizeof(T) / 1024;
@@ -566,6 +567,7 @@ __global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_walk_ker
     typedef typename S::Frag Frag;
     constexpr int KB = S::KB, KS = 2 * KB;
     constexpr int kStages = S::stages(true), kTiles = S::tiles(true), kLoads = S::loads(true);
+    static_assert(kStages >= 2, "a stage is filled while another is read");
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
 
     const Place at(W);
@@ -679,19 +681,12 @@ __global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_walk_ker
             // What is under way behind this chunk's loads may stay so: those of the next
             // chunks and the outputs sent after them.  Then every wave has read the stage
             // that the next loads go to.
-            if constexpr (kStages == 1) {
-                wait_and_meet<0>();
-                send(c, 0);
-                wait_and_meet<0>();
-            } else {
-                constexpr int kAhead = kStages - 2;
-                if (kAhead == 0 || c + kAhead >= count) wait_and_meet<0>();
-                else if (c < kAhead) wait_and_meet<kAhead * kLoads>();
-                else wait_and_meet<kAhead * (kLoads + S::stores)>();
-                if (c + kStages - 1 < count) send(c + kStages - 1, to_fill);
-            }
+            constexpr int kAhead = kStages - 2;
+            if (kAhead == 0 || c + kAhead >= count) wait_and_meet<0>();
+            else if (c < kAhead) wait_and_meet<kAhead * kLoads>();
+            else wait_and_meet<kAhead * (kLoads + S::stores)>();
+            if (c + kStages - 1 < count) send(c + kStages - 1, to_fill);
         } else {
-            if (kStages == 1) __syncthreads();
             kin.store(Ks);
             vin.store(Vs);
             qin.store(Qs);
@@ -800,6 +795,7 @@ __global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_state_ke
     typedef typename S::Type T;
     typedef typename S::Frag Frag;
     constexpr int KB = S::KB, kStages = S::stages(false), kTiles = S::tiles(false), kLoads = S::loads(false);
+    static_assert(kStages >= 2, "a stage is filled while another is read");
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
 
     const Place at(W);
@@ -851,17 +847,10 @@ __global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_state_ke
     for (int c = 0; c < count; ++c) {
         unsigned char *const Ks = smem + stage * kTiles, *const Vs = Ks + S::Keys::kBytes;
         if constexpr (S::VEC) {
-            if constexpr (kStages == 1) {
-                wait_and_meet<0>();
-                send(0);
-                wait_and_meet<0>();
-            } else {
-                if (kStages == 2 || c + kStages - 2 >= count) wait_and_meet<0>();
-                else wait_and_meet<(kStages - 2) * kLoads>();
-                if (c + kStages - 1 < count) send(to_fill);
-            }
+            if (kStages == 2 || c + kStages - 2 >= count) wait_and_meet<0>();
+            else wait_and_meet<(kStages - 2) * kLoads>();
+            if (c + kStages - 1 < count) send(to_fill);
         } else {
-            if (kStages == 1) __syncthreads();
             kin.store(Ks);
             vin.store(Vs);
             __syncthreads();
