@@ -646,8 +646,8 @@ typedef struct {
  * Errors: MSSM_ERR_INVALID_ARG for a null required pointer, a negative size,
  * dim < 1, a rotary that is odd or outside [0, dim], an unknown dtype, a bad
  * base or eps, or an output overlapping an input or another output;
- * MSSM_ERR_UNSUPPORTED for param dtype != F32, dim > MSSM_MAX_HEAD_DIM or
- * tokens * heads >= 2^31.  No elements: nothing to do, MSSM_OK.
+ * MSSM_ERR_UNSUPPORTED for param dtype != F32, dim > MSSM_MAX_HEAD_DIM,
+ * heads >= 2^23, tokens >= 2^31 or tokens * heads >= 2^31.  No elements: nothing to do, MSSM_OK.
  */
 MSSM_API mssm_status mssm_qk_norm_rotary_fwd(const void *q, const void *k,
                                 const int64_t *positions,
@@ -726,7 +726,8 @@ typedef struct {
  * Errors as for mssm_selective_scan_fwd; also MSSM_ERR_INVALID_ARG for a scale
  * that is not finite, key or value < 1, or total != seqs * seqlen without
  * cu_seqlens; MSSM_ERR_UNSUPPORTED for key or value > MSSM_MAX_HEAD_DIM,
- * heads >= 2^15, seqs * heads >= 2^20 or total >= 2^31.  seqs == 0 or heads == 0: o is zeroed.
+ * heads >= 2^15, seqs or seqs * heads >= 2^20, total or seqlen >= 2^31.  seqs == 0 or
+ * heads == 0: o is zeroed.
  */
 MSSM_API mssm_status mssm_linear_attention_fwd(const void *q, const void *k,
                                 const void *v, const float *log_decay,

@@ -1183,7 +1183,13 @@ mssm_status mssm_linear_attention_fwd(const void *q, const void *k, const void *
         if (e != hipSuccess) return hip_fail(e, "zero-fill of o");
         return MSSM_OK;
     }
-    if (dims.total == 0) return copy_or_zero_state("h_last", h_last, "h0", h0, z.states, st);
+    if (dims.total == 0) {
+        const Range ins[] = {range("log_decay", log_decay, dims.heads * 4), range("h0", h0, z.state_bytes),
+                             range("cu_seqlens", cu_seqlens, (dims.seqs + 1) * 8)};
+        const Range outs[] = {range("h_last", h_last, z.state_bytes)};
+        if (mssm_status c = check_overlaps(ins, 3, outs, 1, h0, h_last)) return c;
+        return copy_or_zero_state("h_last", h_last, "h0", h0, z.states, st);
+    }
     if (!q) return fail(MSSM_ERR_INVALID_ARG, "q is null");
     if (!k) return fail(MSSM_ERR_INVALID_ARG, "k is null");
     if (!v) return fail(MSSM_ERR_INVALID_ARG, "v is null");
@@ -1229,7 +1235,9 @@ mssm_status mssm_linear_attention_bwd(const void *q, const void *k, const void *
         return MSSM_OK;
     }
     if (dims.total == 0) {
-        if (dh0 && dh0 == dh_last) return fail(MSSM_ERR_INVALID_ARG, "output dh0 overlaps input dh_last");
+        const Range ins[] = {range("log_decay", log_decay, dims.heads * 4), range("h0", h0, z.state_bytes),
+                             range("cu_seqlens", cu_seqlens, (dims.seqs + 1) * 8), range("dh_last", dh_last, z.state_bytes)};
+        if (mssm_status c = check_overlaps(ins, 4, &outs[3], 1, nullptr, nullptr)) return c;
         return copy_or_zero_state("dh0", dh0, "dh_last", dh_last, z.states, st);
     }
     if (!q) return fail(MSSM_ERR_INVALID_ARG, "q is null");

@@ -6,7 +6,7 @@ import pytest
 
 from selective_state_space_05_amd import _lib
 from test_abi import L, fake  # noqa: F401  (L is the library fixture)
-from test_abi_attention import attn_fwd, beam, reorder
+from test_abi_attention import attn_bwd, attn_fwd, beam, norm_fwd, reorder
 
 
 @pytest.mark.parametrize("io", [0, 1])
@@ -34,3 +34,23 @@ def test_selection_refuses_more_entries_than_its_second_launch_takes(L):
     # the reordering's launch has 256 threads an entry and state
     assert reorder(L, batch=1 << 24, rows=[16, 16]) == _lib.MSSM_ERR_UNSUPPORTED
     assert reorder(L, batch=1 << 23, rows=[4097, 16]) == _lib.MSSM_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_overlaps_are_refused_without_steps_too(L, packed):
+    """What an empty sequence copies or clears may not lie on an input either."""
+    at = fake(900)
+    sizes = dict(seqlen=0, cu_seqlens=fake(950) if packed else None)
+    for f, out, inputs in ((attn_fwd, "h_last", ["log_decay", "h0"]), (attn_bwd, "dh0", ["log_decay", "h0", "dh_last"])):
+        for name in inputs + ["cu_seqlens"] * packed:
+            assert f(L, **{**sizes, out: at + 4, name: at}) == _lib.MSSM_ERR_INVALID_ARG, (out, name)
+            assert b"overlap" in L.mssm_last_error()
+    assert attn_bwd(L, **sizes, dh0=at, dh_last=at) == _lib.MSSM_ERR_INVALID_ARG
+    assert attn_bwd(L, **sizes, dh0=at, h0=at) == _lib.MSSM_ERR_INVALID_ARG
+    assert attn_fwd(L, **sizes, h0=at, h_last=at) == _lib.MSSM_OK          # already there
+
+
+def test_norm_refuses_what_its_indices_do_not_hold(L):
+    for sizes in (dict(tokens=1, q_heads=1 << 23), dict(tokens=1, k_heads=1 << 23), dict(tokens=1 << 31, q_heads=0, k_heads=0),
+                  dict(tokens=1 << 20, q_heads=1 << 11)):
+        assert norm_fwd(L, **sizes) == _lib.MSSM_ERR_UNSUPPORTED, sizes
