@@ -127,6 +127,20 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
+// 1 / sqrt(mean(x^2) + eps) of a head, whose sum of squares is `ss`.  Where float32 cannot
+// hold that sum (values from 1e18 on, or with no eps to speak of below 1e-15), of values
+// that a power of two brings into its range.
+template <int G, int N>
+__device__ __forceinline__ float rstd_of(float ss, const float (&x)[N], float dim, float eps) {
+    const float m = ss / dim + eps;
+    if (m > 0x1p-90f && m < 0x1p120f) return 1.0f / sqrtf(m);
+    const float by = m > 1.0f ? 0x1p-70f : 0x1p70f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum = fmaf(x[i] * by, x[i] * by, sum);
+    return by / sqrtf(group_sum<G>(sum) / dim + eps * by * by);
+}
+
 // G lanes a head, SLOTS slots a lane.
 template <typename T, int VEC, int G, int SLOTS, bool BWD>
 __global__ __launch_bounds__(kThreads, 4) void head_norm_kernel(const HeadNorm N) {
@@ -200,7 +214,7 @@ __global__ __launch_bounds__(kThreads, 4) void head_norm_kernel(const HeadNorm N
             // the group's next head, of this tile or of the next one
             const int64_t next = id + GROUPS < count * heads ? row + GROUPS : (t0 + count) * heads + group;
             if (next < end * heads) load(next);
-            const float r = 1.0f / sqrtf(group_sum<G>(ss) / N.dim + N.eps);
+            const float r = rstd_of<G>(group_sum<G>(ss), reinterpret_cast<const float(&)[SLOTS * 2 * VEC]>(xf), N.dim, N.eps);
             const float2 *const my = turn + id / heads * half;
             float ex = 0.0f;
 #pragma unroll

@@ -7,7 +7,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import attention as A  # noqa: E402
-from test_parity_gpu_attention import IO, NINF, U16, U32, attention_inputs, dev, mssm, randn, rms  # noqa: E402,F401  (fixtures among them)
+from test_parity_gpu_attention import (D_TURN, IO, NINF, U32, attention_inputs, dev, half_step, mssm,  # noqa: E402,F401
+                                       pair_size, randn, rms, within)   # (fixtures among them)
 
 pytestmark = pytest.mark.gpu
 
@@ -155,3 +156,40 @@ def test_linear_attention_is_off_by_its_storage_alone(dev, mssm, shape, io):
         assert rms(got, want) <= rms(want.to(got.dtype), want) + 2 * off, what
     for what, got, want in (("h_last", last, wl), ("dh0", g["dh0"], wg["dh0"])):
         assert rms(got, want) <= 16 * U32, what
+
+
+# ---- norms of very large and very small values -----------------------------------------
+
+@pytest.mark.parametrize("scale,eps", [(2.0 ** 100, 1e-6), (2.0 ** 66, 1e-6), (2.0 ** 60, 0.0), (2.0 ** -44, 0.0), (2.0 ** -50, 0.0),
+                                       (2.0 ** -80, 0.0), (2.0 ** -80, 2.0 ** -160), (2.0 ** -100, 0.0), (2.0 ** -100, 1e-6)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,rotary", [(128, 128), (256, 64), (24, 8), (7, 4)])
+def test_qk_norm_rotary_beyond_the_range_of_squares(dev, mssm, scale, eps, io, dim, rotary):
+    """Heads whose sum of squares float32 cannot hold, beside ordinary ones, forward and
+    backward; bounds as for ordinary ones, since a power of two costs nothing."""
+    announce("norm range", scale, eps, io, dim, rotary)
+    pos = torch.arange(9, device=dev)
+    x = randn(dev, 9, 3, dim, seed=1)
+    x[:, 0] *= scale
+    x[4:, 2] *= scale
+    x = x.to(IO[io])
+    w = randn(dev, dim, seed=2, shift=1.0, scale=0.3)
+    dy = randn(dev, 9, 3, dim, seed=3, dtype=IO[io])
+    got = mssm.qk_norm_rotary_fwd(x, x.clone(), pos, w, None, eps=eps, rotary_dim=rotary)
+    g = mssm.qk_norm_rotary_bwd(dy, dy.clone(), x, x.clone(), pos, w, None, eps=eps, rotary_dim=rotary)
+    eps = float(torch.tensor(eps, dtype=torch.float32))
+    X = x.double()
+    r = (X.square().mean(-1, keepdim=True) + eps).rsqrt()
+    for y, n, wt in ((got[0], "q", w), (got[1], "k", None)):
+        want = A.head_norm_rotary(x, pos, wt, 1e4, eps, rotary)
+        bound = pair_size(A.head_norm_rotary(x, pos, wt, 1e4, eps, 0), rotary) * ((dim / 2 + 12) * U32 + D_TURN)
+        within(y, want, bound + half_step(want, y) * 1.01, n)
+        want = A.head_norm_rotary_grad(dy, x, pos, wt, 1e4, eps, rotary)
+        dn = pair_size(dy.double(), rotary)
+        e = dn if wt is None else dn * wt.double().abs()
+        rel_n, rel_r = D_TURN + 4 * U32, (dim / 2 + 6) * U32
+        c = r.square() * (e * X.abs()).mean(-1, keepdim=True)
+        bound = r * (e * (rel_n + rel_r + 4 * U32) + X.abs() * c * (rel_n + 3 * rel_r + (dim + 10) * U32))
+        within(g["d" + n], want["dx"], bound + half_step(want["dx"], g["d" + n]) * 1.01, "d" + n)
+        size = (dn * X.abs() * r).flatten(0, -2).sum(0)
+        within(g["d%s_weight" % n], want["dweight"], size * (rel_n + rel_r + 40 * U32) + 1e-30, n + " weight")
