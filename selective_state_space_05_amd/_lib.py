@@ -38,6 +38,7 @@ NOALLOC_SCRATCH_BYTES = 8 << 20  # scratch array of the no-alloc entry point
 CONV_WIDTH = 4
 SSD_MAX_DSTATE = 256
 SSD_MAX_HEADDIM = 256
+MAX_BEAM_COUNT = 64
 
 # Every symbol the header declares.
 EXPORTED = (

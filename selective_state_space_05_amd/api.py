@@ -905,7 +905,8 @@ def beam_select(logits, scores, count=None):
     batch, beams, vocab = logits.shape
     n = beams if count is None else int(count)
     dims, dt = _lib.BeamDims(batch, beams, vocab, n), _lib.DTypes(io, _lib.MSSM_F32)
-    best = torch.empty((batch, max(n, 0)), dtype=torch.float32, device=dev)
+    # a count that the call refuses allocates no more than the largest that it takes
+    best = torch.empty((batch, min(max(n, 0), _lib.MAX_BEAM_COUNT)), dtype=torch.float32, device=dev)
     tokens = torch.empty(best.shape, dtype=torch.int64, device=dev)
     origins = torch.empty_like(tokens)
     with _on_device(dev):

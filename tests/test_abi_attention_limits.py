@@ -54,3 +54,10 @@ def test_norm_refuses_what_its_indices_do_not_hold(L):
     for sizes in (dict(tokens=1, q_heads=1 << 23), dict(tokens=1, k_heads=1 << 23), dict(tokens=1 << 31, q_heads=0, k_heads=0),
                   dict(tokens=1 << 20, q_heads=1 << 11)):
         assert norm_fwd(L, **sizes) == _lib.MSSM_ERR_UNSUPPORTED, sizes
+
+
+def test_binding_and_header_agree_on_the_most_candidates():
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "mssm.h")).read()
+    assert int(re.search(r"#define MSSM_MAX_BEAM_COUNT (\d+)", src).group(1)) == _lib.MAX_BEAM_COUNT

@@ -193,3 +193,11 @@ def test_qk_norm_rotary_beyond_the_range_of_squares(dev, mssm, scale, eps, io, d
         within(g["d" + n], want["dx"], bound + half_step(want["dx"], g["d" + n]) * 1.01, "d" + n)
         size = (dn * X.abs() * r).flatten(0, -2).sum(0)
         within(g["d%s_weight" % n], want["dweight"], size * (rel_n + rel_r + 40 * U32) + 1e-30, n + " weight")
+
+
+def test_beam_select_refuses_a_huge_count_without_allocating_for_it(dev, mssm):
+    announce("huge count")
+    logits, scores = randn(dev, 2, 3, 50), randn(dev, 2, 3)
+    for count in (10 ** 13, 65, 151, 0, -1, -10 ** 13):
+        with pytest.raises(mssm.MssmError, match="count"):
+            mssm.beam_select(logits, scores, count)
