@@ -27,11 +27,13 @@
 // a contraction being free.  Every wave has 32 columns of values with their part of the
 // state, and forms q.k again for itself: shared through LDS it would cost a barrier a chunk.
 //
-// Bound by memory and the chunk's chain of products about equally: at 2 x 8448 x 20 x 128
-// in bfloat16 the third launch takes 85 us, its loads and stores alone 81 us, without loads
-// 70 us.  Whole calls: 2 x 4096 x 20 x 128 forward 97 us, backward 213 us, 131072 steps of
-// 4 heads 243 us; 7 packed sequences of 5 heads, 80 and 72 wide, in float32 backward 137 us;
-// one step of 64 sequences 27 us (6.2 TB/s over the states), of one 4 us on the device.
+// Bound by memory and the chunk's chain of products about equally forward, by the chain
+// backward: ten more products a chunk, to 52, took the third launch of 2 x 4096 x 20 x 128 in
+// bfloat16 from 59 to 62 us forward and from 150 to 182 us backward.  Whole calls in bfloat16:
+// 2 x 4096 x 20 x 128 forward 97 us, backward 214 us, 131072 steps of 4 heads 243 us; float32:
+// the same layer 266 and 820 us, 7 packed sequences of 5 heads, 80 and 72 wide, backward 137 us.
+// One step of 64 sequences 36 us from memory (4.7 TB/s over the states), 27 us where the
+// device's 256 MB cache holds part of them; of one sequence 4 us on the device.
 #include <algorithm>
 #include <type_traits>
 
@@ -526,8 +528,9 @@ __device__ __forceinline__ int state_row(int kb, int j, int half) { return 32 * 
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // X <- g X + (keys)^T (weights * values): the keys exact, their partners in bfloat16 as the
-// sum of three roundings, which hold a float32: with two the state is off by 4e-6, with
-// three by what float32 sums are, 3e-7 (2 x 4096 x 20 x 128 forward 90 us and 96 us).
+// sum of three roundings, which hold a float32: with two the state is off by 2.7e-6 in the
+// root mean square, with three by what float32 sums are, 2e-7 (2 x 4096 x 20 x 128 forward
+// 90 us and 96 us).
 template <typename S, typename Frag, int KB>
 __device__ __forceinline__ void advance(f32x16 (&X)[KB], const unsigned char *Ks, const Frag (&vf)[2], const float *weight,
                                         float g, int lane) {
@@ -718,7 +721,7 @@ __global__ __launch_bounds__(S::threads, S::kWavesASimd) void attention_walk_ker
         // The state, and below the decayed products, enter as matrix operands: in bfloat16 as
         // the sum of two roundings, 2^-18 off, which an output stored in bfloat16 hides (one
         // alone moves outputs from 0.0017 to 0.0023 off in the root mean square; 2 x 4096 x 20 x
-        // 128 backward 194 us with one, 213 us with two).
+        // 128 backward 194 us with one, 214 us with two).
         constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -915,11 +918,12 @@ int slices_of(int64_t B) { return static_cast<int>((B + 32 * waves_of(B) - 1) / 
 int blocks_of(int64_t A) { return A <= 64 ? 2 : A <= 96 ? 3 : A <= 128 ? 4 : A <= 192 ? 6 : 8; }
 
 // Segments of a sequence and their steps: so many that the device's 256 compute units have
-// a forward workgroup each; backward, where three walks share a launch, half as many.  More
-// of them cost more in states, each written once, folded and read again, than two
-// workgroups a unit gain (taken with two terms of the state, where the rest of the walk is
-// the same): 2 x 4096 x 20 x 128 in bfloat16 87 us with 6 segments and 91 us
-// with 12, backward 168 us with 3 and 169 us with 6, 131072 steps of 4 heads 200 and 211 us.
+// a forward workgroup each; backward, where three walks share a launch, half as many.  Twice
+// as many fill units that hold two workgroups, but cost more in states, each written once,
+// folded and read again, and end in rounds that are part empty: 2 x 4096 x 20 x 128 in bfloat16
+// 98 and, with twice as many, 97 us, backward 214 and 201 us, 131072 steps of 4 heads 251 and
+// 240 us, but 8 x 2048 x 16 x 128 backward 233 and 280 us, 4096 steps of 16 heads of 256 148 and
+// 187 us, 8 packed sequences of 16 heads of 128 106 and 116 us, backward 200 and 224 us.
 // Sequences of different lengths are cut by what all rows together give a workgroup, the
 // longest into at most four times what it would be cut into otherwise (7 sequences of 431
 // steps in the mean, backward in float32 131 us, cut as if all were as long 154 us).
@@ -1036,8 +1040,9 @@ int64_t floats_of(const AttentionArgs &a, const Walks &W) {
 // A workgroup holds 32 columns of one state, VEC of them a lane; groups of lanes take the
 // rows in turn.  Bound by the state's bytes, or by one workgroup's loads where states are
 // few.  Whole lines of 128 columns give a workgroup four times the loads in turn and gain
-// nothing back: 20, 320, 640 and 1280 states of 128 x 128 take 3.7, 11.4, 20.0 and 35.5 us,
-// with 128 columns 6.4, 14.5, 19.5 and 35.6 us.
+// nothing back: 20, 320, 640 and 1280 states of 128 x 128 take the kernel 5.5, 11.7, 19.9 and
+// 35.7 us, with 128 columns 10.4, 15.3, 20.4 and 35.7 us (over 1 GB of states in turn, which
+// the device's cache does not hold).
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void attention_step_kernel(float *__restrict__ state, const T *__restrict__ q,
                                                              const T *__restrict__ k, const T *__restrict__ v,
