@@ -201,3 +201,20 @@ def test_beam_select_refuses_a_huge_count_without_allocating_for_it(dev, mssm):
     for count in (10 ** 13, 65, 151, 0, -1, -10 ** 13):
         with pytest.raises(mssm.MssmError, match="count"):
             mssm.beam_select(logits, scores, count)
+
+
+@pytest.mark.parametrize("positions", [1 << 6, 1 << 12, 1 << 20])
+@pytest.mark.parametrize("rotary", [2, 64, 256])
+def test_qk_norm_rotary_turns_to_a_step_of_float32(dev, mssm, positions, rotary):
+    """Heads of ones and zeros whose norm is exactly 1 show the cosines and sines
+    themselves: the functions are good to a step (U32 from 1/2 on), the turn by what the
+    fraction's rounding left adds half of one; angles are float64."""
+    announce("turns", positions, rotary)
+    g = torch.Generator().manual_seed(positions + rotary)
+    pos = torch.randint(0, positions, (4000,), generator=g).to(dev)
+    x = torch.zeros(4000, 1, rotary, device=dev)
+    x[..., :rotary // 2] = 1.0
+    y = mssm.qk_norm_rotary_fwd(x, x.clone(), pos, eps=0.5)[0]
+    a = A.angles(pos, rotary, 1e4)
+    want = torch.cat([a.cos(), a.sin()], -1)[:, None]
+    within(y, want, torch.full_like(want, 1.5 * U32 + 2.0 ** -30), "turn")
