@@ -19,7 +19,8 @@
 // Measured in bfloat16 at 8192 tokens of 20 + 20 heads of 128: forward 31 us (5.4 TB/s),
 // backward 49 us (5.1 TB/s) and 4.6 us for the weights' sums; 8 tokens 4 us.  Widths or
 // rotated parts that are no multiple of two vectors go element by element: 8192 tokens of
-// 20 + 20 heads of 120 in whole calls 82 us in bfloat16 (1.9 TB/s), 58 us in float32.
+// 20 + 20 heads of 120 in whole calls 82 us in bfloat16 (1.9 TB/s), 58 us in float32, where
+// they are whole vectors (5.4 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -132,8 +133,8 @@ __device__ __forceinline__ float group_sum(float x) {
 }
 
 // 1 / sqrt(mean(x^2) + eps) of a head, whose sum of squares is `ss`.  Where float32 cannot
-// hold that sum (values from 1e18 on, or with no eps to speak of below 1e-15), of values
-// that a power of two brings into its range.
+// hold that sum (values from 1e18 on, or with no eps to speak of below 3e-14, where squares
+// near the least normal number), of values that a power of two brings into its range.
 template <int G, int N>
 __device__ __forceinline__ float rstd_of(float ss, const float (&x)[N], float dim, float eps) {
     const float m = ss / dim + eps;
