@@ -30,7 +30,7 @@
 // Bound by memory and the chunk's chain of products about equally forward, by the chain
 // backward: ten more products a chunk, to 52, took the third launch of 2 x 4096 x 20 x 128 in
 // bfloat16 from 59 to 62 us forward and from 150 to 182 us backward.  Whole calls in bfloat16:
-// 2 x 4096 x 20 x 128 forward 97 us, backward 214 us, 131072 steps of 4 heads 243 us; float32:
+// 2 x 4096 x 20 x 128 forward 97 us, backward 214 us, 131072 steps of 4 heads 250 us; float32:
 // the same layer 266 and 820 us, 7 packed sequences of 5 heads, 80 and 72 wide, backward 137 us.
 // One step of 64 sequences 36 us from memory (4.7 TB/s over the states), 27 us where the
 // device's 256 MB cache holds part of them; of one sequence 4 us on the device.
